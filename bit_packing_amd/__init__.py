@@ -15,7 +15,14 @@ have the names of the C entry points:
   (in-place) layout of the PCIe transfer mode: each row keeps a slot of its raw
   size, only the used part is read, a bit vector marks compressed rows;
 * ``ibp_gather_raw`` -- the uncompressed zero-copy gather the codec is
-  measured against.
+  measured against;
+* ``ibp_embedding_lookup`` / ``ibp_embedding_grad`` -- embedding rows with scaling, and
+  their gradient by sorted tokens;
+* ``ibp_mx_pack`` / ``ibp_mx_unpack`` -- microscaled tensors (e4m3 or e2m1 elements, a
+  power-of-two scale per 32);
+* ``ibp_mx_swiglu`` / ``ibp_mx_swiglu_backward`` / ``ibp_mx_linear_wgrad`` -- 8-bit
+  activation checkpoints and the backward pass from them;
+* ``ibp_mx_matmul`` -- product of packed activations with packed 4-bit weights.
 
 There is no fallback: if ``libibp.so`` is missing or no GPU is present the calls
 raise.
@@ -38,6 +45,9 @@ IBP_OK, IBP_ERR_INVALID_ARG, IBP_ERR_SIZE, IBP_ERR_CAPACITY, IBP_ERR_DEVICE = 0,
 IBP_DEVERR_CORRUPT, IBP_DEVERR_BAD_ID, IBP_DEVERR_TIMEOUT = 1, 2, 4
 IBP_MAX_S = 1024
 IBP_NOALLOC_SCRATCH_BYTES = 8 << 20  # device array behind ibp_compress_noalloc, per GPU
+IBP_F32, IBP_F16, IBP_BF16 = 0, 1, 2
+IBP_MAX_COLS, IBP_MAX_TOKENS = 1 << 30, 1 << 31
+IBP_MX_E4M3, IBP_MX_E2M1 = 0, 1
 
 EXPORTS = (
     "ibp_status_str", "ibp_num_segments", "ibp_max_stream_bytes", "ibp_stream_bytes",
@@ -48,6 +58,10 @@ EXPORTS = (
     "ibp_zip_table_from_sigma", "ibp_zip_blocks", "ibp_zip_codes_bytes", "ibp_zip_workspace_bytes",
     "ibp_zip_compress", "ibp_zip_decompress", "ibp_set_wait_limit", "ibp_set_halves_min_chunks",
     "ibp_compress_noalloc",
+    "ibp_embedding_lookup", "ibp_embedding_grad", "ibp_embedding_grad_workspace_bytes",
+    "ibp_mx_codes_pitch", "ibp_mx_scales_pitch", "ibp_mx_pack", "ibp_mx_unpack", "ibp_mx_swiglu",
+    "ibp_mx_swiglu_backward", "ibp_mx_matmul", "ibp_mx_matmul_workspace_bytes", "ibp_mx_linear_wgrad",
+    "ibp_mx_linear_wgrad_workspace_bytes",
 )
 
 
@@ -65,6 +79,31 @@ class ibp_pos_meta_t(ctypes.Structure):
     chunk position i of every segment."""
     _fields_ = [("W", ctypes.c_uint32), ("S", ctypes.c_uint32),
                 ("mask", ctypes.c_void_p), ("bitval", ctypes.c_void_p)]
+
+
+class ibp_mx_t(ctypes.Structure):
+    """A packed microscaled tensor: element format, shape, device pointers."""
+    _fields_ = [("format", ctypes.c_uint32), ("reserved", ctypes.c_uint32), ("rows", ctypes.c_uint64),
+                ("cols", ctypes.c_uint64), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+@dataclass
+class MxTensor:
+    """A microscaled tensor of rows x cols elements: uint8 codes [rows, ibp_mx_codes_pitch]
+    and scale bytes [rows, ibp_mx_scales_pitch] on the device."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    rows: int
+    cols: int
+    format: int
+
+    def struct(self) -> ibp_mx_t:
+        # the C side sees pointers only: the tensors must hold what the shape says
+        blocks = -(-self.cols // 32)
+        if _nbytes(self.codes) < self.rows * blocks * (32 if self.format == IBP_MX_E4M3 else 16) or \
+                _nbytes(self.scales) < self.rows * (-(-blocks // 4) * 4):
+            raise ValueError("codes or scales are smaller than their shape needs")
+        return ibp_mx_t(self.format, 0, self.rows, self.cols, _ptr(self.codes), _ptr(self.scales))
 
 
 @dataclass
@@ -139,7 +178,27 @@ def load_library() -> ctypes.CDLL:
         lib.ibp_set_wait_limit.restype = _u32
         lib.ibp_set_halves_min_chunks.argtypes = [_u64]
         lib.ibp_set_halves_min_chunks.restype = _u64
-        for f in ("ibp_build_metadata", "ibp_compress", "ibp_decompress", "ibp_decompress_gather",
+        _flt, _mxp = ctypes.c_float, ctypes.POINTER(ibp_mx_t)
+        lib.ibp_embedding_lookup.argtypes = [_vp, _int, _u64, _u32, _vp, _u64, _flt, _vp, _int, _vp, _vp]
+        lib.ibp_embedding_grad.argtypes = [_vp, _int, _vp, _u64, _u64, _u32, _flt, ctypes.c_int64, _vp, _int, _vp,
+                                           _u64, _vp, _vp]
+        lib.ibp_embedding_grad_workspace_bytes.argtypes = [_u64, _u64, _u32]
+        lib.ibp_mx_codes_pitch.argtypes = [_u64, _u32]
+        lib.ibp_mx_scales_pitch.argtypes = [_u64]
+        lib.ibp_mx_pack.argtypes = [_vp, _int, _mxp, _vp]
+        lib.ibp_mx_unpack.argtypes = [_mxp, _vp, _int, _vp]
+        lib.ibp_mx_swiglu.argtypes = [_vp, _vp, _int, _vp, _mxp, _mxp, _vp]
+        lib.ibp_mx_swiglu_backward.argtypes = [_vp, _int, _mxp, _mxp, _vp, _vp, _vp]
+        lib.ibp_mx_matmul.argtypes = [_mxp, _mxp, _vp, _int, _vp, _u64, _vp]
+        lib.ibp_mx_matmul_workspace_bytes.argtypes = [_u64, _u64, _u64, _u32]
+        lib.ibp_mx_linear_wgrad.argtypes = [_vp, _int, _u64, _mxp, _vp, _int, _vp, _u64, _vp]
+        lib.ibp_mx_linear_wgrad_workspace_bytes.argtypes = [_u64, _u64, _u64]
+        for f in ("ibp_embedding_grad_workspace_bytes", "ibp_mx_codes_pitch", "ibp_mx_scales_pitch",
+                  "ibp_mx_matmul_workspace_bytes", "ibp_mx_linear_wgrad_workspace_bytes"):
+            getattr(lib, f).restype = _u64
+        for f in ("ibp_embedding_lookup", "ibp_embedding_grad", "ibp_mx_pack", "ibp_mx_unpack", "ibp_mx_swiglu",
+                  "ibp_mx_swiglu_backward", "ibp_mx_matmul", "ibp_mx_linear_wgrad",
+                  "ibp_build_metadata", "ibp_compress", "ibp_decompress", "ibp_decompress_gather",
                   "ibp_gather_raw", "ibp_compress_slots", "ibp_decompress_gather_slots",
                   "ibp_build_metadata_pos", "ibp_compress_pos", "ibp_decompress_pos", "ibp_zip_table_from_sigma",
                   "ibp_zip_compress", "ibp_zip_decompress"):
@@ -456,3 +515,194 @@ def ibp_zip_decompress(z: ZipCompressed, out: torch.Tensor | None = None, err: t
                                            _nbytes(z.esc), _ptr(z.eoff), z.n, _ptr(out), _ptr(err), _stream(stream))
     _check(rc, "ibp_zip_decompress")
     return out
+
+
+# ------------------------------------------------------------------ language-model operators
+
+_DTYPES = {torch.float32: IBP_F32, torch.float16: IBP_F16, torch.bfloat16: IBP_BF16}
+
+
+def _dtype(dtype) -> int:
+    if dtype not in _DTYPES:
+        raise ValueError(f"{dtype} is not one of float32, float16, bfloat16")
+    return _DTYPES[dtype]
+
+
+def _ids(ids: torch.Tensor) -> torch.Tensor:
+    if ids.dtype != torch.int64:
+        raise ValueError("ids are int64")
+    return ids
+
+
+def _matrix(x: torch.Tensor) -> tuple[int, int]:
+    """(rows, cols) of a tensor read as rows of its last dimension."""
+    if x.dim() == 0:
+        raise ValueError("a tensor of rows is needed")
+    cols = x.shape[-1]
+    return (x.numel() // cols if cols else 0), cols
+
+
+def _out(out: torch.Tensor | None, shape, dtype, device) -> torch.Tensor:
+    """A new tensor, or the caller's after a check of its shape and dtype."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(out.shape) != tuple(shape) or out.dtype != dtype:
+        raise ValueError(f"the output is {tuple(out.shape)} {out.dtype}, not {tuple(shape)} {dtype}")
+    return out
+
+
+def ibp_embedding_lookup(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, out_dtype=None,
+                         out: torch.Tensor | None = None, err: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor:
+    """scale * table[ids], of out_dtype (the table's by default); table [rows, dim] may be
+    pinned host memory.  Ids out of range give zero rows and set IBP_DEVERR_BAD_ID."""
+    if table.dim() != 2:
+        raise ValueError("a table is [rows, dim]")
+    rows, dim = table.shape
+    out = _out(out, (*_ids(ids).shape, dim), out_dtype or (table.dtype if out is None else out.dtype),
+               _device(ids, table))
+    rc = load_library().ibp_embedding_lookup(_ptr(table), _dtype(table.dtype), rows, dim, _ptr(ids), ids.numel(),
+                                             scale, _ptr(out), _dtype(out.dtype), _ptr(err), _stream(stream))
+    _check(rc, "ibp_embedding_lookup")
+    return out
+
+
+def ibp_embedding_grad(dout: torch.Tensor, ids: torch.Tensor, n_rows: int, scale: float = 1.0, padding_id: int = -1,
+                       grad_dtype=None, grad: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                       err: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Gradient [n_rows, dim] of ibp_embedding_lookup's table: scale times the sum of dout's
+    rows of each id, in 32 bits, of grad_dtype (dout's by default).  Tokens with padding_id
+    take no part."""
+    n, dim = _matrix(dout)
+    if _ids(ids).numel() * dim != dout.numel() or tuple(dout.shape[:-1]) != tuple(ids.shape):
+        raise ValueError("dout is [*ids.shape, dim]")
+    n = ids.numel()
+    dev = _device(dout, ids)
+    grad = _out(grad, (n_rows, dim), grad_dtype or (dout.dtype if grad is None else grad.dtype), dev)
+    lib = load_library()
+    if workspace is None:
+        workspace = torch.empty(max(int(lib.ibp_embedding_grad_workspace_bytes(n_rows, n, dim)), 16),
+                                dtype=torch.uint8, device=dev)
+    rc = lib.ibp_embedding_grad(_ptr(dout), _dtype(dout.dtype), _ptr(ids), n, n_rows, dim, scale, padding_id,
+                                _ptr(grad), _dtype(grad.dtype), _ptr(workspace), _nbytes(workspace), _ptr(err),
+                                _stream(stream))
+    _check(rc, "ibp_embedding_grad")
+    return grad
+
+
+def ibp_mx_codes_pitch(cols: int, format: int) -> int:
+    return int(load_library().ibp_mx_codes_pitch(cols, format))
+
+
+def ibp_mx_scales_pitch(cols: int) -> int:
+    return int(load_library().ibp_mx_scales_pitch(cols))
+
+
+def ibp_mx_matmul_workspace_bytes(m: int, n: int, k: int, a_format: int) -> int:
+    return int(load_library().ibp_mx_matmul_workspace_bytes(m, n, k, a_format))
+
+
+def ibp_mx_linear_wgrad_workspace_bytes(tokens: int, outs: int, ins: int) -> int:
+    return int(load_library().ibp_mx_linear_wgrad_workspace_bytes(tokens, outs, ins))
+
+
+def ibp_embedding_grad_workspace_bytes(n_rows: int, n_ids: int, dim: int) -> int:
+    return int(load_library().ibp_embedding_grad_workspace_bytes(n_rows, n_ids, dim))
+
+
+def make_mx(rows: int, cols: int, format: int, device) -> MxTensor:
+    """An MxTensor of unwritten codes and scales."""
+    return MxTensor(torch.empty((rows, ibp_mx_codes_pitch(cols, format)), dtype=torch.uint8, device=device),
+                    torch.empty((rows, ibp_mx_scales_pitch(cols)), dtype=torch.uint8, device=device),
+                    rows, cols, format)
+
+
+def _mx(m: MxTensor | None, rows: int, cols: int, format: int, device) -> MxTensor:
+    if m is None:
+        return make_mx(rows, cols, format, device)
+    if (m.rows, m.cols, m.format) != (rows, cols, format):
+        raise ValueError("the packed output has another shape or format")
+    return m
+
+
+def ibp_mx_pack(x: torch.Tensor, format: int, out: MxTensor | None = None, stream=None) -> MxTensor:
+    """Pack the rows (last dimension) of x into IBP_MX_E4M3 or IBP_MX_E2M1 blocks of 32."""
+    if format not in (IBP_MX_E4M3, IBP_MX_E2M1):
+        raise ValueError("a format is IBP_MX_E4M3 or IBP_MX_E2M1")
+    rows, cols = _matrix(x)
+    out = _mx(out, rows, cols, format, _device(x))
+    _check(load_library().ibp_mx_pack(_ptr(x), _dtype(x.dtype), ctypes.byref(out.struct()), _stream(stream)),
+           "ibp_mx_pack")
+    return out
+
+
+def ibp_mx_unpack(m: MxTensor, dtype=torch.bfloat16, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The values [rows, cols] of a packed tensor."""
+    out = _out(out, (m.rows, m.cols), dtype, _device(m.codes))
+    _check(load_library().ibp_mx_unpack(ctypes.byref(m.struct()), _ptr(out), _dtype(out.dtype), _stream(stream)),
+           "ibp_mx_unpack")
+    return out
+
+
+def ibp_mx_swiglu(gate: torch.Tensor, up: torch.Tensor, h: torch.Tensor | None = None,
+                  gate8: MxTensor | None = None, up8: MxTensor | None = None,
+                  stream=None) -> tuple[torch.Tensor, MxTensor, MxTensor]:
+    """(silu(gate) * up, and the e4m3 checkpoints of gate and up), in one pass."""
+    if gate.shape != up.shape or gate.dtype != up.dtype:
+        raise ValueError("gate and up differ in shape or dtype")
+    rows, cols = _matrix(gate)
+    dev = _device(gate)
+    h = _out(h, gate.shape, gate.dtype, dev)
+    gate8, up8 = _mx(gate8, rows, cols, IBP_MX_E4M3, dev), _mx(up8, rows, cols, IBP_MX_E4M3, dev)
+    rc = load_library().ibp_mx_swiglu(_ptr(gate), _ptr(up), _dtype(gate.dtype), _ptr(h),
+                                      ctypes.byref(gate8.struct()), ctypes.byref(up8.struct()), _stream(stream))
+    _check(rc, "ibp_mx_swiglu")
+    return h, gate8, up8
+
+
+def ibp_mx_swiglu_backward(dh: torch.Tensor, gate8: MxTensor, up8: MxTensor, dgate: torch.Tensor | None = None,
+                           dup: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """(dgate, dup) of ibp_mx_swiglu from its checkpoints."""
+    if _matrix(dh) != (gate8.rows, gate8.cols) and dh.numel():
+        raise ValueError("dh and the checkpoints differ in shape")
+    dev = _device(dh)
+    dgate, dup = _out(dgate, dh.shape, dh.dtype, dev), _out(dup, dh.shape, dh.dtype, dev)
+    rc = load_library().ibp_mx_swiglu_backward(_ptr(dh), _dtype(dh.dtype), ctypes.byref(gate8.struct()),
+                                               ctypes.byref(up8.struct()), _ptr(dgate), _ptr(dup), _stream(stream))
+    _check(rc, "ibp_mx_swiglu_backward")
+    return dgate, dup
+
+
+def _workspace(workspace: torch.Tensor | None, need: int, device) -> torch.Tensor | None:
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace
+
+
+def ibp_mx_matmul(a: MxTensor, b: MxTensor, dtype=torch.bfloat16, out: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """[a.rows, b.rows] product of packed a with packed 4-bit b, both along their columns."""
+    lib, dev = load_library(), _device(a.codes)
+    out = _out(out, (a.rows, b.rows), dtype, dev)
+    workspace = _workspace(workspace, int(lib.ibp_mx_matmul_workspace_bytes(a.rows, b.rows, a.cols, a.format)), dev)
+    rc = lib.ibp_mx_matmul(ctypes.byref(a.struct()), ctypes.byref(b.struct()), _ptr(out), _dtype(out.dtype),
+                           _ptr(workspace), 0 if workspace is None else _nbytes(workspace), _stream(stream))
+    _check(rc, "ibp_mx_matmul")
+    return out
+
+
+def ibp_mx_linear_wgrad(dy: torch.Tensor, x8: MxTensor, dw_dtype=None, dw: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """[outs, x8.cols] weight gradient: the sum over tokens of dy's row times x8's row; dy
+    [x8.rows, outs] in bfloat16, x8 in e4m3."""
+    if dy.dim() != 2 or dy.shape[0] != x8.rows:
+        raise ValueError("dy is [x8.rows, outs]")
+    lib, dev = load_library(), _device(dy)
+    outs = dy.shape[1]
+    dw = _out(dw, (outs, x8.cols), dw_dtype or (dy.dtype if dw is None else dw.dtype), dev)
+    workspace = _workspace(workspace, int(lib.ibp_mx_linear_wgrad_workspace_bytes(x8.rows, outs, x8.cols)), dev)
+    rc = lib.ibp_mx_linear_wgrad(_ptr(dy), _dtype(dy.dtype), outs, ctypes.byref(x8.struct()), _ptr(dw),
+                                 _dtype(dw.dtype), _ptr(workspace), 0 if workspace is None else _nbytes(workspace),
+                                 _stream(stream))
+    _check(rc, "ibp_mx_linear_wgrad")
+    return dw

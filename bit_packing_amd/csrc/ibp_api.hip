@@ -2,15 +2,17 @@
 //
 // Every argument is checked here, on the host, before any HIP call; then the
 // launch geometry and the workspace layout are derived and the kernels in
-// ibp_meta.hip, ibp_encode.hip, ibp_decode.hip and ibp_slots.hip are enqueued on the caller's stream.
+// the other files of this folder are enqueued on the caller's stream.
 #include <math.h>
 #include <string.h>
 
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 
 #include "ibp.h"
 #include "ibp_internal.h"
+#include "ibp_ops.h"
 
 namespace {
 
@@ -716,6 +718,274 @@ IBP_API int ibp_zip_decompress(const uint8_t *table, const uint8_t *d_sm, const 
   a.nblk = nblk;
   for (int k = 0; k < 7; ++k) a.table[k] = table[k];
   return status_of(launch_zip_decode(a, static_cast<hipStream_t>(hip_stream)));
+}
+
+// ------------------------------------------------------------------ language-model operators
+
+static uint64_t dtype_size(int dtype) { return dtype == IBP_F32 ? 4 : 2; }
+static bool dtype_ok(int dtype) { return dtype == IBP_F32 || dtype == IBP_F16 || dtype == IBP_BF16; }
+
+// Bytes of rows x cols elements; false when they do not fit 64 bits.
+static bool matrix_bytes(uint64_t rows, uint64_t cols, uint64_t size, uint64_t *out) {
+  return mul_ok(rows, cols, out) && mul_ok(*out, size, out);
+}
+
+IBP_API int ibp_embedding_lookup(const void *table, int table_dtype, uint64_t n_rows, uint32_t dim,
+                                 const int64_t *d_ids, uint64_t n_ids, float scale, void *d_out, int out_dtype,
+                                 uint32_t *d_err_word, void *hip_stream) {
+  if (!dtype_ok(table_dtype) || !dtype_ok(out_dtype)) return IBP_ERR_INVALID_ARG;
+  if (dim > IBP_MAX_COLS || (n_rows == 0 && n_ids > 0)) return IBP_ERR_SIZE;
+  uint64_t tb, ib, ob;
+  if (!matrix_bytes(n_rows, dim, dtype_size(table_dtype), &tb) || !mul_ok(n_ids, 8, &ib) ||
+      !matrix_bytes(n_ids, dim, dtype_size(out_dtype), &ob))
+    return IBP_ERR_SIZE;
+  if (n_ids == 0 || dim == 0) return IBP_OK;
+  if (!table || !d_ids || !d_out || !aligned(table, dtype_size(table_dtype)) || !aligned(d_ids, 8) ||
+      !aligned(d_out, dtype_size(out_dtype)) || !aligned(d_err_word, 4))
+    return IBP_ERR_INVALID_ARG;
+  if (!view(table, tb) || !view(d_ids, ib) || !view(d_out, ob) || !view(d_err_word, d_err_word ? 4 : 0))
+    return IBP_ERR_INVALID_ARG;
+  LookupArgs a;
+  a.table = table;
+  a.ids = d_ids;
+  a.out = d_out;
+  a.err = d_err_word;
+  a.n_rows = n_rows;
+  a.n_ids = n_ids;
+  a.dim = dim;
+  a.scale = scale;
+  a.in_dtype = table_dtype;
+  a.out_dtype = out_dtype;
+  return status_of(launch_lookup(a, static_cast<hipStream_t>(hip_stream)));
+}
+
+static bool grad_sizes_ok(uint64_t n_rows, uint64_t n_ids, uint32_t dim) {
+  return n_rows < 0xFFFFFFFFull && n_ids < IBP_MAX_TOKENS && dim <= IBP_MAX_COLS;
+}
+
+IBP_API uint64_t ibp_embedding_grad_workspace_bytes(uint64_t n_rows, uint64_t n_ids, uint32_t dim) {
+  return grad_sizes_ok(n_rows, n_ids, dim) ? embed_grad_workspace(n_rows, n_ids, dim) : 0;
+}
+
+IBP_API int ibp_embedding_grad(const void *d_dout, int dout_dtype, const int64_t *d_ids, uint64_t n_ids,
+                               uint64_t n_rows, uint32_t dim, float scale, int64_t padding_id, void *d_grad,
+                               int grad_dtype, void *d_workspace, uint64_t workspace_bytes, uint32_t *d_err_word,
+                               void *hip_stream) {
+  if (!dtype_ok(dout_dtype) || !dtype_ok(grad_dtype) || padding_id < -1) return IBP_ERR_INVALID_ARG;
+  if (!grad_sizes_ok(n_rows, n_ids, dim) || (n_rows == 0 && n_ids > 0)) return IBP_ERR_SIZE;
+  uint64_t db, gb;
+  if (!matrix_bytes(n_ids, dim, dtype_size(dout_dtype), &db) || !matrix_bytes(n_rows, dim, dtype_size(grad_dtype), &gb))
+    return IBP_ERR_SIZE;
+  if (n_rows == 0 || dim == 0) return IBP_OK;
+  const uint64_t wb = embed_grad_workspace(n_rows, n_ids, dim);
+  if (workspace_bytes < wb) return IBP_ERR_CAPACITY;
+  if (!d_grad || !d_workspace || (n_ids && (!d_dout || !d_ids))) return IBP_ERR_INVALID_ARG;
+  if (!aligned(d_dout, dtype_size(dout_dtype)) || !aligned(d_ids, 8) || !aligned(d_grad, dtype_size(grad_dtype)) ||
+      !aligned(d_workspace, 16) || !aligned(d_err_word, 4))
+    return IBP_ERR_INVALID_ARG;
+  if (!view(d_dout, db) || !view(d_ids, 8 * n_ids) || !view(d_grad, gb) || !view(d_workspace, wb) ||
+      !view(d_err_word, d_err_word ? 4 : 0))
+    return IBP_ERR_INVALID_ARG;
+  EmbedGradArgs a;
+  a.dout = d_dout;
+  a.ids = d_ids;
+  a.grad = d_grad;
+  a.err = d_err_word;
+  a.ws = static_cast<uint8_t *>(d_workspace);
+  a.n_rows = n_rows;
+  a.n_ids = n_ids;
+  a.padding_id = padding_id;
+  a.dim = dim;
+  a.scale = scale;
+  a.in_dtype = dout_dtype;
+  a.out_dtype = grad_dtype;
+  return status_of(launch_embed_grad(a, static_cast<hipStream_t>(hip_stream)));
+}
+
+IBP_API uint64_t ibp_mx_codes_pitch(uint64_t cols, uint32_t format) {
+  if (format > IBP_MX_E2M1 || cols > IBP_MAX_COLS) return 0;
+  return mx_code_pitch(cols, format == IBP_MX_E4M3);
+}
+
+IBP_API uint64_t ibp_mx_scales_pitch(uint64_t cols) { return cols > IBP_MAX_COLS ? 0 : mx_scale_pitch(cols); }
+
+// Field checks of a packed tensor, before any HIP call.
+static int mx_check(const ibp_mx_t *t) {
+  if (!t || t->format > IBP_MX_E2M1 || t->reserved) return IBP_ERR_INVALID_ARG;
+  uint64_t b;
+  if (t->cols > IBP_MAX_COLS || !mul_ok(t->rows, mx_code_pitch(t->cols, true), &b)) return IBP_ERR_SIZE;
+  if (!aligned(t->codes, 16) || !aligned(t->scales, 4)) return IBP_ERR_INVALID_ARG;
+  if (t->rows && t->cols && (!t->codes || !t->scales)) return IBP_ERR_INVALID_ARG;
+  return IBP_OK;
+}
+
+// The tensor's device pointers, checked against their allocations.
+static bool mx_view(const ibp_mx_t *t, uint8_t **codes, uint8_t **scales) {
+  *codes = t->codes;
+  *scales = t->scales;
+  return view(*codes, t->rows * mx_code_pitch(t->cols, t->format == IBP_MX_E4M3)) &&
+         view(*scales, t->rows * mx_scale_pitch(t->cols));
+}
+
+static void mx_fill(MxArgs *a, const ibp_mx_t *t, int dtype) {
+  memset(a, 0, sizeof(*a));
+  a->rows = t->rows;
+  a->cols = (uint32_t)t->cols;
+  a->e4m3 = t->format == IBP_MX_E4M3;
+  a->dtype = dtype;
+}
+
+IBP_API int ibp_mx_pack(const void *d_in, int dtype, const ibp_mx_t *out, void *hip_stream) {
+  if (!dtype_ok(dtype)) return IBP_ERR_INVALID_ARG;
+  if (const int rc = mx_check(out)) return rc;
+  uint64_t b;
+  if (!matrix_bytes(out->rows, out->cols, dtype_size(dtype), &b)) return IBP_ERR_SIZE;
+  if (b == 0) return IBP_OK;
+  if (!d_in || !aligned(d_in, dtype_size(dtype))) return IBP_ERR_INVALID_ARG;
+  MxArgs a;
+  mx_fill(&a, out, dtype);
+  if (!view(d_in, b) || !mx_view(out, &a.codes, &a.scales)) return IBP_ERR_INVALID_ARG;
+  a.in = d_in;
+  return status_of(launch_mx_pack(a, static_cast<hipStream_t>(hip_stream)));
+}
+
+IBP_API int ibp_mx_unpack(const ibp_mx_t *in, void *d_out, int dtype, void *hip_stream) {
+  if (!dtype_ok(dtype)) return IBP_ERR_INVALID_ARG;
+  if (const int rc = mx_check(in)) return rc;
+  uint64_t b;
+  if (!matrix_bytes(in->rows, in->cols, dtype_size(dtype), &b)) return IBP_ERR_SIZE;
+  if (b == 0) return IBP_OK;
+  if (!d_out || !aligned(d_out, dtype_size(dtype))) return IBP_ERR_INVALID_ARG;
+  MxArgs a;
+  mx_fill(&a, in, dtype);
+  if (!view(d_out, b) || !mx_view(in, &a.codes, &a.scales)) return IBP_ERR_INVALID_ARG;
+  a.out = d_out;
+  return status_of(launch_mx_unpack(a, static_cast<hipStream_t>(hip_stream)));
+}
+
+// Checks shared by the gated activation's two directions: two e4m3 checkpoints of one
+// shape, three plain tensors of it.
+static int gated_check(const void *x, const void *y, const void *z, int dtype, const ibp_mx_t *gate8,
+                       const ibp_mx_t *up8, uint64_t *bytes) {
+  if (!dtype_ok(dtype)) return IBP_ERR_INVALID_ARG;
+  if (const int rc = mx_check(gate8)) return rc;
+  if (const int rc = mx_check(up8)) return rc;
+  if (gate8->format != IBP_MX_E4M3 || up8->format != IBP_MX_E4M3) return IBP_ERR_INVALID_ARG;
+  if (gate8->rows != up8->rows || gate8->cols != up8->cols) return IBP_ERR_SIZE;
+  if (!matrix_bytes(gate8->rows, gate8->cols, dtype_size(dtype), bytes)) return IBP_ERR_SIZE;
+  if (*bytes == 0) return IBP_OK;
+  for (const void *p : {x, y, z})
+    if (!p || !aligned(p, dtype_size(dtype))) return IBP_ERR_INVALID_ARG;
+  return IBP_OK;
+}
+
+IBP_API int ibp_mx_swiglu(const void *d_gate, const void *d_up, int dtype, void *d_h, const ibp_mx_t *gate8,
+                          const ibp_mx_t *up8, void *hip_stream) {
+  uint64_t b = 0;
+  if (const int rc = gated_check(d_gate, d_up, d_h, dtype, gate8, up8, &b)) return rc;
+  if (b == 0) return IBP_OK;
+  MxArgs a;
+  mx_fill(&a, gate8, dtype);
+  if (!view(d_gate, b) || !view(d_up, b) || !view(d_h, b) || !mx_view(gate8, &a.codes, &a.scales) ||
+      !mx_view(up8, &a.codes2, &a.scales2))
+    return IBP_ERR_INVALID_ARG;
+  a.in = d_gate;
+  a.in2 = d_up;
+  a.out = d_h;
+  return status_of(launch_mx_swiglu(a, static_cast<hipStream_t>(hip_stream)));
+}
+
+IBP_API int ibp_mx_swiglu_backward(const void *d_dh, int dtype, const ibp_mx_t *gate8, const ibp_mx_t *up8,
+                                   void *d_dgate, void *d_dup, void *hip_stream) {
+  uint64_t b = 0;
+  if (const int rc = gated_check(d_dh, d_dgate, d_dup, dtype, gate8, up8, &b)) return rc;
+  if (b == 0) return IBP_OK;
+  MxArgs a;
+  mx_fill(&a, gate8, dtype);
+  if (!view(d_dh, b) || !view(d_dgate, b) || !view(d_dup, b) || !mx_view(gate8, &a.codes, &a.scales) ||
+      !mx_view(up8, &a.codes2, &a.scales2))
+    return IBP_ERR_INVALID_ARG;
+  a.in2 = d_dh;
+  a.out = d_dgate;
+  a.out2 = d_dup;
+  return status_of(launch_mx_swiglu_backward(a, static_cast<hipStream_t>(hip_stream)));
+}
+
+// Rows of a product: the launch grids and 32-bit row numbers hold up to 2^30.
+static bool product_rows_ok(uint64_t n) { return n <= IBP_MAX_COLS; }
+
+IBP_API uint64_t ibp_mx_matmul_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, uint32_t a_format) {
+  if (!product_rows_ok(m) || !product_rows_ok(n) || k > IBP_MAX_COLS || a_format > IBP_MX_E2M1) return 0;
+  return m && n ? mx_matmul_workspace(m, n, (uint32_t)k, a_format == IBP_MX_E4M3) : 0;
+}
+
+IBP_API uint64_t ibp_mx_linear_wgrad_workspace_bytes(uint64_t tokens, uint64_t outs, uint64_t ins) {
+  if (!product_rows_ok(outs) || ins > IBP_MAX_COLS) return 0;
+  return outs && ins ? mx_wgrad_workspace(tokens, (uint32_t)outs, (uint32_t)ins) : 0;
+}
+
+IBP_API int ibp_mx_matmul(const ibp_mx_t *a, const ibp_mx_t *b, void *d_y, int dtype, void *d_workspace,
+                          uint64_t workspace_bytes, void *hip_stream) {
+  if (!dtype_ok(dtype)) return IBP_ERR_INVALID_ARG;
+  if (const int rc = mx_check(a)) return rc;
+  if (const int rc = mx_check(b)) return rc;
+  if (b->format != IBP_MX_E2M1) return IBP_ERR_INVALID_ARG;
+  uint64_t yb;
+  if (a->cols != b->cols || !product_rows_ok(a->rows) || !product_rows_ok(b->rows) ||
+      !matrix_bytes(a->rows, b->rows, dtype_size(dtype), &yb))
+    return IBP_ERR_SIZE;
+  if (yb == 0) return IBP_OK;
+  const uint64_t wb = mx_matmul_workspace(a->rows, b->rows, (uint32_t)a->cols, a->format == IBP_MX_E4M3);
+  if (workspace_bytes < wb) return IBP_ERR_CAPACITY;
+  if (!d_y || !aligned(d_y, dtype_size(dtype)) || (wb && !d_workspace) || !aligned(d_workspace, 16))
+    return IBP_ERR_INVALID_ARG;
+  uint8_t *ac, *as, *bc, *bs;
+  if (!view(d_y, yb) || !mx_view(a, &ac, &as) || !mx_view(b, &bc, &bs) || !view(d_workspace, wb))
+    return IBP_ERR_INVALID_ARG;
+  MxMatmulArgs p;
+  p.a_codes = ac;
+  p.a_scales = as;
+  p.b_codes = bc;
+  p.b_scales = bs;
+  p.y = d_y;
+  p.ws = static_cast<float *>(d_workspace);
+  p.M = a->rows;
+  p.N = b->rows;
+  p.K = (uint32_t)a->cols;
+  p.a_e4m3 = a->format == IBP_MX_E4M3;
+  p.dtype = dtype;
+  return status_of(launch_mx_matmul(p, static_cast<hipStream_t>(hip_stream)));
+}
+
+IBP_API int ibp_mx_linear_wgrad(const void *d_dy, int dy_dtype, uint64_t outs, const ibp_mx_t *x8, void *d_dw,
+                                int dw_dtype, void *d_workspace, uint64_t workspace_bytes, void *hip_stream) {
+  if (dy_dtype != IBP_BF16 || !dtype_ok(dw_dtype)) return IBP_ERR_INVALID_ARG;
+  if (const int rc = mx_check(x8)) return rc;
+  if (x8->format != IBP_MX_E4M3) return IBP_ERR_INVALID_ARG;
+  uint64_t yb, wgb;
+  if (!product_rows_ok(outs) || !matrix_bytes(x8->rows, outs, 2, &yb) ||
+      !matrix_bytes(outs, x8->cols, dtype_size(dw_dtype), &wgb))
+    return IBP_ERR_SIZE;
+  if (wgb == 0) return IBP_OK;
+  const uint64_t wb = mx_wgrad_workspace(x8->rows, (uint32_t)outs, (uint32_t)x8->cols);
+  if (workspace_bytes < wb) return IBP_ERR_CAPACITY;
+  if (!d_dw || !aligned(d_dw, dtype_size(dw_dtype)) || (yb && !d_dy) || !aligned(d_dy, 2) || (wb && !d_workspace) ||
+      !aligned(d_workspace, 16))
+    return IBP_ERR_INVALID_ARG;
+  uint8_t *xc, *xs;
+  if (!view(d_dy, yb) || !mx_view(x8, &xc, &xs) || !view(d_dw, wgb) || !view(d_workspace, wb))
+    return IBP_ERR_INVALID_ARG;
+  MxWgradArgs p;
+  p.dy = d_dy;
+  p.x_codes = xc;
+  p.x_scales = xs;
+  p.dw = d_dw;
+  p.ws = static_cast<float *>(d_workspace);
+  p.T = x8->rows;
+  p.N = (uint32_t)outs;
+  p.K = (uint32_t)x8->cols;
+  p.dtype = dw_dtype;
+  return status_of(launch_mx_wgrad(p, static_cast<hipStream_t>(hip_stream)));
 }
 
 }  // extern "C"

@@ -336,6 +336,121 @@ IBP_API int ibp_zip_decompress(const uint8_t *table, const uint8_t *d_sm, const 
                                const uint8_t *d_esc, uint64_t esc_bytes, const uint64_t *d_eoff, uint64_t n,
                                void *d_out, uint32_t *d_err_word, void *hip_stream);
 
+/*
+ * Language-model operators: what is done with the tensors next to the codec.  An
+ * embedding table's lookup and gradient, and microscaled tensors: activation
+ * checkpoints in 8 bits with their use in the backward pass, and 4-bit weights with
+ * their product.  Matrices are row-major and contiguous; element alignment is enough
+ * for plain tensors, packed ones are aligned to 16.  Sums are held in 32 bits and
+ * each result is rounded once (to nearest, ties to even).  Results do not depend on
+ * timing.  Sizes of zero are allowed and write what there is to write.
+ */
+
+/* Element types of plain tensors. */
+#define IBP_F32 0
+#define IBP_F16 1
+#define IBP_BF16 2
+
+/* Largest row length (dim, cols) and largest number of tokens of one gradient. */
+#define IBP_MAX_COLS (1u << 30)
+#define IBP_MAX_TOKENS (1ull << 31)
+
+/*
+ * Embedding lookup: d_out[j] = scale * table[d_ids[j]], j < n_ids, rows of dim
+ * elements.  table: n_rows x dim of table_dtype (device, or pinned host memory read
+ * zero-copy); d_out: n_ids x dim of out_dtype.  An id that is negative or >= n_rows
+ * gives a row of zeros and sets IBP_DEVERR_BAD_ID.  n_rows == 0 with n_ids > 0 is
+ * IBP_ERR_SIZE.  Asynchronous.
+ */
+IBP_API int ibp_embedding_lookup(const void *table, int table_dtype, uint64_t n_rows, uint32_t dim,
+                                 const int64_t *d_ids, uint64_t n_ids, float scale, void *d_out, int out_dtype,
+                                 uint32_t *d_err_word, void *hip_stream);
+
+/* Workspace of ibp_embedding_grad. */
+IBP_API uint64_t ibp_embedding_grad_workspace_bytes(uint64_t n_rows, uint64_t n_ids, uint32_t dim);
+
+/*
+ * Its gradient: d_grad[v] = scale * sum of d_dout[j] over all j with d_ids[j] == v, in
+ * 32 bits and in an order that depends on the ids alone; rows without tokens are 0.
+ * Every element of d_grad (n_rows x dim of grad_dtype) is written.  padding_id: an id
+ * whose tokens take no part, -1 for none.  Ids out of range take no part and set
+ * IBP_DEVERR_BAD_ID.  n_rows < 2^32 - 1, n_ids < IBP_MAX_TOKENS.  d_workspace: aligned
+ * to 16, ibp_embedding_grad_workspace_bytes(...) bytes.  Asynchronous.
+ */
+IBP_API int ibp_embedding_grad(const void *d_dout, int dout_dtype, const int64_t *d_ids, uint64_t n_ids,
+                               uint64_t n_rows, uint32_t dim, float scale, int64_t padding_id, void *d_grad,
+                               int grad_dtype, void *d_workspace, uint64_t workspace_bytes, uint32_t *d_err_word,
+                               void *hip_stream);
+
+/*
+ * Microscaled tensors.  A row of cols elements is cut into blocks of 32 (the last one
+ * filled up with zeros).  A block has the scale 2^s, s the smallest exponent with
+ * max|x| <= M * 2^s, where M is the element type's largest value (448 for e4m3, 6 for
+ * e2m1), at least -117 and at most 119 (e4m3) or 125 (e2m1); an element is x / 2^s
+ * rounded to the nearest code, ties to even, saturating at M.  A block that holds an
+ * infinity or a NaN reads back as NaN throughout.
+ *   codes:  rows x ibp_mx_codes_pitch(cols, format) bytes; e4m3 one byte an element,
+ *           e2m1 two elements a byte, the even one in the low nibble.
+ *   scales: rows x ibp_mx_scales_pitch(cols) bytes; block b's byte is s + 127, 255 for
+ *           a NaN block; the bytes that fill a row up to a multiple of 4 are 0.
+ * Both are device memory, codes aligned to 16, scales to 4.  Codes and scales made
+ * elsewhere are taken as they are (any scale byte, 255 as NaN).
+ */
+#define IBP_MX_E4M3 0
+#define IBP_MX_E2M1 1
+typedef struct {
+  uint32_t format;   /* IBP_MX_E4M3 or IBP_MX_E2M1 */
+  uint32_t reserved; /* must be 0 */
+  uint64_t rows;
+  uint64_t cols;     /* <= IBP_MAX_COLS */
+  uint8_t *codes;
+  uint8_t *scales;
+} ibp_mx_t;
+
+/* Bytes from one row of codes, or of scales, to the next; 0 for an unknown format. */
+IBP_API uint64_t ibp_mx_codes_pitch(uint64_t cols, uint32_t format);
+IBP_API uint64_t ibp_mx_scales_pitch(uint64_t cols);
+
+/* Pack d_in (out->rows x out->cols of dtype) into out's codes and scales, and read a
+ * packed tensor back (values past the type's range become infinities).  Asynchronous. */
+IBP_API int ibp_mx_pack(const void *d_in, int dtype, const ibp_mx_t *out, void *hip_stream);
+IBP_API int ibp_mx_unpack(const ibp_mx_t *in, void *d_out, int dtype, void *hip_stream);
+
+/*
+ * Gated activation that keeps its inputs in 8 bits: d_h = silu(d_gate) * d_up with
+ * silu(g) = g / (1 + exp(-g)), from the inputs as they come, and gate8 / up8 = their
+ * e4m3 packings, in one pass.  All are gate8->rows x gate8->cols; gate8 and up8 have
+ * one shape.  The backward pass takes g and u from the checkpoints: with
+ * s = 1 / (1 + exp(-g)), d_dgate = dh u s (1 + g (1 - s)) and d_dup = dh g s.
+ * Asynchronous.
+ */
+IBP_API int ibp_mx_swiglu(const void *d_gate, const void *d_up, int dtype, void *d_h, const ibp_mx_t *gate8,
+                          const ibp_mx_t *up8, void *hip_stream);
+IBP_API int ibp_mx_swiglu_backward(const void *d_dh, int dtype, const ibp_mx_t *gate8, const ibp_mx_t *up8,
+                                   void *d_dgate, void *d_dup, void *hip_stream);
+
+/* Workspaces of the two products (0 where the shape needs none). */
+IBP_API uint64_t ibp_mx_matmul_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, uint32_t a_format);
+IBP_API uint64_t ibp_mx_linear_wgrad_workspace_bytes(uint64_t tokens, uint64_t outs, uint64_t ins);
+
+/*
+ * Product with packed weights: d_y[i][j] = sum over k of a[i][k] * b[j][k], a of M rows
+ * (e4m3 or e2m1), b of N rows (e2m1), a->cols == b->cols, d_y M x N of dtype.
+ * d_workspace may be NULL when the query says 0; aligned to 16.  Asynchronous.
+ */
+IBP_API int ibp_mx_matmul(const ibp_mx_t *a, const ibp_mx_t *b, void *d_y, int dtype, void *d_workspace,
+                          uint64_t workspace_bytes, void *hip_stream);
+
+/*
+ * Weight gradient of a linear layer from the 8-bit checkpoint of its input:
+ * d_dw[o][i] = sum over t of d_dy[t][o] * x8[t][i], d_dy x8->rows x outs of dy_dtype
+ * (IBP_BF16), x8 in e4m3, d_dw outs x x8->cols of dw_dtype.  x8 is decoded exactly
+ * (every e4m3 value times its scale is a BF16 number for scale bytes of 10 to 246).
+ * Asynchronous.
+ */
+IBP_API int ibp_mx_linear_wgrad(const void *d_dy, int dy_dtype, uint64_t outs, const ibp_mx_t *x8, void *d_dw,
+                                int dw_dtype, void *d_workspace, uint64_t workspace_bytes, void *hip_stream);
+
 #ifdef __cplusplus
 }
 #endif
