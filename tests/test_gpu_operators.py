@@ -292,7 +292,8 @@ def device(ibp, codes, scales, cols, fmt):
 
 
 PRODUCTS = [(1, 1, 1), (1, 16, 32), (2, 33, 31), (16, 17, 129), (17, 100, 512), (31, 64, 513), (64, 65, 1000),
-            (65, 200, 96), (130, 129, 640), (257, 300, 1056), (1, 1000, 2080), (300, 20, 160), (512, 512, 256)]
+            (65, 200, 96), (130, 129, 640), (257, 300, 1056), (1, 1000, 2080), (300, 20, 160), (512, 512, 256),
+            (1000, 1100, 288), (1030, 1000, 33), (3500, 3600, 160), (3600, 3500, 545)]
 
 
 @pytest.mark.parametrize("fmt", [mx_ref.E4M3, mx_ref.E2M1])
