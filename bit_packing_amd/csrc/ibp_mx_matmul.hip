@@ -11,6 +11,7 @@
 // results are consecutive n of one m.
 #include "ibp_device.h"
 #include "ibp_num.h"
+#include "ibp_tile.h"
 
 namespace ibp {
 namespace {
@@ -140,19 +141,6 @@ template <uint32_t PITCH> __device__ __forceinline__ uint32_t swizzle(uint32_t r
   return PITCH == 128 ? piece ^ ((row >> 1) & 7) : piece ^ ((row >> 2) & 3);
 }
 
-__device__ __align__(16) const uint8_t kZeros[16] = {};
-
-typedef __attribute__((address_space(3))) void lds_void;
-typedef const __attribute__((address_space(1))) void global_void;
-
-// Lane l's 16 (or 4) bytes at `from` go to byte 16 l (4 l) of the wavefront's `to`.
-__device__ __forceinline__ void to_lds16(const uint8_t *from, uint8_t *to) {
-  __builtin_amdgcn_global_load_lds((global_void *)from, (lds_void *)to, 16, 0, 0);
-}
-__device__ __forceinline__ void to_lds4(const uint8_t *from, uint8_t *to) {
-  __builtin_amdgcn_global_load_lds((global_void *)from, (lds_void *)to, 4, 0, 0);
-}
-
 // One operand's part of a stage: ROWS rows of PITCH bytes of codes, their scale bytes.
 template <uint32_t ROWS, uint32_t PITCH, uint32_t SCALES, uint32_t WAVES> struct Tile {
   static constexpr uint32_t kCodes = ROWS * PITCH, kBytes = kCodes + ROWS * SCALES;
@@ -205,15 +193,8 @@ __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, uin
   constexpr uint32_t kStage = TileA::kBytes + TileB::kBytes;
   __shared__ __align__(1024) uint8_t stages[2 * kStage];
   const uint32_t lane = lane_id(), wave = uniform(threadIdx.x / kWave), r = lane & 15, g = lane >> 4;
-  // Tiles of one XCD lie together (workgroups go to the eight XCDs in turn), in bands of
-  // kBand tile rows walked column by column, so its L2 keeps the band's rows of A.
-  constexpr uint32_t kXcds = 8, kBand = 8;
-  const uint32_t total = tiles_m * tiles_n, per = total / kXcds, rest = total % kXcds;
-  const uint32_t x = blockIdx.x % kXcds, q = blockIdx.x / kXcds;
-  const uint32_t id = x * per + (x < rest ? x : rest) + q;
-  const uint32_t band = id / (kBand * tiles_n), in = id % (kBand * tiles_n);
-  const uint32_t high = tiles_m - band * kBand < kBand ? tiles_m - band * kBand : kBand;
-  const uint64_t m0 = (uint64_t)(band * kBand + in % high) * kRowsA, n0 = (uint64_t)(in / high) * kRowsB;
+  const TileId t = tile_of(blockIdx.x, tiles_m, tiles_n);
+  const uint64_t m0 = (uint64_t)t.row * kRowsA, n0 = (uint64_t)t.col * kRowsB;
 
   const uint32_t nblk = (uint32_t)mx_blocks(a.K), sp = (uint32_t)mx_scale_pitch(a.K);
   const uint32_t cpa = (uint32_t)mx_code_pitch(a.K, A8), cpb = (uint32_t)mx_code_pitch(a.K, false);

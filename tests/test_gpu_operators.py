@@ -345,7 +345,8 @@ def test_matmul_of_nothing(ibp):
 
 
 WGRADS = [(1, 1, 1), (31, 16, 32), (32, 33, 31), (33, 128, 129), (100, 130, 257), (999, 50, 100), (3000, 40, 64),
-          (700, 300, 520), (5000, 129, 64), (64, 512, 512)]
+          (700, 300, 520), (5000, 129, 64), (64, 512, 512),
+          (130, 3504, 3600), (97, 3601, 3500), (2100, 520, 500)]
 
 
 @pytest.mark.parametrize("t,n,k", WGRADS)
