@@ -99,11 +99,16 @@ class MxTensor:
 
     def struct(self) -> ibp_mx_t:
         # the C side sees pointers only: the tensors must hold what the shape says
-        blocks = -(-self.cols // 32)
-        if _nbytes(self.codes) < self.rows * blocks * (32 if self.format == IBP_MX_E4M3 else 16) or \
-                _nbytes(self.scales) < self.rows * (-(-blocks // 4) * 4):
+        codes, scales = _mx_pitches(self.cols, self.format)
+        if _nbytes(self.codes) < self.rows * codes or _nbytes(self.scales) < self.rows * scales:
             raise ValueError("codes or scales are smaller than their shape needs")
         return ibp_mx_t(self.format, 0, self.rows, self.cols, _ptr(self.codes), _ptr(self.scales))
+
+
+def _mx_pitches(cols: int, format: int) -> tuple[int, int]:
+    """Bytes from one row of codes, and of scales, to the next."""
+    blocks = (cols + 31) // 32
+    return blocks * (32 if format == IBP_MX_E4M3 else 16), (blocks + 3) // 4 * 4
 
 
 @dataclass
@@ -228,8 +233,14 @@ def _nbytes(t: torch.Tensor) -> int:
     return t.numel() * t.element_size()
 
 
+# the current stream's handle without a Stream object around it (2.7 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -612,9 +623,9 @@ def ibp_embedding_grad_workspace_bytes(n_rows: int, n_ids: int, dim: int) -> int
 
 def make_mx(rows: int, cols: int, format: int, device) -> MxTensor:
     """An MxTensor of unwritten codes and scales."""
-    return MxTensor(torch.empty((rows, ibp_mx_codes_pitch(cols, format)), dtype=torch.uint8, device=device),
-                    torch.empty((rows, ibp_mx_scales_pitch(cols)), dtype=torch.uint8, device=device),
-                    rows, cols, format)
+    codes, scales = _mx_pitches(cols, format)
+    return MxTensor(torch.empty((rows, codes), dtype=torch.uint8, device=device),
+                    torch.empty((rows, scales), dtype=torch.uint8, device=device), rows, cols, format)
 
 
 def _mx(m: MxTensor | None, rows: int, cols: int, format: int, device) -> MxTensor:

@@ -56,16 +56,16 @@ template <int DI, int DO> __global__ __launch_bounds__(kBlock) void lookup_kerne
       if (live[k] && !ok[k] && tx == 0 && a.err) atomicOr(a.err, IBP_DEVERR_BAD_ID);
     }
     for (uint32_t c = tx * 8; c < a.dim; c += w.lanes * 8) {
-      F8 x[kRowsEach];
+      Vec8<TI> x[kRowsEach];
 #pragma unroll
-      for (uint32_t k = 0; k < kRowsEach; ++k) x[k] = load8<TI>(table + id[k] * a.dim, ok[k] ? c : a.dim, a.dim);
+      for (uint32_t k = 0; k < kRowsEach; ++k) x[k] = load8<TI>(table + id[k] * a.dim, c, a.dim);
 #pragma unroll
       for (uint32_t k = 0; k < kRowsEach; ++k) {
         if (!live[k]) continue;
+        F8 y = widen<TI>(x[k]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[k].v[i] *= a.scale;
-        if (!ok[k]) x[k] = F8{};
-        store8<TO>(out + (j0 + (uint64_t)k * w.rows_blk) * a.dim, c, a.dim, x[k]);
+        for (int i = 0; i < 8; ++i) y.v[i] = ok[k] ? y.v[i] * a.scale : 0.0f;
+        store8<TO>(out + (j0 + (uint64_t)k * w.rows_blk) * a.dim, c, a.dim, y);
       }
     }
   }
@@ -314,7 +314,7 @@ template <typename TI, typename TO> __device__ __forceinline__ void sum_chunk(co
   constexpr uint32_t kFlight = 8;
   for (uint32_t i = i0; i < i1; i += kFlight) {
     Pair p[kFlight];
-    F8 x[kFlight];
+    Vec8<TI> x[kFlight];
 #pragma unroll
     for (uint32_t k = 0; k < kFlight; ++k) p[k] = a.sorted[i + k < i1 ? i + k : i1 - 1];
 #pragma unroll
@@ -329,8 +329,9 @@ template <typename TI, typename TO> __device__ __forceinline__ void sum_chunk(co
         acc = F8{};
         key = p[k].key;
       }
+      const F8 y = widen<TI>(x[k]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc.v[e] += x[k].v[e];
+      for (int e = 0; e < 8; ++e) acc.v[e] += y.v[e];
     }
   }
   if (key == none) return;
@@ -374,10 +375,10 @@ template <typename TO> __device__ __forceinline__ void join_chunk(const SumArgs 
     else hi = mid;
   }
   const uint32_t last = (lo - 1) / a.chunk;
-  F8 acc = load8<float>(a.part + ((uint64_t)ck * 2 + 1) * a.dim, c, a.dim);
+  F8 acc = widen<float>(load8<float>(a.part + ((uint64_t)ck * 2 + 1) * a.dim, c, a.dim));
   constexpr uint32_t kFlight = 8;
   for (uint32_t k0 = ck + 1; k0 <= last; k0 += kFlight) {
-    F8 x[kFlight];
+    Vec8<float> x[kFlight];
 #pragma unroll
     for (uint32_t k = 0; k < kFlight; ++k)
       x[k] = load8<float>(a.part + (uint64_t)(k0 + k <= last ? k0 + k : last) * 2 * a.dim, c, a.dim);
@@ -385,7 +386,7 @@ template <typename TO> __device__ __forceinline__ void join_chunk(const SumArgs 
     for (uint32_t k = 0; k < kFlight; ++k)
       if (k0 + k <= last) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc.v[e] += x[k].v[e];
+        for (int e = 0; e < 8; ++e) acc.v[e] += x[k][e];
       }
   }
   put_row<TO>(a, key, c, acc);

@@ -5,9 +5,9 @@
 // All four are one pass over the data, bound by HBM.  A lane takes eight consecutive
 // elements (16 bytes of a 16-bit type), so four lanes hold a block and share its
 // largest magnitude by two lane exchanges, and 16 lanes hold the four blocks whose
-// scale bytes make one dword.  A row is taken by the smallest power of two of lanes,
-// from 16 to the workgroup, that covers it; kRowsEach rows per lane are loaded before
-// any of them is worked on, so a wavefront keeps that many loads in flight.
+// scale bytes make one dword.  A row is cut into strips of 8 times the smallest power of
+// two of lanes, from 16 to the workgroup, that covers it; a workgroup step is one strip
+// of R * 256 / lanes rows, R of them per lane, loaded before any is worked on.
 #include "ibp_device.h"
 #include "ibp_num.h"
 
@@ -16,7 +16,12 @@ namespace {
 
 using namespace dev;
 
-constexpr uint32_t kRowsEach = 4;
+// Exchanges within a row of 16 lanes: lane ^ 1, lane ^ 2 (quad permutes), rotations by
+// 4 and 8 lanes.
+template <int CTRL> __device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kRor4 = 0x124, kRor8 = 0x128;
 
 // Largest magnitude of the block that the lane's four-lane group holds, as float bits.
 __device__ __forceinline__ uint32_t block_amax(const F8 &x) {
@@ -26,31 +31,28 @@ __device__ __forceinline__ uint32_t block_amax(const F8 &x) {
     const uint32_t b = __builtin_bit_cast(uint32_t, x.v[i]) & 0x7FFFFFFFu;  // ordered as integers, NaN on top
     m = b > m ? b : m;
   }
-  uint32_t o = (uint32_t)__shfl_xor((int)m, 1, kWave);
+  uint32_t o = dpp<kXor1>(m);
   m = o > m ? o : m;
-  o = (uint32_t)__shfl_xor((int)m, 2, kWave);
+  o = dpp<kXor2>(m);
   return o > m ? o : m;
 }
 
 // One lane's eight elements at column c of a row into the row's codes and scales.
-// All 16 lanes of the group call it; columns past the row's blocks write nothing but
-// the padding bytes of the scale dword.
+// All 16 lanes of the group call it; columns past the row's blocks write nothing, and
+// their bytes of a scale dword are 0.
 template <bool E4M3>
 __device__ __forceinline__ void encode_lane(const F8 &x, uint8_t *codes, uint8_t *scales, uint32_t c, uint32_t nblk,
                                             bool row_ok) {
   const uint32_t scale = mx_scale<E4M3>(block_amax(x));
   const uint2 q = mx_encode<E4M3>(x, scale);
   const uint32_t blk = c / kMxBlock;
-  // bytes of blocks past the row's end are 0
   uint32_t s = blk < nblk ? scale << (8 * (blk & 3)) : 0u;
-  s |= (uint32_t)__shfl_xor((int)s, 4, kWave);
-  s |= (uint32_t)__shfl_xor((int)s, 8, kWave);
-  if (!row_ok) return;
-  if (blk < nblk) {
-    if constexpr (E4M3) *reinterpret_cast<uint2 *>(codes + c) = q;
-    else *reinterpret_cast<uint32_t *>(codes + c / 2) = q.x;
-  }
-  if ((c & 127) == 0 && blk < nblk) *reinterpret_cast<uint32_t *>(scales + blk) = s;
+  s |= dpp<kRor4>(s);
+  s |= dpp<kRor8>(s);
+  if (!row_ok || blk >= nblk) return;
+  if constexpr (E4M3) *reinterpret_cast<uint2 *>(codes + c) = q;
+  else *reinterpret_cast<uint32_t *>(codes + c / 2) = q.x;
+  if ((c & 127) == 0) *reinterpret_cast<uint32_t *>(scales + blk) = s;
 }
 
 template <bool E4M3> __device__ __forceinline__ uint2 load_codes(const uint8_t *codes, uint32_t c) {
@@ -58,193 +60,211 @@ template <bool E4M3> __device__ __forceinline__ uint2 load_codes(const uint8_t *
   return make_uint2(*reinterpret_cast<const uint32_t *>(codes + c / 2), 0u);
 }
 
-// Row and column walk shared by the kernels: `lanes` lanes a row, kRowsEach rows a lane.
+// 1 / (1 + exp(-g)).  The 16-bit types take it from the hardware's exp2 and reciprocal
+// (1 unit of the last place each), the argument's rounding made good by a factor: 6 half
+// units in all, far below the result's own rounding, for a third of the instructions
+// (the kernels are bound by instructions otherwise: forward 16384 x 8192 in bf16 FWD us
+// against FWDL us).  32-bit results take the library's exp and a true quotient.
+template <int D> __device__ __forceinline__ float sigmoid(float g) {
+  if constexpr (D == IBP_F32) {
+    return 1.0f / (1.0f + expf(-g));
+  } else {
+    constexpr float kLog2e = 1.44269502162933349609375f, kLog2eRest = 1.925963033500011e-8f, kLn2 = 0.693147182f;
+    const float x = fminf(fmaxf(-g, -200.0f), 200.0f);  // exp2 is 0 or infinite beyond
+    const float t = x * kLog2e;
+    const float rest = fmaf(x, kLog2eRest, fmaf(x, kLog2e, -t));
+    const float e = __builtin_amdgcn_exp2f(t) * fmaf(rest, kLn2, 1.0f);
+    return __builtin_amdgcn_rcpf(1.0f + e);
+  }
+}
+
 struct Walk {
-  uint32_t lanes;     // power of two, 16..kBlock
-  uint32_t rows_blk;  // rows that a workgroup's lanes cover: kBlock / lanes
-  uint64_t steps;     // workgroup steps of rows_blk * kRowsEach rows, walked by the grid
+  uint32_t lanes;   // lanes a row, a power of two, 16..kBlock
+  uint32_t strips;  // strips of lanes * 8 columns a row
+  uint32_t units;   // strips of all groups of R * kBlock / lanes rows
 };
 
-template <int D, bool E4M3>
-__global__ __launch_bounds__(kBlock) void mx_pack_kernel(MxArgs a, Walk w) {
+// This lane's column and rows of one unit.
+template <uint32_t R> struct Place {
+  uint32_t c;
+  uint64_t row[R];
+  bool ok[R];
+  __device__ __forceinline__ Place(const Walk &w, uint32_t unit, uint64_t rows) {
+    const uint32_t group = unit / w.strips, strip = unit - group * w.strips, rows_blk = kBlock / w.lanes;
+    c = (strip * w.lanes + (threadIdx.x & (w.lanes - 1))) * 8;
+#pragma unroll
+    for (uint32_t k = 0; k < R; ++k) {
+      row[k] = ((uint64_t)group * R + k) * rows_blk + threadIdx.x / w.lanes;
+      ok[k] = row[k] < rows;
+      if (!ok[k]) row[k] = rows - 1;
+    }
+  }
+};
+
+template <int D, bool E4M3, uint32_t R> __global__ __launch_bounds__(kBlock) void mx_pack_kernel(MxArgs a, Walk w) {
   using T = typename Num<D>::T;
-  const uint32_t tx = threadIdx.x & (w.lanes - 1), ty = threadIdx.x / w.lanes;
   const uint32_t nblk = (uint32_t)mx_blocks(a.cols);
   const uint64_t cp = mx_code_pitch(a.cols, E4M3), sp = mx_scale_pitch(a.cols);
   const T *in = static_cast<const T *>(a.in);
-  for (uint64_t step = blockIdx.x; step < w.steps; step += gridDim.x)
-  for (uint32_t c0 = 0; c0 < nblk * kMxBlock; c0 += w.lanes * 8) {
-    const uint64_t r0 = step * w.rows_blk * kRowsEach + ty;
-    const uint32_t c = c0 + tx * 8;
-    F8 x[kRowsEach];
+  for (uint32_t unit = blockIdx.x; unit < w.units; unit += gridDim.x) {
+    const Place<R> p(w, unit, a.rows);
+    Vec8<T> x[R];
 #pragma unroll
-    for (uint32_t k = 0; k < kRowsEach; ++k) {
-      const uint64_t r = r0 + (uint64_t)k * w.rows_blk;
-      x[k] = load8<T>(in + (r < a.rows ? r : 0) * a.cols, r < a.rows ? c : a.cols, a.cols);
-    }
+    for (uint32_t k = 0; k < R; ++k) x[k] = load8<T>(in + p.row[k] * a.cols, p.c, a.cols);
 #pragma unroll
-    for (uint32_t k = 0; k < kRowsEach; ++k) {
-      const uint64_t r = r0 + (uint64_t)k * w.rows_blk;
-      encode_lane<E4M3>(x[k], a.codes + r * cp, a.scales + r * sp, c, nblk, r < a.rows);
-    }
+    for (uint32_t k = 0; k < R; ++k)
+      encode_lane<E4M3>(widen<T>(x[k]), a.codes + p.row[k] * cp, a.scales + p.row[k] * sp, p.c, nblk, p.ok[k]);
   }
 }
 
-template <int D, bool E4M3>
-__global__ __launch_bounds__(kBlock) void mx_unpack_kernel(MxArgs a, Walk w) {
+template <int D, bool E4M3, uint32_t R> __global__ __launch_bounds__(kBlock) void mx_unpack_kernel(MxArgs a, Walk w) {
   using T = typename Num<D>::T;
-  const uint32_t tx = threadIdx.x & (w.lanes - 1), ty = threadIdx.x / w.lanes;
   const uint64_t cp = mx_code_pitch(a.cols, E4M3), sp = mx_scale_pitch(a.cols);
   T *out = static_cast<T *>(a.out);
-  for (uint64_t step = blockIdx.x; step < w.steps; step += gridDim.x)
-  for (uint32_t c0 = 0; c0 < a.cols; c0 += w.lanes * 8) {
-    const uint64_t r0 = step * w.rows_blk * kRowsEach + ty;
-    const uint32_t c = c0 + tx * 8;
-    uint2 q[kRowsEach];
-    uint32_t s[kRowsEach];
+  for (uint32_t unit = blockIdx.x; unit < w.units; unit += gridDim.x) {
+    const Place<R> p(w, unit, a.rows);
+    if (p.c >= a.cols) continue;
+    uint2 q[R];
+    uint32_t s[R];
 #pragma unroll
-    for (uint32_t k = 0; k < kRowsEach; ++k) {
-      const uint64_t r = r0 + (uint64_t)k * w.rows_blk;
-      if (r < a.rows && c < a.cols) {
-        q[k] = load_codes<E4M3>(a.codes + r * cp, c);
-        s[k] = a.scales[r * sp + c / kMxBlock];
-      }
+    for (uint32_t k = 0; k < R; ++k) {
+      q[k] = load_codes<E4M3>(a.codes + p.row[k] * cp, p.c);
+      s[k] = a.scales[p.row[k] * sp + p.c / kMxBlock];
     }
 #pragma unroll
-    for (uint32_t k = 0; k < kRowsEach; ++k) {
-      const uint64_t r = r0 + (uint64_t)k * w.rows_blk;
-      if (r < a.rows && c < a.cols) store8<T>(out + r * a.cols, c, a.cols, mx_decode<E4M3>(q[k], s[k]));
-    }
+    for (uint32_t k = 0; k < R; ++k)
+      if (p.ok[k]) store8<T>(out + p.row[k] * a.cols, p.c, a.cols, mx_decode<E4M3>(q[k], s[k]));
   }
 }
 
-// h = g / (1 + exp(-g)) * u in 32 bits from the inputs as they came; g and u packed.
-template <int D>
-__global__ __launch_bounds__(kBlock) void mx_swiglu_kernel(MxArgs a, Walk w) {
+// h = g * sigmoid(g) * u in 32 bits from the inputs as they came; g and u packed.
+template <int D, uint32_t R> __global__ __launch_bounds__(kBlock) void mx_swiglu_kernel(MxArgs a, Walk w) {
   using T = typename Num<D>::T;
-  const uint32_t tx = threadIdx.x & (w.lanes - 1), ty = threadIdx.x / w.lanes;
   const uint32_t nblk = (uint32_t)mx_blocks(a.cols);
   const uint64_t cp = mx_code_pitch(a.cols, true), sp = mx_scale_pitch(a.cols);
   const T *gate = static_cast<const T *>(a.in), *up = static_cast<const T *>(a.in2);
   T *h = static_cast<T *>(a.out);
-  for (uint64_t step = blockIdx.x; step < w.steps; step += gridDim.x)
-  for (uint32_t c0 = 0; c0 < nblk * kMxBlock; c0 += w.lanes * 8) {
-    const uint64_t r0 = step * w.rows_blk * kRowsEach + ty;
-    const uint32_t c = c0 + tx * 8;
-    F8 g[kRowsEach], u[kRowsEach];
+  for (uint32_t unit = blockIdx.x; unit < w.units; unit += gridDim.x) {
+    const Place<R> p(w, unit, a.rows);
+    Vec8<T> vg[R], vu[R];
 #pragma unroll
-    for (uint32_t k = 0; k < kRowsEach; ++k) {
-      const uint64_t r = r0 + (uint64_t)k * w.rows_blk;
-      const uint64_t at = (r < a.rows ? r : 0) * a.cols;
-      g[k] = load8<T>(gate + at, r < a.rows ? c : a.cols, a.cols);
-      u[k] = load8<T>(up + at, r < a.rows ? c : a.cols, a.cols);
+    for (uint32_t k = 0; k < R; ++k) {
+      vg[k] = load8<T>(gate + p.row[k] * a.cols, p.c, a.cols);
+      vu[k] = load8<T>(up + p.row[k] * a.cols, p.c, a.cols);
     }
 #pragma unroll
-    for (uint32_t k = 0; k < kRowsEach; ++k) {
-      const uint64_t r = r0 + (uint64_t)k * w.rows_blk;
-      encode_lane<true>(g[k], a.codes + r * cp, a.scales + r * sp, c, nblk, r < a.rows);
-      encode_lane<true>(u[k], a.codes2 + r * cp, a.scales2 + r * sp, c, nblk, r < a.rows);
+    for (uint32_t k = 0; k < R; ++k) {
+      const F8 g = widen<T>(vg[k]), u = widen<T>(vu[k]);
+      encode_lane<true>(g, a.codes + p.row[k] * cp, a.scales + p.row[k] * sp, p.c, nblk, p.ok[k]);
+      encode_lane<true>(u, a.codes2 + p.row[k] * cp, a.scales2 + p.row[k] * sp, p.c, nblk, p.ok[k]);
       F8 o;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o.v[i] = g[k].v[i] / (1.0f + expf(-g[k].v[i])) * u[k].v[i];
-      if (r < a.rows && c < a.cols) store8<T>(h + r * a.cols, c, a.cols, o);
+      for (int i = 0; i < 8; ++i) o.v[i] = g.v[i] * sigmoid<D>(g.v[i]) * u.v[i];
+      if (p.ok[k] && p.c < a.cols) store8<T>(h + p.row[k] * a.cols, p.c, a.cols, o);
     }
   }
 }
 
-// With s = 1 / (1 + exp(-g)): dgate = dh u s (1 + g (1 - s)), dup = dh g s, g and u read
-// back from the checkpoints.
-template <int D>
-__global__ __launch_bounds__(kBlock) void mx_swiglu_backward_kernel(MxArgs a, Walk w) {
+// With s = sigmoid(g): dgate = dh u s (1 + g (1 - s)), dup = dh g s, g and u read back
+// from the checkpoints.
+template <int D, uint32_t R> __global__ __launch_bounds__(kBlock) void mx_swiglu_backward_kernel(MxArgs a, Walk w) {
   using T = typename Num<D>::T;
-  const uint32_t tx = threadIdx.x & (w.lanes - 1), ty = threadIdx.x / w.lanes;
   const uint64_t cp = mx_code_pitch(a.cols, true), sp = mx_scale_pitch(a.cols);
   const T *dh = static_cast<const T *>(a.in2);
   T *dgate = static_cast<T *>(a.out), *dup = static_cast<T *>(a.out2);
-  for (uint64_t step = blockIdx.x; step < w.steps; step += gridDim.x)
-  for (uint32_t c0 = 0; c0 < a.cols; c0 += w.lanes * 8) {
-    const uint64_t r0 = step * w.rows_blk * kRowsEach + ty;
-    const uint32_t c = c0 + tx * 8;
-    uint2 qg[kRowsEach], qu[kRowsEach];
-    uint32_t sg[kRowsEach], su[kRowsEach];
-    F8 d[kRowsEach];
+  for (uint32_t unit = blockIdx.x; unit < w.units; unit += gridDim.x) {
+    const Place<R> p(w, unit, a.rows);
+    if (p.c >= a.cols) continue;
+    uint2 qg[R], qu[R];
+    uint32_t sg[R], su[R];
+    Vec8<T> vd[R];
 #pragma unroll
-    for (uint32_t k = 0; k < kRowsEach; ++k) {
-      const uint64_t r = r0 + (uint64_t)k * w.rows_blk;
-      if (r < a.rows && c < a.cols) {
-        qg[k] = load_codes<true>(a.codes + r * cp, c);
-        qu[k] = load_codes<true>(a.codes2 + r * cp, c);
-        sg[k] = a.scales[r * sp + c / kMxBlock];
-        su[k] = a.scales2[r * sp + c / kMxBlock];
-        d[k] = load8<T>(dh + r * a.cols, c, a.cols);
-      }
+    for (uint32_t k = 0; k < R; ++k) {
+      qg[k] = load_codes<true>(a.codes + p.row[k] * cp, p.c);
+      qu[k] = load_codes<true>(a.codes2 + p.row[k] * cp, p.c);
+      sg[k] = a.scales[p.row[k] * sp + p.c / kMxBlock];
+      su[k] = a.scales2[p.row[k] * sp + p.c / kMxBlock];
+      vd[k] = load8<T>(dh + p.row[k] * a.cols, p.c, a.cols);
     }
 #pragma unroll
-    for (uint32_t k = 0; k < kRowsEach; ++k) {
-      const uint64_t r = r0 + (uint64_t)k * w.rows_blk;
-      if (r < a.rows && c < a.cols) {
-        const F8 g = mx_decode<true>(qg[k], sg[k]), u = mx_decode<true>(qu[k], su[k]);
-        F8 og, ou;
+    for (uint32_t k = 0; k < R; ++k) {
+      if (!p.ok[k]) continue;
+      const F8 g = mx_decode<true>(qg[k], sg[k]), u = mx_decode<true>(qu[k], su[k]), d = widen<T>(vd[k]);
+      F8 og, ou;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float s = 1.0f / (1.0f + expf(-g.v[i]));
-          og.v[i] = d[k].v[i] * u.v[i] * s * (1.0f + g.v[i] * (1.0f - s));
-          ou.v[i] = d[k].v[i] * g.v[i] * s;
-        }
-        store8<T>(dgate + r * a.cols, c, a.cols, og);
-        store8<T>(dup + r * a.cols, c, a.cols, ou);
+      for (int i = 0; i < 8; ++i) {
+        const float s = sigmoid<D>(g.v[i]), ds = d.v[i] * s;
+        og.v[i] = ds * u.v[i] * (1.0f + g.v[i] * (1.0f - s));
+        ou.v[i] = ds * g.v[i];
       }
+      store8<T>(dgate + p.row[k] * a.cols, p.c, a.cols, og);
+      store8<T>(dup + p.row[k] * a.cols, p.c, a.cols, ou);
     }
   }
 }
 
-uint32_t walk_of(const MxArgs &a, Walk *w) {
+constexpr uint32_t kMaxGrid = 1u << 22;
+
+// Rows per lane: four where that leaves the GPU full (1024 workgroups), else one, so
+// that small calls spread over the CUs.
+bool walk_of(const MxArgs &a, uint32_t each, Walk *w) {
   const uint32_t need = (a.cols + 7) / 8;  // lanes that a row has work for
   w->lanes = 16;
   while (w->lanes < need && w->lanes < kBlock) w->lanes *= 2;
-  w->rows_blk = kBlock / w->lanes;
-  const uint64_t each = (uint64_t)w->rows_blk * kRowsEach;
-  w->steps = (a.rows + each - 1) / each;
-  return (uint32_t)(w->steps < (1u << 22) ? w->steps : (1u << 22));
+  w->strips = (need + w->lanes - 1) / w->lanes;
+  const uint64_t rows = (uint64_t)(kBlock / w->lanes) * each, groups = (a.rows + rows - 1) / rows;
+  const unsigned __int128 units = (unsigned __int128)groups * w->strips;
+  if (units > 0xFFFFFFFFu - kMaxGrid) return false;
+  w->units = (uint32_t)units;
+  return true;
+}
+
+template <typename F> hipError_t with_walk(const MxArgs &a, F &&f) {
+  Walk w;
+  if (!walk_of(a, 4, &w)) return hipErrorInvalidValue;
+  auto grid = [&] { return w.units < kMaxGrid ? w.units : kMaxGrid; };
+  if (w.units >= 1024) {
+    f(std::integral_constant<uint32_t, 4>{}, w, grid());
+  } else {
+    if (!walk_of(a, 1, &w)) return hipErrorInvalidValue;
+    f(std::integral_constant<uint32_t, 1>{}, w, grid());
+  }
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_mx_pack(const MxArgs &a, hipStream_t s) {
-  Walk w;
-  const uint32_t blocks = walk_of(a, &w);
   return with_dtype(a.dtype, [&](auto d) {
-    if (a.e4m3) mx_pack_kernel<d.value, true><<<blocks, kBlock, 0, s>>>(a, w);
-    else mx_pack_kernel<d.value, false><<<blocks, kBlock, 0, s>>>(a, w);
-    return hipGetLastError();
+    return with_walk(a, [&](auto r, const Walk &w, uint32_t grid) {
+      if (a.e4m3) mx_pack_kernel<d.value, true, r.value><<<grid, kBlock, 0, s>>>(a, w);
+      else mx_pack_kernel<d.value, false, r.value><<<grid, kBlock, 0, s>>>(a, w);
+    });
   });
 }
 
 hipError_t launch_mx_unpack(const MxArgs &a, hipStream_t s) {
-  Walk w;
-  const uint32_t blocks = walk_of(a, &w);
   return with_dtype(a.dtype, [&](auto d) {
-    if (a.e4m3) mx_unpack_kernel<d.value, true><<<blocks, kBlock, 0, s>>>(a, w);
-    else mx_unpack_kernel<d.value, false><<<blocks, kBlock, 0, s>>>(a, w);
-    return hipGetLastError();
+    return with_walk(a, [&](auto r, const Walk &w, uint32_t grid) {
+      if (a.e4m3) mx_unpack_kernel<d.value, true, r.value><<<grid, kBlock, 0, s>>>(a, w);
+      else mx_unpack_kernel<d.value, false, r.value><<<grid, kBlock, 0, s>>>(a, w);
+    });
   });
 }
 
 hipError_t launch_mx_swiglu(const MxArgs &a, hipStream_t s) {
-  Walk w;
-  const uint32_t blocks = walk_of(a, &w);
   return with_dtype(a.dtype, [&](auto d) {
-    mx_swiglu_kernel<d.value><<<blocks, kBlock, 0, s>>>(a, w);
-    return hipGetLastError();
+    return with_walk(a, [&](auto r, const Walk &w, uint32_t grid) {
+      mx_swiglu_kernel<d.value, r.value><<<grid, kBlock, 0, s>>>(a, w);
+    });
   });
 }
 
 hipError_t launch_mx_swiglu_backward(const MxArgs &a, hipStream_t s) {
-  Walk w;
-  const uint32_t blocks = walk_of(a, &w);
   return with_dtype(a.dtype, [&](auto d) {
-    mx_swiglu_backward_kernel<d.value><<<blocks, kBlock, 0, s>>>(a, w);
-    return hipGetLastError();
+    return with_walk(a, [&](auto r, const Walk &w, uint32_t grid) {
+      mx_swiglu_backward_kernel<d.value, r.value><<<grid, kBlock, 0, s>>>(a, w);
+    });
   });
 }
 

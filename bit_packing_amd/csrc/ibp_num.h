@@ -23,17 +23,24 @@ template <typename T> using Vec8 = typename VecOf<T>::type;
 
 struct F8 { float v[8]; };
 
-// Elements [c, c + 8) of a row of `cols` elements, zeros past its end.
-template <typename T> __device__ __forceinline__ F8 load8(const T *row, uint32_t c, uint32_t cols) {
-  F8 r;
+// Elements [c, c + 8) of a row of `cols` elements, zeros past its end, as they lie in
+// memory: widened where they are used, so that the next load need not wait for this one.
+template <typename T> __device__ __forceinline__ Vec8<T> load8(const T *row, uint32_t c, uint32_t cols) {
+  Vec8<T> x = {};
   if (c + 8 <= cols) {
-    const Vec8<T> x = *reinterpret_cast<const Vec8<T> *>(row + c);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r.v[i] = (float)x[i];
+    x = *reinterpret_cast<const Vec8<T> *>(row + c);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r.v[i] = c + i < cols ? (float)row[c + i] : 0.0f;
+    for (int i = 0; i < 8; ++i)
+      if (c + i < cols) x[i] = row[c + i];
   }
+  return x;
+}
+
+template <typename T> __device__ __forceinline__ F8 widen(Vec8<T> x) {
+  F8 r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r.v[i] = (float)x[i];
   return r;
 }
 
