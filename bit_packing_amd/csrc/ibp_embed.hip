@@ -89,7 +89,7 @@ struct SortArgs {
   uint32_t *err;
   Pair *from, *to;      // from: unused by the first pass
   uint32_t *counts;     // [workgroup][kBins]
-  uint32_t *present;    // bit per row: has tokens
+  uint32_t *crossing;   // [0] cleared for the sums: chunks listed
   uint64_t n_rows;
   int64_t padding_id;
   uint32_t n;
@@ -117,21 +117,12 @@ __device__ __forceinline__ uint64_t same_digit(uint32_t d, uint32_t bits, uint64
   return m;
 }
 
-__device__ __forceinline__ void mark_present(uint32_t *present, uint32_t key) {
-  const uint32_t bit = 1u << (key & 31);
-  if (!(__hip_atomic_load(&present[key >> 5], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) & bit))
-    atomicOr(&present[key >> 5], bit);
-}
-
-// Per workgroup, how many of its tokens have each digit.  The first pass also clears
-// the presence bits that the next kernel sets.
+// Per workgroup, how many of its tokens have each digit.
 template <bool FIRST> __global__ __launch_bounds__(kBlock) void sort_count_kernel(SortArgs a) {
   __shared__ uint32_t hist[kBins];
   for (uint32_t i = threadIdx.x; i < kBins; i += kBlock) hist[i] = 0;
   if constexpr (FIRST) {
-    const uint64_t words = (a.n_rows + 31) / 32;
-    for (uint64_t i = (uint64_t)blockIdx.x * kBlock + threadIdx.x; i < words; i += (uint64_t)gridDim.x * kBlock)
-      a.present[i] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.crossing[0] = 0;
   }
   __syncthreads();
   const uint64_t b0 = (uint64_t)blockIdx.x * a.per_wave * kWavesPerBlock;
@@ -163,13 +154,21 @@ template <bool FIRST> __global__ __launch_bounds__(kBlock) void sort_scatter_ker
   }
   // totals of each digit, and its tokens in earlier workgroups; two digits a thread
   constexpr uint32_t kEach = kBins / kBlock;
+  static_assert(kEach == 2, "a thread reads its digits' counts as pairs");
   uint32_t total[kEach] = {}, before[kEach] = {};
-  for (uint32_t b = 0; b < gridDim.x; ++b) {
+  const uint2 *counts = reinterpret_cast<const uint2 *>(a.counts) + threadIdx.x;
+  constexpr uint32_t kFlight = 16;  // loads in flight: the counts come from L2
+  for (uint32_t b0 = 0; b0 < gridDim.x; b0 += kFlight) {
+    uint2 v[kFlight];
 #pragma unroll
-    for (uint32_t e = 0; e < kEach; ++e) {
-      const uint32_t v = a.counts[b * kBins + threadIdx.x * kEach + e];
-      total[e] += v;
-      before[e] += b < blockIdx.x ? v : 0u;
+    for (uint32_t k = 0; k < kFlight; ++k)
+      v[k] = b0 + k < gridDim.x ? counts[(b0 + k) * (kBins / 2)] : make_uint2(0u, 0u);
+#pragma unroll
+    for (uint32_t k = 0; k < kFlight; ++k) {
+      total[0] += v[k].x;
+      total[1] += v[k].y;
+      before[0] += b0 + k < blockIdx.x ? v[k].x : 0u;
+      before[1] += b0 + k < blockIdx.x ? v[k].y : 0u;
     }
   }
   uint32_t mine = 0;
@@ -207,23 +206,36 @@ template <bool FIRST> __global__ __launch_bounds__(kBlock) void sort_scatter_ker
     wave_lds_sync();
     if (live && rank == 0) off[wave][d] += popc(same);
     wave_lds_sync();
-    if (live && at < a.n) {  // always, unless the ids change while the call runs
-      a.to[at] = p;
-      if (FIRST && p.key < a.n_rows) mark_present(a.present, p.key);
-    }
+    if (live && at < a.n) a.to[at] = p;  // always, unless the ids change while the call runs
   }
 }
 
-// The whole sort of up to kSmallTokens tokens in one workgroup, pairs in LDS.
-__global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(SortArgs a, uint32_t passes, uint32_t total_bits) {
+// The whole sort of up to kSmallTokens tokens in one workgroup, pairs in LDS.  Further
+// workgroups clear `clear` (n_clear elements) meanwhile.
+template <int DO>
+__global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(SortArgs a, uint32_t passes, uint32_t total_bits,
+                                                                   void *clear, uint64_t n_clear) {
+  if (blockIdx.x > 0) {
+    using TO = typename Num<DO>::T;
+    TO *p = static_cast<TO *>(clear);
+    constexpr uint32_t kEach = 16 / sizeof(TO);
+    typedef TO V __attribute__((ext_vector_type(kEach), aligned(sizeof(TO))));
+    const uint64_t step = (uint64_t)(gridDim.x - 1) * kSmallThreads * kEach;
+    for (uint64_t i = ((uint64_t)(blockIdx.x - 1) * kSmallThreads + threadIdx.x) * kEach; i < n_clear; i += step) {
+      if (i + kEach <= n_clear) {
+        *reinterpret_cast<V *>(p + i) = V{};
+      } else {
+        for (uint64_t e = i; e < n_clear; ++e) p[e] = (TO)0.0f;
+      }
+    }
+    return;
+  }
   constexpr uint32_t kWaves = kSmallThreads / kWave;
   __shared__ Pair buf[2][kSmallTokens];
   __shared__ uint32_t off[kWaves][kBins];
   __shared__ uint32_t wave_total[kWaves];
   const uint32_t t = threadIdx.x, wave = uniform(t / kWave), lane = lane_id();
-  const uint64_t words = (a.n_rows + 31) / 32;
-  for (uint64_t i = t; i < words; i += kSmallThreads) a.present[i] = 0;
-  __threadfence();  // before other wavefronts set bits of them
+  if (t == 0) a.crossing[0] = 0;
   for (uint32_t j = t; j < a.n; j += kSmallThreads) buf[0][j] = Pair{key_of(a, j), j};
   const uint32_t w0 = wave * a.per_wave, w1 = w0 + a.per_wave, end = w1 < a.n ? w1 : a.n;
   uint32_t shift = 0, cur = 0;
@@ -268,11 +280,7 @@ __global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(SortArgs a, u
     cur ^= 1;
     shift += bits;
   }
-  for (uint32_t j = t; j < a.n; j += kSmallThreads) {
-    const Pair p = buf[cur][j];
-    a.to[j] = p;
-    if (p.key < a.n_rows) mark_present(a.present, p.key);
-  }
+  for (uint32_t j = t; j < a.n; j += kSmallThreads) a.to[j] = buf[cur][j];
 }
 
 // ------------------------------------------------------------------ sums of the sorted rows
@@ -280,8 +288,8 @@ __global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(SortArgs a, u
 struct SumArgs {
   const void *dout;
   const Pair *sorted;
-  const uint32_t *present;
   void *grad;
+  uint32_t *crossing;   // [0] how many chunks a run that is cut begins in, then those chunks in any order
   float *part;          // [chunk][2][dim]: sum of the chunk's first run when it began earlier, of its last when it goes on
   uint64_t n_rows;
   uint32_t n;
@@ -291,7 +299,7 @@ struct SumArgs {
   uint32_t lanes;       // lanes a row, a power of two up to kBlock
   uint32_t slab;        // columns that a group of lanes covers: lanes * 8
   uint32_t slabs;       // ceil(dim / slab)
-  uint32_t sum_blocks;  // workgroups that sum; the rest write zeros
+  uint32_t zero_blocks; // workgroups that write the rows without tokens; the rest sum
   float scale;
 };
 
@@ -301,28 +309,49 @@ template <typename TO> __device__ __forceinline__ void put_row(const SumArgs &a,
   store8<TO>(static_cast<TO *>(a.grad) + (uint64_t)row * a.dim, c, a.dim, v);
 }
 
-// Sums columns [c, c + 8) of the rows of chunk ck.
+// First of the sorted tokens [lo, hi) whose id is not below `key` (above it, with UPPER).
+template <bool UPPER> __device__ __forceinline__ uint32_t bound(const Pair *sorted, uint32_t lo, uint32_t hi, uint32_t key) {
+  while (lo < hi) {
+    const uint32_t mid = lo + (hi - lo) / 2, k = sorted[mid].key;
+    if (UPPER ? k <= key : k < key) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Sums columns [c, c + 8) of the rows of chunk ck: the runs that begin in it.  A run that
+// fills no chunk is taken to its end, into the next chunk if need be; one that fills a
+// chunk is cut at the chunks' borders, each chunk leaving a partial row.
 template <typename TI, typename TO> __device__ __forceinline__ void sum_chunk(const SumArgs &a, uint32_t ck, uint32_t c) {
   const TI *dout = static_cast<const TI *>(a.dout);
   const uint32_t i0 = ck * a.chunk, i1 = i0 + a.chunk < a.n ? i0 + a.chunk : a.n;
   const uint32_t none = (uint32_t)a.n_rows;
   uint32_t key = a.sorted[i0].key;
+  const uint32_t last = a.sorted[i1 - 1].key;
   if (key == none) return;
-  bool first = i0 > 0 && a.sorted[i0 - 1].key == key;  // the run began in an earlier chunk
+  const bool full = key == last;
+  const bool from_before = i0 > 0 && a.sorted[i0 - 1].key == key;
+  bool first = from_before && (full || a.sorted[i0 - a.chunk].key == key);  // the rest of a run that is cut
+  const bool goes_on = i1 < a.n && last != none && a.sorted[i1].key == last;
+  const uint32_t i2 = i1 + a.chunk < a.n ? i1 + a.chunk : a.n;
+  const bool cut = goes_on && (full || a.sorted[i2 - 1].key == last);
+  const uint32_t begin = from_before && !first ? bound<true>(a.sorted, i0, i1, key) : i0;
+  const uint32_t end = goes_on && !cut ? bound<true>(a.sorted, i1, i2, last) : i1;
   F8 acc{};
   float *part = a.part + (uint64_t)ck * 2 * a.dim;
+  if (begin > i0) key = a.sorted[begin].key;  // not full: begin < i1
   constexpr uint32_t kFlight = 8;
-  for (uint32_t i = i0; i < i1; i += kFlight) {
+  for (uint32_t i = begin; i < end; i += kFlight) {
     Pair p[kFlight];
     Vec8<TI> x[kFlight];
 #pragma unroll
-    for (uint32_t k = 0; k < kFlight; ++k) p[k] = a.sorted[i + k < i1 ? i + k : i1 - 1];
+    for (uint32_t k = 0; k < kFlight; ++k) p[k] = a.sorted[i + k < end ? i + k : end - 1];
 #pragma unroll
     for (uint32_t k = 0; k < kFlight; ++k) x[k] = load8<TI>(dout + (uint64_t)p[k].pos * a.dim, c, a.dim);
 #pragma unroll
     for (uint32_t k = 0; k < kFlight; ++k) {
-      if (i + k >= i1) break;
-      if (p[k].key != key) {  // the run ended inside the chunk
+      if (i + k >= end) break;
+      if (p[k].key != key) {  // the run ended
         if (first) store8<float>(part, c, a.dim, acc);
         else if (key != none) put_row<TO>(a, key, c, acc);
         first = false;
@@ -335,70 +364,97 @@ template <typename TI, typename TO> __device__ __forceinline__ void sum_chunk(co
     }
   }
   if (key == none) return;
-  if (first) store8<float>(part, c, a.dim, acc);
-  else if (i1 < a.n && a.sorted[i1].key == key) store8<float>(part + a.dim, c, a.dim, acc);
-  else put_row<TO>(a, key, c, acc);
+  if (first) {
+    store8<float>(part, c, a.dim, acc);
+  } else if (cut) {
+    store8<float>(part + a.dim, c, a.dim, acc);
+    if (c == 0) a.crossing[1 + atomicAdd(a.crossing, 1u)] = ck;
+  } else {
+    put_row<TO>(a, key, c, acc);
+  }
 }
 
+// The first zero_blocks workgroups write the rows without tokens, which they find by
+// search in the sorted tokens, a lane a row; the others sum.
 template <int DI, int DO> __global__ __launch_bounds__(kBlock) void grad_sum_kernel(SumArgs a) {
   using TI = typename Num<DI>::T;
   using TO = typename Num<DO>::T;
   const uint32_t tx = threadIdx.x & (a.lanes - 1), ty = threadIdx.x / a.lanes, groups = kBlock / a.lanes;
-  if (blockIdx.x >= a.sum_blocks) {
-    // rows without tokens are 0
-    const uint32_t zb = blockIdx.x - a.sum_blocks, zn = gridDim.x - a.sum_blocks;
-    for (uint64_t r = (uint64_t)zb * groups + ty; r < a.n_rows; r += (uint64_t)zn * groups)
-      if (!((a.present[r >> 5] >> (r & 31)) & 1u))
-        for (uint32_t c = tx * 8; c < a.dim; c += a.slab)
-          store8<TO>(static_cast<TO *>(a.grad) + r * a.dim, c, a.dim, F8{});
+  if (blockIdx.x < a.zero_blocks) {
+    __shared__ uint64_t empty;
+    for (uint64_t r0 = (uint64_t)blockIdx.x * kWave; r0 < a.n_rows; r0 += (uint64_t)a.zero_blocks * kWave) {
+      if (threadIdx.x < kWave) {
+        const uint64_t r = r0 + threadIdx.x;
+        bool none = false;
+        if (r < a.n_rows) {
+          const uint32_t at = bound<false>(a.sorted, 0, a.n, (uint32_t)r);
+          none = at >= a.n || a.sorted[at].key != (uint32_t)r;
+        }
+        const uint64_t m = ballot(none);
+        if (threadIdx.x == 0) empty = m;
+      }
+      __syncthreads();
+      const uint64_t m = empty;
+      for (uint32_t k = ty; k < kWave; k += groups)
+        if ((m >> k) & 1)
+          for (uint32_t c = tx * 8; c < a.dim; c += a.slab)
+            store8<TO>(static_cast<TO *>(a.grad) + (r0 + k) * a.dim, c, a.dim, F8{});
+      __syncthreads();
+    }
     return;
   }
-  const uint64_t units = (uint64_t)a.nchunks * a.slabs;
-  for (uint64_t unit = (uint64_t)blockIdx.x * groups + ty; unit < units; unit += (uint64_t)a.sum_blocks * groups) {
+  const uint64_t units = (uint64_t)a.nchunks * a.slabs, step = (uint64_t)(gridDim.x - a.zero_blocks) * groups;
+  for (uint64_t unit = (uint64_t)(blockIdx.x - a.zero_blocks) * groups + ty; unit < units; unit += step) {
     const uint32_t c = (uint32_t)(unit % a.slabs) * a.slab + tx * 8;
     if (c < a.dim) sum_chunk<TI, TO>(a, (uint32_t)(unit / a.slabs), c);
   }
 }
 
-// Runs that cross chunks: the group of the chunk in which such a run begins adds its
-// partial rows in order.
-template <typename TO> __device__ __forceinline__ void join_chunk(const SumArgs &a, uint32_t ck, uint32_t c) {
-  const uint32_t i0 = ck * a.chunk, i1 = i0 + a.chunk;
-  if (i1 >= a.n) return;
-  const uint32_t key = a.sorted[i1 - 1].key;
-  if (key == (uint32_t)a.n_rows || a.sorted[i1].key != key) return;
-  if (i0 > 0 && a.sorted[i0 - 1].key == key) return;  // sorted: it then fills this chunk and began earlier
-  uint32_t lo = i1 + 1, hi = a.n;  // first token after the run
-  while (lo < hi) {
-    const uint32_t mid = lo + (hi - lo) / 2;
-    if (a.sorted[mid].key == key) lo = mid + 1;
-    else hi = mid;
-  }
-  const uint32_t last = (lo - 1) / a.chunk;
-  F8 acc = widen<float>(load8<float>(a.part + ((uint64_t)ck * 2 + 1) * a.dim, c, a.dim));
-  constexpr uint32_t kFlight = 8;
-  for (uint32_t k0 = ck + 1; k0 <= last; k0 += kFlight) {
-    Vec8<float> x[kFlight];
-#pragma unroll
-    for (uint32_t k = 0; k < kFlight; ++k)
-      x[k] = load8<float>(a.part + (uint64_t)(k0 + k <= last ? k0 + k : last) * 2 * a.dim, c, a.dim);
-#pragma unroll
-    for (uint32_t k = 0; k < kFlight; ++k)
-      if (k0 + k <= last) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc.v[e] += x[k][e];
-      }
-  }
-  put_row<TO>(a, key, c, acc);
-}
-
-template <int DO> __global__ __launch_bounds__(kBlock) void grad_join_kernel(SumArgs a) {
+// Runs that are cut.  A workgroup takes a run and a strip of its columns; groups of
+// lanes add consecutive shares of the run's partial rows (a frequent token has hundreds)
+// and their sums are added in order, so the result does not depend on who took it.
+template <int DO> __global__ __launch_bounds__(kBlock) void grad_join_kernel(SumArgs a, uint32_t lanes, uint32_t strips) {
   using TO = typename Num<DO>::T;
-  const uint32_t tx = threadIdx.x & (a.lanes - 1), ty = threadIdx.x / a.lanes, groups = kBlock / a.lanes;
-  const uint64_t units = (uint64_t)a.nchunks * a.slabs;
-  for (uint64_t unit = (uint64_t)blockIdx.x * groups + ty; unit < units; unit += (uint64_t)gridDim.x * groups) {
-    const uint32_t c = (uint32_t)(unit % a.slabs) * a.slab + tx * 8;
-    if (c < a.dim) join_chunk<TO>(a, (uint32_t)(unit / a.slabs), c);
+  __shared__ float sums[kBlock * 8];
+  const uint32_t tx = threadIdx.x & (lanes - 1), ty = threadIdx.x / lanes, groups = kBlock / lanes;
+  const uint64_t items = (uint64_t)a.crossing[0] * strips;
+  for (uint64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const uint32_t ck = a.crossing[1 + item / strips], c = ((uint32_t)(item % strips) * lanes + tx) * 8;
+    const uint32_t key = a.sorted[(ck + 1) * a.chunk].key;
+    uint32_t follow = 0, found;  // chunks after ck that begin with the run's id
+    do {
+      const uint32_t k = ck + 1 + follow + threadIdx.x;
+      found = (uint32_t)__syncthreads_count(k < a.nchunks && a.sorted[k * a.chunk].key == key);
+      follow += found;
+    } while (found == kBlock);
+    const uint32_t parts = follow + 1, share = (parts + groups - 1) / groups;
+    const uint32_t p0 = ty * share, p1 = p0 + share < parts ? p0 + share : parts;
+    // partial 0 is the last run of chunk ck, partial p the first of chunk ck + p
+    auto row = [&](uint32_t p) { return a.part + ((uint64_t)(ck + p) * 2 + (p == 0)) * a.dim; };
+    F8 acc{};
+    constexpr uint32_t kFlight = 8;
+    for (uint32_t p = p0; p < p1; p += kFlight) {
+      Vec8<float> x[kFlight];
+#pragma unroll
+      for (uint32_t k = 0; k < kFlight; ++k) x[k] = load8<float>(row(p + k < p1 ? p + k : p1 - 1), c, a.dim);
+#pragma unroll
+      for (uint32_t k = 0; k < kFlight; ++k)
+        if (p + k < p1) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc.v[e] += x[k][e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sums[e * kBlock + threadIdx.x] = acc.v[e];
+    __syncthreads();
+    if (ty == 0 && c < a.dim) {
+      for (uint32_t g = 1; g < groups && g * share < parts; ++g) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc.v[e] += sums[e * kBlock + g * lanes + tx];
+      }
+      put_row<TO>(a, key, c, acc);
+    }
+    __syncthreads();
   }
 }
 
@@ -411,24 +467,24 @@ uint32_t grad_chunk(uint64_t n) { return n < 32768 ? 8 : 32; }
 uint64_t up16(uint64_t v) { return (v + 15) & ~15ull; }
 
 struct GradLayout {
-  uint64_t pairs, counts, present, part, bytes;  // byte offsets: two pair lists at pairs
+  uint64_t pairs, counts, crossing, part, bytes;  // byte offsets: two pair lists at pairs
 };
 
-GradLayout grad_layout(uint64_t n_rows, uint64_t n, uint32_t dim) {
+GradLayout grad_layout(uint64_t n, uint32_t dim) {
   GradLayout l;
   l.pairs = 0;
   l.counts = up16(2 * n * sizeof(Pair));
-  l.present = l.counts + kSortBlocks * kBins * 4;
-  l.part = l.present + up16((n_rows + 31) / 32 * 4);
-  const uint32_t ck = grad_chunk(n);
-  l.bytes = l.part + (n + ck - 1) / ck * 2 * dim * 4ull;
+  l.crossing = l.counts + kSortBlocks * kBins * 4;
+  const uint64_t ck = grad_chunk(n), chunks = (n + ck - 1) / ck;
+  l.part = l.crossing + up16(4 * (chunks + 1));
+  l.bytes = l.part + chunks * 2 * dim * 4;
   return l;
 }
 
 }  // namespace
 
-uint64_t embed_grad_workspace(uint64_t n_rows, uint64_t n_ids, uint32_t dim) {
-  return grad_layout(n_rows, n_ids, dim).bytes;
+uint64_t embed_grad_workspace(uint64_t, uint64_t n_ids, uint32_t dim) {
+  return grad_layout(n_ids, dim).bytes;
 }
 
 hipError_t launch_lookup(const LookupArgs &a, hipStream_t s) {
@@ -447,7 +503,7 @@ hipError_t launch_lookup(const LookupArgs &a, hipStream_t s) {
 }
 
 hipError_t launch_embed_grad(const EmbedGradArgs &a, hipStream_t s) {
-  const GradLayout l = grad_layout(a.n_rows, a.n_ids, a.dim);
+  const GradLayout l = grad_layout(a.n_ids, a.dim);
   Pair *pa = reinterpret_cast<Pair *>(a.ws + l.pairs), *pb = pa + a.n_ids;
   SortArgs so;
   so.ids = a.ids;
@@ -455,7 +511,7 @@ hipError_t launch_embed_grad(const EmbedGradArgs &a, hipStream_t s) {
   so.from = pb;
   so.to = pa;
   so.counts = reinterpret_cast<uint32_t *>(a.ws + l.counts);
-  so.present = reinterpret_cast<uint32_t *>(a.ws + l.present);
+  so.crossing = reinterpret_cast<uint32_t *>(a.ws + l.crossing);
   so.n_rows = a.n_rows;
   so.padding_id = a.padding_id;
   so.n = (uint32_t)a.n_ids;
@@ -463,13 +519,24 @@ hipError_t launch_embed_grad(const EmbedGradArgs &a, hipStream_t s) {
   const uint32_t passes = (total_bits + kDigitBits - 1) / kDigitBits;
   so.bits = (total_bits + passes - 1) / passes;
   so.shift = 0;
+  // With few tokens for the rows, the sort (one workgroup) hides behind clearing every
+  // row, at the cost of writing the tokens' rows twice; else only rows without tokens
+  // are cleared, by the summing kernel.
+  const bool clear_first = a.n_ids <= kSmallTokens && a.n_ids * 4 <= a.n_rows;
   hipError_t e = hipSuccess;
   const Pair *sorted = pa;
   if (a.n_ids <= kSmallTokens) {
     const uint32_t per = (so.n + kSmallThreads - 1) / kSmallThreads;
     so.per_wave = (per ? per : 1) * kWave;
-    sort_small_kernel<<<1, kSmallThreads, 0, s>>>(so, passes, total_bits);
-    e = hipGetLastError();
+    uint32_t clearers = 0;
+    if (clear_first) {
+      const uint64_t want = (a.n_rows * a.dim + kSmallThreads * 8 - 1) / (kSmallThreads * 8);
+      clearers = (uint32_t)(want < 512 ? want : 512);
+    }
+    e = with_dtype(a.out_dtype, [&](auto d) {
+      sort_small_kernel<d.value><<<1 + clearers, kSmallThreads, 0, s>>>(so, passes, total_bits, a.grad, a.n_rows * a.dim);
+      return hipGetLastError();
+    });
   } else {
     const uint64_t want = (a.n_ids + kSortMin - 1) / kSortMin;
     const uint32_t blocks = (uint32_t)(want < kSortBlocks ? want : kSortBlocks);
@@ -495,8 +562,8 @@ hipError_t launch_embed_grad(const EmbedGradArgs &a, hipStream_t s) {
   SumArgs m;
   m.dout = a.dout;
   m.sorted = sorted;
-  m.present = so.present;
   m.grad = a.grad;
+  m.crossing = so.crossing;
   m.part = reinterpret_cast<float *>(a.ws + l.part);
   m.n_rows = a.n_rows;
   m.n = so.n;
@@ -510,9 +577,10 @@ hipError_t launch_embed_grad(const EmbedGradArgs &a, hipStream_t s) {
   const uint32_t groups = kBlock / m.lanes;
   uint64_t sum_blocks = ((uint64_t)m.nchunks * m.slabs + groups - 1) / groups;
   if (sum_blocks > (1u << 22)) sum_blocks = 1u << 22;
-  const uint64_t zero = (a.n_rows + groups - 1) / groups;
-  const uint64_t zero_blocks = zero < 4096 ? zero : 4096;
-  m.sum_blocks = (uint32_t)sum_blocks;
+  const uint64_t zero = (a.n_rows + kWave - 1) / kWave;
+  const uint64_t zero_blocks = clear_first ? 0 : zero < 8192 ? zero : 8192;
+  m.zero_blocks = (uint32_t)zero_blocks;
+  if (sum_blocks + zero_blocks == 0) return e;  // no tokens, rows cleared
   e = with_dtype(a.in_dtype, [&](auto di) {
     return with_dtype(a.out_dtype, [&](auto dO) {
       grad_sum_kernel<di.value, dO.value><<<(uint32_t)(sum_blocks + zero_blocks), kBlock, 0, s>>>(m);
@@ -520,8 +588,10 @@ hipError_t launch_embed_grad(const EmbedGradArgs &a, hipStream_t s) {
     });
   });
   if (e != hipSuccess || m.nchunks < 2) return e;
+  const uint32_t lanes = m.lanes < 32 ? m.lanes : 32, strips = (a.dim + lanes * 8 - 1) / (lanes * 8);
+  const uint64_t items = (uint64_t)m.nchunks * strips;  // at most
   return with_dtype(a.out_dtype, [&](auto dO) {
-    grad_join_kernel<dO.value><<<m.sum_blocks, kBlock, 0, s>>>(m);
+    grad_join_kernel<dO.value><<<(uint32_t)(items < 1024 ? items : 1024), kBlock, 0, s>>>(m, lanes, strips);
     return hipGetLastError();
   });
 }
