@@ -128,57 +128,43 @@ template <bool A8, int MI> hipError_t go_direct(const MxMatmulArgs &a, hipStream
 
 // ------------------------------------------------------------------ many rows
 
-// A workgroup of WM x WN wavefronts computes 16 FM WM rows of A by 16 FN WN rows of B,
-// operands staged in LDS through the direct global-to-LDS loads, two stages of which one
-// is filled while the other is multiplied.  A stage holds 128 bytes of each row of A:
-// 256 elements of e2m1 (two matrix instructions deep, instruction s takes blocks s,
-// 2 + s, 4 + s, 6 + s) or 128 of e4m3 (one deep), and the same elements of B.
+// A workgroup of WM x WN wavefronts computes 16 FM WM rows of A by 16 FN WN rows of B.
+// Operands go through LDS by the direct global-to-LDS loads, in stages of 128 elements
+// of every row, one matrix instruction deep; kStages of them form a ring, so that while
+// one is multiplied the loads of the next kStages - 1 are in flight (with one stage in
+// flight a stage's multiplication, 0.4 us, does not cover the loads' latency:
+// 8192 x 8192 x 8192 in e2m1 took OLD us against NEW us).
 //
-// LDS rows are 128 or 64 bytes; the 16-byte pieces of a row are permuted by the row
-// number so that the 16 rows which a read takes at one piece fall into all 64 banks.
-// The loads write LDS in lane order, so the permutation is made by the lanes' sources.
+// LDS rows are 128 (e4m3) or 64 bytes (e2m1).  The 16-byte pieces of a row are permuted by
+// the row number, so that eight rows read at one piece lie in different banks: a read
+// takes 4 clocks then, 256 bytes a clock (measured; 8 with (row >> 2) & 3 for 64-byte
+// rows, 8 and 16 with none).  The loads write LDS in lane order, so the lanes' sources
+// make the permutation.
 template <uint32_t PITCH> __device__ __forceinline__ uint32_t swizzle(uint32_t row, uint32_t piece) {
-  return PITCH == 128 ? piece ^ ((row >> 1) & 7) : piece ^ ((row >> 2) & 3);
+  return piece ^ (PITCH == 128 ? row & 7 : (row >> 1) & 3);
 }
 
-// One operand's part of a stage: ROWS rows of PITCH bytes of codes, their scale bytes.
-template <uint32_t ROWS, uint32_t PITCH, uint32_t SCALES, uint32_t WAVES> struct Tile {
-  static constexpr uint32_t kCodes = ROWS * PITCH, kBytes = kCodes + ROWS * SCALES;
-  static constexpr uint32_t kLoads = kCodes / (1024 * WAVES);            // 16 bytes a lane
-  static constexpr uint32_t kScaleLoads = (ROWS * SCALES / 4 + 64 * WAVES - 1) / (64 * WAVES);  // 4 bytes a lane
-
+// One operand's codes of a stage: ROWS rows of PITCH bytes, the loads shared by WAVES wavefronts.
+template <uint32_t ROWS, uint32_t PITCH, uint32_t WAVES> struct Tile {
+  static constexpr uint32_t kBytes = ROWS * PITCH, kLoads = kBytes / (1024 * WAVES);
   const uint8_t *code[kLoads];
   uint32_t at[kLoads];
-  const uint8_t *scale[kScaleLoads];
-  uint32_t scale_at[kScaleLoads];
 
-  __device__ __forceinline__ void init(const uint8_t *codes, const uint8_t *scales, uint64_t row0, uint64_t rows,
-                                       uint32_t cp, uint32_t sp, uint32_t wave, uint32_t lane) {
+  __device__ __forceinline__ void init(const uint8_t *codes, uint64_t row0, uint64_t rows, uint32_t cp, uint32_t wave,
+                                       uint32_t lane) {
 #pragma unroll
     for (uint32_t i = 0; i < kLoads; ++i) {
       const uint32_t slot = (i * WAVES + wave) * 64 + lane, row = slot / (PITCH / 16);
-      const uint64_t r = row0 + row < rows ? row0 + row : rows - 1;
+      const uint64_t r = row0 + row < rows ? row0 + row : rows - 1;  // results of rows past the end are not stored
       at[i] = swizzle<PITCH>(row, slot % (PITCH / 16)) * 16;
-      code[i] = codes + r * cp;
-    }
-#pragma unroll
-    for (uint32_t i = 0; i < kScaleLoads; ++i) {
-      const uint32_t slot = (i * WAVES + wave) * 64 + lane, row = slot / (SCALES / 4);
-      const uint64_t r = row0 + row < rows ? row0 + row : rows - 1;
-      scale_at[i] = slot % (SCALES / 4) * 4;
-      scale[i] = scales + r * sp;
+      code[i] = codes + r * cp + at[i];
     }
   }
-
-  // Fills the tile with its rows' bytes from `k` (codes) and `b` (scales) on, zeros past the rows' ends.
-  __device__ __forceinline__ void load(uint8_t *lds, uint32_t k, uint32_t cp, uint32_t b, uint32_t sp, uint32_t wave) {
+  // The rows' bytes from k on, zeros past the rows' ends.
+  __device__ __forceinline__ void load(uint8_t *lds, uint32_t k, uint32_t cp, uint32_t wave) {
 #pragma unroll
     for (uint32_t i = 0; i < kLoads; ++i)
-      to_lds16(k + at[i] < cp ? code[i] + k + at[i] : kZeros, lds + (i * WAVES + wave) * 1024);
-#pragma unroll
-    for (uint32_t i = 0; i < kScaleLoads; ++i)
-      if ((i * WAVES + wave) * 256 < ROWS * SCALES)
-        to_lds4(b + scale_at[i] < sp ? scale[i] + b + scale_at[i] : kZeros, lds + kCodes + (i * WAVES + wave) * 256);
+      to_lds16(k + at[i] < cp ? code[i] + k : kZeros, lds + (i * WAVES + wave) * 1024);
   }
 };
 
@@ -186,12 +172,17 @@ template <bool A8, int WM, int WN, int FM, int FN, int DO>
 __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, uint32_t tiles_m, uint32_t tiles_n) {
   using TO = typename Num<DO>::T;
   constexpr uint32_t kWaves = WM * WN, kRowsA = 16 * FM * WM, kRowsB = 16 * FN * WN;
-  constexpr uint32_t kPitchA = 128, kPitchB = A8 ? 64 : 128, kBlocks = A8 ? 4 : 8;
-  constexpr int kDeep = A8 ? 1 : 2;
-  using TileA = Tile<kRowsA, kPitchA, kBlocks, kWaves>;
-  using TileB = Tile<kRowsB, kPitchB, kBlocks, kWaves>;
-  constexpr uint32_t kStage = TileA::kBytes + TileB::kBytes;
-  __shared__ __align__(1024) uint8_t stages[2 * kStage];
+  constexpr uint32_t kPitchA = A8 ? 128 : 64, kPitchB = 64, kBlocks = 4;
+  using TileA = Tile<kRowsA, kPitchA, kWaves>;
+  using TileB = Tile<kRowsB, kPitchB, kWaves>;
+  static_assert(kRowsA + kRowsB == 64 * kWaves, "a wavefront loads the scale dwords of 64 rows");
+  constexpr uint32_t kStage = TileA::kBytes + TileB::kBytes, kStages = A8 ? 3 : 4;
+  constexpr uint32_t kLoads = TileA::kLoads + TileB::kLoads;  // a wavefront's loads per stage
+  // Scales come for kGroup stages at a time, 16 bytes of each row of A, then of B: a dword
+  // a stage would ask L2 for a line per row and stage, as many requests as the codes.
+  constexpr uint32_t kGroup = 4, kRows = kRowsA + kRowsB, kScales = kRows * 16;
+  static_assert(kStages * kStage + 2 * kScales <= 160 * 1024 && (kStages - 2) * kLoads < 16, "");
+  __shared__ __align__(1024) uint8_t ring[kStages * kStage + 2 * kScales];
   const uint32_t lane = lane_id(), wave = uniform(threadIdx.x / kWave), r = lane & 15, g = lane >> 4;
   const TileId t = tile_of(blockIdx.x, tiles_m, tiles_n);
   const uint64_t m0 = (uint64_t)t.row * kRowsA, n0 = (uint64_t)t.col * kRowsB;
@@ -200,8 +191,15 @@ __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, uin
   const uint32_t cpa = (uint32_t)mx_code_pitch(a.K, A8), cpb = (uint32_t)mx_code_pitch(a.K, false);
   TileA ta;
   TileB tb;
-  ta.init(a.a_codes, a.a_scales, m0, a.M, cpa, sp, wave, lane);
-  tb.init(a.b_codes, a.b_scales, n0, a.N, cpb, sp, wave, lane);
+  ta.init(a.a_codes, m0, a.M, cpa, wave, lane);
+  tb.init(a.b_codes, n0, a.N, cpb, wave, lane);
+  const uint8_t *scale;
+  {
+    const uint32_t row = wave * 64 + lane;
+    const bool of_a = row < kRowsA;
+    const uint64_t at = of_a ? m0 + row : n0 + row - kRowsA, rows = of_a ? a.M : a.N;
+    scale = (of_a ? a.a_scales : a.b_scales) + (at < rows ? at : rows - 1) * sp;
+  }
   const uint32_t wm = (wave % WM) * 16 * FM, wn = (wave / WM) * 16 * FN;
   v4f acc[FN][FM];
 #pragma unroll
@@ -210,70 +208,148 @@ __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, uin
     for (int m = 0; m < FM; ++m) acc[n][m] = v4f{0, 0, 0, 0};
 
   const uint32_t steps = (nblk + kBlocks - 1) / kBlocks;
+  // Always kLoads loads, of zeros past the last stage: the waits below count on it.
   auto fill = [&](uint8_t *st, uint32_t k) {
-    ta.load(st, k * kPitchA, cpa, k * kBlocks, sp, wave);
-    tb.load(st + TileA::kBytes, k * kPitchB, cpb, k * kBlocks, sp, wave);
+    ta.load(st, k * kPitchA, cpa, wave);
+    tb.load(st + TileA::kBytes, k * kPitchB, cpb, wave);
   };
-  auto multiply = [&](const uint8_t *st) {
-    const uint8_t *sa = st, *sb = st + TileA::kBytes;
-    int xs[FM], ws[FN];
+  // Scales of group q, 16 bytes a row; where the rows end inside, their last dwords come
+  // through registers with zeros after them (a neighbour's scale may be NaN).
+  auto fill_scales = [&](uint8_t *sc, uint32_t q) {
+    if ((q + 1) * 16 <= sp) {
+      to_lds16(scale + q * 16, sc + wave * 1024);
+    } else {
+      uint32_t d[kGroup];
 #pragma unroll
-    for (int m = 0; m < FM; ++m) {
-      const uint8_t *p = sa + TileA::kCodes + (wm + 16 * m + r) * kBlocks + g * kDeep;
-      xs[m] = A8 ? *p : *reinterpret_cast<const uint16_t *>(p);
+      for (uint32_t j = 0; j < kGroup; ++j)
+        d[j] = q * 16 + j * 4 < sp ? *reinterpret_cast<const uint32_t *>(scale + q * 16 + j * 4) : 0u;
+      *reinterpret_cast<uint4 *>(sc + wave * 1024 + lane * 16) = make_uint4(d[0], d[1], d[2], d[3]);
     }
-#pragma unroll
-    for (int n = 0; n < FN; ++n) {
-      const uint8_t *p = sb + TileB::kCodes + (wn + 16 * n + r) * kBlocks + g * kDeep;
-      ws[n] = A8 ? *p : *reinterpret_cast<const uint16_t *>(p);
-    }
+  };
+  v8i w[FN], v[FM];
+  int ws[FN], xs[FM];
+  // a fragment's rows are 16 apart and its permutation goes by r alone: one address, then offsets
+  const uint32_t at_a = (wm + r) * kPitchA + swizzle<kPitchA>(r, g) * 16;
+  const uint32_t at_a2 = (wm + r) * kPitchA + swizzle<kPitchA>(r, 4 + g) * 16;  // e4m3: blocks 2 and 3
+  const uint32_t at_b = (wn + r) * kPitchB + swizzle<kPitchB>(r, g) * 16;
+  auto read = [&](const uint8_t *st, const uint8_t *sc) {
     const uint4 none = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-    for (int d = 0; d < kDeep; ++d) {
-      v8i w[FN];
+    for (int n = 0; n < FN; ++n) {
+      w[n] = operand(*reinterpret_cast<const uint4 *>(st + TileA::kBytes + at_b + n * 16 * kPitchB), none);
+      ws[n] = sc[(kRowsA + wn + r) * 16 + g + n * 256];
+    }
 #pragma unroll
-      for (int n = 0; n < FN; ++n) {
-        const uint32_t row = wn + 16 * n + r;
-        w[n] = operand(*reinterpret_cast<const uint4 *>(sb + row * kPitchB + swizzle<kPitchB>(row, g * kDeep + d) * 16), none);
-      }
-#pragma unroll
-      for (int m = 0; m < FM; ++m) {
-        const uint32_t row = wm + 16 * m + r;
-        v8i v;
-        if constexpr (A8)
-          v = operand(*reinterpret_cast<const uint4 *>(sa + row * kPitchA + swizzle<kPitchA>(row, g) * 16),
-                      *reinterpret_cast<const uint4 *>(sa + row * kPitchA + swizzle<kPitchA>(row, 4 + g) * 16));
-        else
-          v = operand(*reinterpret_cast<const uint4 *>(sa + row * kPitchA + swizzle<kPitchA>(row, g * 2 + d) * 16), none);
-#pragma unroll
-        for (int n = 0; n < FN; ++n) acc[n][m] = mfma_mx<A8>(w[n], v, acc[n][m], ws[n], xs[m], d);
-      }
+    for (int m = 0; m < FM; ++m) {
+      v[m] = operand(*reinterpret_cast<const uint4 *>(st + at_a + m * 16 * kPitchA),
+                     A8 ? *reinterpret_cast<const uint4 *>(st + at_a2 + m * 16 * kPitchA) : none);
+      xs[m] = sc[(wm + r) * 16 + g + m * 256];
     }
   };
-  // The two stages do not overlap; __restrict__ says so to the compiler, which otherwise
-  // would wait for the loads in flight before every LDS read.
-  auto both = [&](uint8_t *__restrict__ next, const uint8_t *__restrict__ now, uint32_t k) {
-    if (k < steps) fill(next, k);
-    multiply(now);
+  uint8_t *const scales = ring + kStages * kStage;
+  auto barrier = [&] {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
   };
-  // the loads of a stage are waited for, then all wavefronts know that it is full and that the other is free
-  auto ready = [&] {
-    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
-    __syncthreads();
+  // Each turn of the loop is a reading phase and a multiplying phase with a barrier after
+  // each.  With two wavefronts a SIMD the second half of the wavefronts runs one phase
+  // behind the first (kPingPong), so LDS serves one half while the other multiplies; in
+  // step, all would read at once and the matrix units idle meanwhile.  With four stages
+  // the loads are issued between the matrix instructions (they cost the reading phase,
+  // the longer one, a third of its time); with three they would come too late there.
+  constexpr bool kPingPong = kWaves == 8, kLateFill = kStages >= 4;
+  const bool behind = kPingPong && wave >= kWaves / 2;
+  // vmcnt that leaves `stages` stages' loads in flight, and no LDS access
+  auto wait = [](auto stages) { __builtin_amdgcn_s_waitcnt(0x0070 | (stages.value * kLoads)); };
+  using Two = std::integral_constant<uint32_t, kStages - 2>;
+  using Three = std::integral_constant<uint32_t, kStages - 3>;
+  // What is filled is not what is read; __restrict__ says so to the compiler, which
+  // otherwise would wait for all loads in flight before an LDS read.
+  auto load_phase = [&](uint8_t *__restrict__ next, uint8_t *__restrict__ next_scales, const uint8_t *__restrict__ now,
+                        const uint8_t *__restrict__ now_scales, uint32_t k) {
+    if (!kLateFill) fill(next, k + kStages - 1);
+    if (k % kGroup == 0) fill_scales(next_scales, k / kGroup + 1);
+    read(now, now_scales);
   };
-  if (steps) fill(stages, 0);
+#pragma unroll
+  for (uint32_t k = 0; k + 1 < kStages; ++k) fill(ring + k * kStage, k);
+  fill_scales(scales, 0);
+  __builtin_amdgcn_s_waitcnt(kWaitVmcnt0 & ~0x0F00);  // and LDS writes
+  barrier();
+  if (behind) barrier();
+  uint32_t now = 0, next = kStages - 1;  // ring places of stage k and of stage k - 1, which is filled anew
 #pragma unroll 1
   for (uint32_t k = 0; k < steps; ++k) {
-    ready();
-    both(stages + ((k + 1) & 1) * kStage, stages + (k & 1) * kStage, k + 1);
+    const uint32_t odd = k / kGroup & 1;
+    uint8_t *const free_stage = ring + next * kStage;
+    load_phase(free_stage, scales + (odd ^ 1) * kScales, ring + now * kStage, scales + odd * kScales + k % kGroup * 4, k);
+    next = now;
+    now = now + 1 == kStages ? 0 : now + 1;
+    // Before the barrier after which stage k + 1 is read by the first half, every wavefront
+    // has waited for its loads of that stage: the half behind in its reading phase, the
+    // first half in its multiplying phase (loads of scales in between make a wait longer,
+    // never shorter, and are kGroup stages early).
+    if constexpr (!kLateFill) wait(Two{});
+    else if (behind) wait(Three{});
+    else __builtin_amdgcn_s_waitcnt(0xC07F);  // LDS reads only
+    barrier();
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int m = 0; m < FM; ++m) {
+#pragma unroll
+      for (int n = 0; n < FN; ++n) acc[n][m] = mfma_mx<A8>(w[n], v[m], acc[n][m], ws[n], xs[m], 0);
+      if (kLateFill && m == 0) {
+        __builtin_amdgcn_sched_barrier(0);  // the compiler would issue the loads first
+        fill(free_stage, k + kStages - 1);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(0);
+    if constexpr (kLateFill)
+      if (!behind) wait(Two{});
+    barrier();
   }
+  if (kPingPong && wave < kWaves / 2) barrier();
+  __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);  // no load into LDS outlives the workgroup
+  // Results go through LDS, two fragments' rows at a time, so that a store covers whole
+  // lines of y (from the fragments themselves a row gets 32 bytes at a time).
+  __syncthreads();
+  constexpr uint32_t kCols = 16 * FN, kPad = 16 / sizeof(TO), kEach = 16 / sizeof(TO);
+  constexpr uint32_t kOutRows = 32, kPieces = kOutRows * kCols / kEach / 64;
+  static_assert(kWaves * kOutRows * (kCols + kPad) * sizeof(TO) <= sizeof(ring), "");
+  TO *const out = reinterpret_cast<TO *>(ring) + wave * kOutRows * (kCols + kPad);
   TO *y = static_cast<TO *>(a.y);
+  typedef TO Aligned __attribute__((ext_vector_type(kEach)));
+  typedef TO Loose __attribute__((ext_vector_type(kEach), aligned(sizeof(TO))));
+  typedef TO Four __attribute__((ext_vector_type(4)));
 #pragma unroll
-  for (int m = 0; m < FM; ++m) {
-    const uint64_t row = m0 + wm + 16 * m + r;
-    if (row >= a.M) continue;
+  for (int m = 0; m < FM; m += 2) {
+    wave_lds_sync();
 #pragma unroll
-    for (int n = 0; n < FN; ++n) store4<TO>(y + row * a.N, n0 + wn + 16 * n + 4 * g, a.N, acc[n][m]);
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int n = 0; n < FN; ++n) {
+        const v4f x = acc[n][m + h];
+        *reinterpret_cast<Four *>(out + (16 * h + r) * (kCols + kPad) + 16 * n + 4 * g) = Four{(TO)x[0], (TO)x[1], (TO)x[2], (TO)x[3]};
+      }
+    wave_lds_sync();
+#pragma unroll
+    for (uint32_t p = 0; p < kPieces; ++p) {
+      const uint32_t slot = p * 64 + lane, row = slot / (kCols / kEach), c = slot % (kCols / kEach) * kEach;
+      const uint64_t gm = m0 + wm + 16 * m + row, gn = n0 + wn + c;
+      if (gm >= a.M || gn >= a.N) continue;
+      const Aligned x = *reinterpret_cast<const Aligned *>(out + row * (kCols + kPad) + c);
+      if (gn + kEach <= a.N) {
+        *reinterpret_cast<Loose *>(y + gm * a.N + gn) = x;
+      } else {
+#pragma unroll
+        for (uint32_t e = 0; e < kEach; ++e)
+          if (gn + e < a.N) y[gm * a.N + gn + e] = x[e];
+      }
+    }
   }
 }
 
