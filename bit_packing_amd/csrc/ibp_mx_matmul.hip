@@ -22,15 +22,9 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 
 constexpr uint32_t kStep = 16;  // blocks per step of the direct kernel: 512 elements
 
-template <bool A8> __device__ __forceinline__ v4f mfma_mx(v8i w, v8i x, v4f acc, int ws, int xs, int sel) {
-  // format codes: 0 e4m3, 4 e2m1; sel: which byte of the scale words
-  constexpr int fx = A8 ? 0 : 4;
-  switch (sel) {
-    case 0: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, acc, 4, fx, 0, ws, 0, xs);
-    case 1: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, acc, 4, fx, 1, ws, 1, xs);
-    case 2: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, acc, 4, fx, 2, ws, 2, xs);
-    default: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, acc, 4, fx, 3, ws, 3, xs);
-  }
+// Scales are the low bytes of ws and xs; format codes: 0 e4m3, 4 e2m1.
+template <bool A8> __device__ __forceinline__ v4f mfma_mx(v8i w, v8i x, v4f acc, int ws, int xs) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, acc, 4, A8 ? 0 : 4, 0, ws, 0, xs);
 }
 
 // A 16-byte piece of a row, zero from byte `pitch` on.
@@ -42,11 +36,24 @@ __device__ __forceinline__ v8i operand(uint4 lo, uint4 hi) {
   return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
 }
 
+// 16 scale bytes of a row from block b on, zeros past its end.
+__device__ __forceinline__ uint4 scales16(const uint8_t *row, uint32_t b, uint32_t pitch) {
+  typedef uint32_t V __attribute__((ext_vector_type(4), aligned(4)));
+  V v = {};
+  if (b + 16 <= pitch) {
+    v = *reinterpret_cast<const V *>(row + b);
+  } else {
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j)
+      if (b + 4 * j < pitch) v[j] = *reinterpret_cast<const uint32_t *>(row + b + 4 * j);
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
 // Few rows of A: bound by the weights' bytes.  A workgroup computes 16 MI x 16 outputs,
 // its wavefronts take the steps of k in turn and their sums are added in order through
-// LDS.  A step covers 16 blocks, four matrix instructions of which instruction s takes
-// blocks s, 4 + s, 8 + s, 12 + s (the sum over k may take its blocks in any order), so
-// lane group g's weights are 64 consecutive bytes and its scales one dword.
+// LDS.  A step is 16 blocks, four matrix instructions; each load takes 64 consecutive
+// bytes of 16 rows.
 template <bool A8, int MI, int DO> __global__ void mx_direct_kernel(MxMatmulArgs a) {
   using TO = typename Num<DO>::T;
   extern __shared__ float red[];
@@ -69,27 +76,28 @@ template <bool A8, int MI, int DO> __global__ void mx_direct_kernel(MxMatmulArgs
 #pragma unroll
   for (int i = 0; i < MI; ++i) acc[i] = v4f{0, 0, 0, 0};
   for (uint32_t b0 = wave * kStep; b0 < nblk; b0 += waves * kStep) {
-    const uint32_t sb = b0 + 4 * g;
-    uint4 w[4];
+    uint4 w[4], lo[MI][4], hi[MI][4];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) w[s] = piece(wc, (sb + s) * 16, wp);
-    const int ws = sb < sp ? *reinterpret_cast<const int *>(wsc + sb) : 0;
-    int xs[MI];
-#pragma unroll
-    for (int i = 0; i < MI; ++i) xs[i] = sb < sp ? *reinterpret_cast<const int *>(xsc[i] + sb) : 0;
+    for (int s = 0; s < 4; ++s) w[s] = piece(wc, (b0 + 4 * s + g) * 16, wp);
+    const uint4 wsc4 = scales16(wsc, b0, sp);
+    uint4 xsc4[MI];
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
+      xsc4[i] = scales16(xsc[i], b0, sp);
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        uint4 lo, hi = make_uint4(0u, 0u, 0u, 0u);
-        if constexpr (A8) {
-          lo = piece(xc[i], (b0 + 4 * (g >> 1) + s) * 32 + 16 * (g & 1), xp);
-          hi = piece(xc[i], (b0 + 4 * (2 + (g >> 1)) + s) * 32 + 16 * (g & 1), xp);
-        } else {
-          lo = piece(xc[i], (sb + s) * 16, xp);
-        }
-        acc[i] = mfma_mx<A8>(operand(w[s], make_uint4(0u, 0u, 0u, 0u)), operand(lo, hi), acc[i], ws, xs[i], s);
+        lo[i][s] = piece(xc[i], A8 ? (b0 + 4 * s) * 32 + 16 * g : (b0 + 4 * s + g) * 16, xp);
+        hi[i][s] = A8 ? piece(xc[i], (b0 + 4 * s) * 32 + 64 + 16 * g, xp) : make_uint4(0u, 0u, 0u, 0u);
       }
+    }
+    const uint32_t wd[4] = {wsc4.x, wsc4.y, wsc4.z, wsc4.w};
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const uint32_t xd[4] = {xsc4[i].x, xsc4[i].y, xsc4[i].z, xsc4[i].w};
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        acc[i] = mfma_mx<A8>(operand(w[s], make_uint4(0u, 0u, 0u, 0u)), operand(lo[i][s], hi[i][s]), acc[i],
+                             (int)(wd[s] >> (8 * g)), (int)(xd[s] >> (8 * g)));
     }
   }
   if (waves > 1) {
@@ -128,7 +136,8 @@ template <bool A8, int MI> hipError_t go_direct(const MxMatmulArgs &a, hipStream
 
 // ------------------------------------------------------------------ many rows
 
-// A workgroup of WM x WN wavefronts computes 16 FM WM rows of A by 16 FN WN rows of B.
+// A workgroup of WM x WN wavefronts computes 16 FM WM rows of A by 16 FN WN rows of B over
+// stages_each stages of k, from blockIdx.y * stages_each on, into dst + blockIdx.y * M * N.
 // Operands go through LDS by the direct global-to-LDS loads, in stages of 128 elements
 // of every row, one matrix instruction deep; kStages of them form a ring, so that while
 // one is multiplied the loads of the next kStages - 1 are in flight (with one stage in
@@ -169,7 +178,8 @@ template <uint32_t ROWS, uint32_t PITCH, uint32_t WAVES> struct Tile {
 };
 
 template <bool A8, int WM, int WN, int FM, int FN, int DO>
-__global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, uint32_t tiles_m, uint32_t tiles_n) {
+__global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, void *dst, uint32_t tiles_m,
+                                                             uint32_t tiles_n, uint32_t stages_each) {
   using TO = typename Num<DO>::T;
   constexpr uint32_t kWaves = WM * WN, kRowsA = 16 * FM * WM, kRowsB = 16 * FN * WN;
   constexpr uint32_t kPitchA = A8 ? 128 : 64, kPitchB = 64, kBlocks = 4;
@@ -207,15 +217,19 @@ __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, uin
 #pragma unroll
     for (int m = 0; m < FM; ++m) acc[n][m] = v4f{0, 0, 0, 0};
 
-  const uint32_t steps = (nblk + kBlocks - 1) / kBlocks;
-  // Always kLoads loads, of zeros past the last stage: the waits below count on it.
-  auto fill = [&](uint8_t *st, uint32_t k) {
+  // stages of this workgroup's range of k, which begins at a whole group of scales
+  const uint32_t all = (nblk + kBlocks - 1) / kBlocks, begin = blockIdx.y * stages_each;
+  const uint32_t steps = all - begin < stages_each ? all - begin : stages_each;
+  // Always kLoads loads, of zeros past the rows' end: the waits below count on it.
+  auto fill = [&](uint8_t *st, uint32_t stage) {
+    const uint32_t k = begin + stage;
     ta.load(st, k * kPitchA, cpa, wave);
     tb.load(st + TileA::kBytes, k * kPitchB, cpb, wave);
   };
   // Scales of group q, 16 bytes a row; where the rows end inside, their last dwords come
   // through registers with zeros after them (a neighbour's scale may be NaN).
-  auto fill_scales = [&](uint8_t *sc, uint32_t q) {
+  auto fill_scales = [&](uint8_t *sc, uint32_t group) {
+    const uint32_t q = begin / kGroup + group;
     if ((q + 1) * 16 <= sp) {
       to_lds16(scale + q * 16, sc + wave * 1024);
     } else {
@@ -300,7 +314,7 @@ __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, uin
 #pragma unroll
     for (int m = 0; m < FM; ++m) {
 #pragma unroll
-      for (int n = 0; n < FN; ++n) acc[n][m] = mfma_mx<A8>(w[n], v[m], acc[n][m], ws[n], xs[m], 0);
+      for (int n = 0; n < FN; ++n) acc[n][m] = mfma_mx<A8>(w[n], v[m], acc[n][m], ws[n], xs[m]);
       if (kLateFill && m == 0) {
         __builtin_amdgcn_sched_barrier(0);  // the compiler would issue the loads first
         fill(free_stage, k + kStages - 1);
@@ -321,7 +335,7 @@ __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, uin
   constexpr uint32_t kOutRows = 32, kPieces = kOutRows * kCols / kEach / 64;
   static_assert(kWaves * kOutRows * (kCols + kPad) * sizeof(TO) <= sizeof(ring), "");
   TO *const out = reinterpret_cast<TO *>(ring) + wave * kOutRows * (kCols + kPad);
-  TO *y = static_cast<TO *>(a.y);
+  TO *y = static_cast<TO *>(dst) + (uint64_t)blockIdx.y * a.M * a.N;
   typedef TO Aligned __attribute__((ext_vector_type(kEach)));
   typedef TO Loose __attribute__((ext_vector_type(kEach), aligned(sizeof(TO))));
   typedef TO Four __attribute__((ext_vector_type(4)));
@@ -353,27 +367,80 @@ __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, uin
   }
 }
 
-template <bool A8, int WM, int WN, int FM, int FN> hipError_t go_tile(const MxMatmulArgs &a, hipStream_t s) {
-  const uint64_t tm = (a.M + 16 * FM * WM - 1) / (16 * FM * WM), tn = (a.N + 16 * FN * WN - 1) / (16 * FN * WN);
-  if (tm * tn > 0x3FFFFF) return hipErrorInvalidValue;
+// Adds the ranges' sums in order.
+template <int DO> __global__ __launch_bounds__(kBlock) void mx_join_kernel(MxMatmulArgs a, uint32_t splits) {
+  using TO = typename Num<DO>::T;
+  const uint64_t n = a.M * a.N;
+  for (uint64_t e = ((uint64_t)blockIdx.x * kBlock + threadIdx.x) * 4; e < n; e += (uint64_t)gridDim.x * kBlock * 4) {
+    v4f s{0, 0, 0, 0};
+    for (uint32_t k = 0; k < splits; ++k) s += load4(a.ws + k * n, e, n);
+    store4<TO>(static_cast<TO *>(a.y), e, n, s);
+  }
+}
+
+// Which kernel, and how often k is cut.
+struct Plan {
+  enum { kDirect, kMiddle, kBig } kind;
+  uint32_t tiles_m, tiles_n, splits, stages_each;
+};
+
+Plan plan_of(uint64_t M, uint64_t N, uint32_t K) {
+  Plan p{Plan::kDirect, 0, 0, 1, 1};
+  // Few rows, or so few outputs that one round of the direct kernel's workgroups covers
+  // them (8192 x 8192 weights: 16 rows 13 us against 15 for the tiles, 32 rows 21 against 15).
+  if (M <= 16 || ((M + 15) / 16) * ((N + 15) / 16) <= 512) return p;
+  // Many rows: the larger tiles from 192 of them on (1536 x 8192 outputs, 4096 deep: 37 us
+  // against 47; 1024 x 8192, 8192 deep, 128 large tiles: 62 against 56).
+  const bool big = ((M + 255) / 256) * ((N + 255) / 256) >= 192;
+  const uint32_t wide = big ? 256 : 128;
+  p.kind = big ? Plan::kBig : Plan::kMiddle;
+  p.tiles_m = (uint32_t)((M + wide - 1) / wide);
+  p.tiles_n = (uint32_t)((N + wide - 1) / wide);
+  const uint64_t tiles = (uint64_t)p.tiles_m * p.tiles_n;
+  const uint32_t stages = (uint32_t)((mx_blocks(K) + 3) / 4);
+  // One workgroup takes half a microsecond a stage however few there are: k is cut into
+  // ranges of whole scale groups (4 stages), at least 8 stages each, until there is one per
+  // CU (128 x 8192 outputs, 8192 deep: 31.5 us in one range, 19.8 in four).
+  const uint64_t want = big ? 1 : 256 / tiles, most = stages / 8;
+  uint32_t n = (uint32_t)(want < most ? want : most);
+  n = n < 1 ? 1 : (n > 8 ? 8 : n);
+  p.stages_each = ((stages + n - 1) / n + 3) / 4 * 4;
+  if (p.stages_each == 0) p.stages_each = 4;
+  p.splits = stages ? (stages + p.stages_each - 1) / p.stages_each : 1;
+  return p;
+}
+
+template <bool A8, int DO> hipError_t go_tile(const MxMatmulArgs &a, const Plan &p, void *dst, hipStream_t s) {
+  const dim3 grid(p.tiles_m * p.tiles_n, p.splits);
+  if (p.kind == Plan::kBig)
+    mx_tile_kernel<A8, 2, 4, 8, 4, DO><<<grid, 512, 0, s>>>(a, dst, p.tiles_m, p.tiles_n, p.stages_each);
+  else
+    mx_tile_kernel<A8, 2, 2, 4, 4, DO><<<grid, 256, 0, s>>>(a, dst, p.tiles_m, p.tiles_n, p.stages_each);
+  return hipGetLastError();
+}
+
+template <bool A8> hipError_t go(const MxMatmulArgs &a, hipStream_t s) {
+  const Plan p = plan_of(a.M, a.N, a.K);
+  if (p.kind == Plan::kDirect) return go_direct<A8, 1>(a, s);
+  if ((uint64_t)p.tiles_m * p.tiles_n > 0x7FFFFF) return hipErrorInvalidValue;
+  if (p.splits > 1) {
+    const hipError_t e = go_tile<A8, IBP_F32>(a, p, a.ws, s);
+    if (e != hipSuccess) return e;
+  }
   return with_dtype(a.dtype, [&](auto d) {
-    mx_tile_kernel<A8, WM, WN, FM, FN, d.value>
-        <<<(uint32_t)(tm * tn), WM * WN * kWave, 0, s>>>(a, (uint32_t)tm, (uint32_t)tn);
+    if (p.splits == 1) return go_tile<A8, d.value>(a, p, a.y, s);
+    const uint64_t n = (a.M * a.N + kBlock * 4 - 1) / (kBlock * 4);
+    mx_join_kernel<d.value><<<(uint32_t)(n < 4096 ? n : 4096), kBlock, 0, s>>>(a, p.splits);
     return hipGetLastError();
   });
 }
 
-template <bool A8> hipError_t go(const MxMatmulArgs &a, hipStream_t s) {
-  const uint64_t big = ((a.M + 255) / 256) * ((a.N + 255) / 256), mid = ((a.M + 127) / 128) * ((a.N + 127) / 128);
-  if (a.M <= 16) return go_direct<A8, 1>(a, s);
-  if (big >= 192) return go_tile<A8, 2, 4, 8, 4>(a, s);
-  if (mid >= 64) return go_tile<A8, 2, 2, 4, 4>(a, s);
-  return go_direct<A8, 4>(a, s);
-}
-
 }  // namespace
 
-uint64_t mx_matmul_workspace(uint64_t, uint64_t, uint32_t, bool) { return 0; }
+uint64_t mx_matmul_workspace(uint64_t M, uint64_t N, uint32_t K, bool) {
+  const Plan p = plan_of(M, N, K);
+  return p.splits > 1 ? p.splits * M * N * 4 : 0;
+}
 
 hipError_t launch_mx_matmul(const MxMatmulArgs &a, hipStream_t s) {
   return a.a_e4m3 ? go<true>(a, s) : go<false>(a, s);
