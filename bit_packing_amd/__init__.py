@@ -87,22 +87,49 @@ class ibp_mx_t(ctypes.Structure):
                 ("cols", ctypes.c_uint64), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
-@dataclass
 class MxTensor:
     """A microscaled tensor of rows x cols elements: uint8 codes [rows, ibp_mx_codes_pitch]
     and scale bytes [rows, ibp_mx_scales_pitch] on the device."""
-    codes: torch.Tensor
-    scales: torch.Tensor
-    rows: int
-    cols: int
-    format: int
+    __slots__ = ("rows", "cols", "format", "_codes", "_scales", "_both")
+
+    def __init__(self, codes: torch.Tensor | None, scales: torch.Tensor | None, rows: int, cols: int, format: int,
+                 both: torch.Tensor | None = None):
+        self.rows, self.cols, self.format = rows, cols, format
+        # tensors made here share one allocation, scales behind the codes; views of it are
+        # made when asked for (the calls need the addresses alone)
+        self._codes, self._scales, self._both = codes, scales, both
+
+    def __repr__(self):
+        return f"MxTensor({self.rows} x {self.cols}, {'e4m3' if self.format == IBP_MX_E4M3 else 'e2m1'})"
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            pitch = _mx_pitches(self.cols, self.format)[0]
+            self._codes = self._both[: self.rows * pitch].view(self.rows, pitch)
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            codes, scales = _mx_pitches(self.cols, self.format)
+            self._scales = self._both[self.rows * codes:].view(self.rows, scales)
+        return self._scales
+
+    @property
+    def device(self) -> torch.device:
+        return _device(self._both if self._both is not None else self._codes)
 
     def struct(self) -> ibp_mx_t:
+        rows, cols = self.rows, self.cols
+        codes, scales = _mx_pitches(cols, self.format)
+        if self._both is not None:
+            at = self._both.data_ptr()
+            return ibp_mx_t(self.format, 0, rows, cols, at, at + rows * codes)
         # the C side sees pointers only: the tensors must hold what the shape says
-        codes, scales = _mx_pitches(self.cols, self.format)
-        if _nbytes(self.codes) < self.rows * codes or _nbytes(self.scales) < self.rows * scales:
+        if _nbytes(self._codes) < rows * codes or _nbytes(self._scales) < rows * scales:
             raise ValueError("codes or scales are smaller than their shape needs")
-        return ibp_mx_t(self.format, 0, self.rows, self.cols, _ptr(self.codes), _ptr(self.scales))
+        return ibp_mx_t(self.format, 0, rows, cols, _ptr(self._codes), _ptr(self._scales))
 
 
 def _mx_pitches(cols: int, format: int) -> tuple[int, int]:
@@ -556,7 +583,7 @@ def _matrix(x: torch.Tensor) -> tuple[int, int]:
 def _out(out: torch.Tensor | None, shape, dtype, device) -> torch.Tensor:
     """A new tensor, or the caller's after a check of its shape and dtype."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)
     if tuple(out.shape) != tuple(shape) or out.dtype != dtype:
         raise ValueError(f"the output is {tuple(out.shape)} {out.dtype}, not {tuple(shape)} {dtype}")
     return out
@@ -624,8 +651,8 @@ def ibp_embedding_grad_workspace_bytes(n_rows: int, n_ids: int, dim: int) -> int
 def make_mx(rows: int, cols: int, format: int, device) -> MxTensor:
     """An MxTensor of unwritten codes and scales."""
     codes, scales = _mx_pitches(cols, format)
-    return MxTensor(torch.empty((rows, codes), dtype=torch.uint8, device=device),
-                    torch.empty((rows, scales), dtype=torch.uint8, device=device), rows, cols, format)
+    return MxTensor(None, None, rows, cols, format,
+                    torch.empty(rows * (codes + scales), dtype=torch.uint8, device=device))
 
 
 def _mx(m: MxTensor | None, rows: int, cols: int, format: int, device) -> MxTensor:
@@ -649,7 +676,7 @@ def ibp_mx_pack(x: torch.Tensor, format: int, out: MxTensor | None = None, strea
 
 def ibp_mx_unpack(m: MxTensor, dtype=torch.bfloat16, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The values [rows, cols] of a packed tensor."""
-    out = _out(out, (m.rows, m.cols), dtype, _device(m.codes))
+    out = _out(out, (m.rows, m.cols), dtype, m.device)
     _check(load_library().ibp_mx_unpack(ctypes.byref(m.struct()), _ptr(out), _dtype(out.dtype), _stream(stream)),
            "ibp_mx_unpack")
     return out
@@ -663,7 +690,7 @@ def ibp_mx_swiglu(gate: torch.Tensor, up: torch.Tensor, h: torch.Tensor | None =
         raise ValueError("gate and up differ in shape or dtype")
     rows, cols = _matrix(gate)
     dev = _device(gate)
-    h = _out(h, gate.shape, gate.dtype, dev)
+    h = torch.empty_like(gate) if h is None else _out(h, gate.shape, gate.dtype, dev)
     gate8, up8 = _mx(gate8, rows, cols, IBP_MX_E4M3, dev), _mx(up8, rows, cols, IBP_MX_E4M3, dev)
     rc = load_library().ibp_mx_swiglu(_ptr(gate), _ptr(up), _dtype(gate.dtype), _ptr(h),
                                       ctypes.byref(gate8.struct()), ctypes.byref(up8.struct()), _stream(stream))
@@ -677,7 +704,8 @@ def ibp_mx_swiglu_backward(dh: torch.Tensor, gate8: MxTensor, up8: MxTensor, dga
     if _matrix(dh) != (gate8.rows, gate8.cols) and dh.numel():
         raise ValueError("dh and the checkpoints differ in shape")
     dev = _device(dh)
-    dgate, dup = _out(dgate, dh.shape, dh.dtype, dev), _out(dup, dh.shape, dh.dtype, dev)
+    dgate = torch.empty_like(dh) if dgate is None else _out(dgate, dh.shape, dh.dtype, dev)
+    dup = torch.empty_like(dh) if dup is None else _out(dup, dh.shape, dh.dtype, dev)
     rc = load_library().ibp_mx_swiglu_backward(_ptr(dh), _dtype(dh.dtype), ctypes.byref(gate8.struct()),
                                                ctypes.byref(up8.struct()), _ptr(dgate), _ptr(dup), _stream(stream))
     _check(rc, "ibp_mx_swiglu_backward")
@@ -693,7 +721,7 @@ def _workspace(workspace: torch.Tensor | None, need: int, device) -> torch.Tenso
 def ibp_mx_matmul(a: MxTensor, b: MxTensor, dtype=torch.bfloat16, out: torch.Tensor | None = None,
                   workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """[a.rows, b.rows] product of packed a with packed 4-bit b, both along their columns."""
-    lib, dev = load_library(), _device(a.codes)
+    lib, dev = load_library(), a.device
     out = _out(out, (a.rows, b.rows), dtype, dev)
     workspace = _workspace(workspace, int(lib.ibp_mx_matmul_workspace_bytes(a.rows, b.rows, a.cols, a.format)), dev)
     rc = lib.ibp_mx_matmul(ctypes.byref(a.struct()), ctypes.byref(b.struct()), _ptr(out), _dtype(out.dtype),
