@@ -62,7 +62,7 @@ template <int DI, int DO> __global__ __launch_bounds__(kBlock) void lookup_kerne
 #pragma unroll
       for (uint32_t k = 0; k < kRowsEach; ++k) {
         if (!live[k]) continue;
-        F8 y = widen<TI>(x[k]);
+        F8 y = widen<TI>(x[k], c, a.dim);
 #pragma unroll
         for (int i = 0; i < 8; ++i) y.v[i] = ok[k] ? y.v[i] * a.scale : 0.0f;
         store8<TO>(out + (j0 + (uint64_t)k * w.rows_blk) * a.dim, c, a.dim, y);
@@ -358,7 +358,7 @@ template <typename TI, typename TO> __device__ __forceinline__ void sum_chunk(co
         acc = F8{};
         key = p[k].key;
       }
-      const F8 y = widen<TI>(x[k]);
+      const F8 y = widen<TI>(x[k], c, a.dim);
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc.v[e] += y.v[e];
     }
@@ -440,8 +440,9 @@ template <int DO> __global__ __launch_bounds__(kBlock) void grad_join_kernel(Sum
 #pragma unroll
       for (uint32_t k = 0; k < kFlight; ++k)
         if (p + k < p1) {
+          const F8 y = widen<float>(x[k], c, a.dim);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc.v[e] += x[k][e];
+          for (int e = 0; e < 8; ++e) acc.v[e] += y.v[e];
         }
     }
 #pragma unroll

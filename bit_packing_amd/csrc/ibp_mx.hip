@@ -113,7 +113,7 @@ template <int D, bool E4M3, uint32_t R> __global__ __launch_bounds__(kBlock) voi
     for (uint32_t k = 0; k < R; ++k) x[k] = load8<T>(in + p.row[k] * a.cols, p.c, a.cols);
 #pragma unroll
     for (uint32_t k = 0; k < R; ++k)
-      encode_lane<E4M3>(widen<T>(x[k]), a.codes + p.row[k] * cp, a.scales + p.row[k] * sp, p.c, nblk, p.ok[k]);
+      encode_lane<E4M3>(widen<T>(x[k], p.c, a.cols), a.codes + p.row[k] * cp, a.scales + p.row[k] * sp, p.c, nblk, p.ok[k]);
   }
 }
 
@@ -154,7 +154,7 @@ template <int D, uint32_t R> __global__ __launch_bounds__(kBlock) void mx_swiglu
     }
 #pragma unroll
     for (uint32_t k = 0; k < R; ++k) {
-      const F8 g = widen<T>(vg[k]), u = widen<T>(vu[k]);
+      const F8 g = widen<T>(vg[k], p.c, a.cols), u = widen<T>(vu[k], p.c, a.cols);
       encode_lane<true>(g, a.codes + p.row[k] * cp, a.scales + p.row[k] * sp, p.c, nblk, p.ok[k]);
       encode_lane<true>(u, a.codes2 + p.row[k] * cp, a.scales2 + p.row[k] * sp, p.c, nblk, p.ok[k]);
       F8 o;
@@ -189,7 +189,7 @@ template <int D, uint32_t R> __global__ __launch_bounds__(kBlock) void mx_swiglu
 #pragma unroll
     for (uint32_t k = 0; k < R; ++k) {
       if (!p.ok[k]) continue;
-      const F8 g = mx_decode<true>(qg[k], sg[k]), u = mx_decode<true>(qu[k], su[k]), d = widen<T>(vd[k]);
+      const F8 g = mx_decode<true>(qg[k], sg[k]), u = mx_decode<true>(qu[k], su[k]), d = widen<T>(vd[k], p.c, a.cols);
       F8 og, ou;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {

@@ -23,21 +23,50 @@ template <typename T> using Vec8 = typename VecOf<T>::type;
 
 struct F8 { float v[8]; };
 
-// Elements [c, c + 8) of a row of `cols` elements, zeros past its end, as they lie in
-// memory: widened where they are used, so that the next load need not wait for this one.
-template <typename T> __device__ __forceinline__ Vec8<T> load8(const T *row, uint32_t c, uint32_t cols) {
-  Vec8<T> x = {};
-  if (c + 8 <= cols) {
-    x = *reinterpret_cast<const Vec8<T> *>(row + c);
-  } else {
+// x with its elements moved down by n (1..7), zeros moving in.
+template <typename T> __device__ __forceinline__ Vec8<T> move_down(Vec8<T> x, uint32_t n) {
+  constexpr int W = 2 * sizeof(T);  // dwords
+  uint32_t d[W];
+  __builtin_memcpy(d, &x, sizeof(d));
+  if constexpr (sizeof(T) == 2) {
+    if (n & 1) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < cols) x[i] = row[c + i];
+      for (int i = 0; i < W; ++i) d[i] = (d[i] >> 16) | (i + 1 < W ? d[i + 1] << 16 : 0u);
+    }
+    n >>= 1;
   }
+#pragma unroll
+  for (int k = 1; k < W; k *= 2) {
+    const bool on = n & k;
+#pragma unroll
+    for (int i = 0; i < W; ++i) d[i] = on ? (i + k < W ? d[i + k] : 0u) : d[i];
+  }
+  __builtin_memcpy(&x, d, sizeof(d));
   return x;
 }
 
-template <typename T> __device__ __forceinline__ F8 widen(Vec8<T> x) {
+// Elements [c, c + 8) of a row of `cols` elements are loaded by load8 as they lie in
+// memory, and given zeros past the row's end by settle8 where they are used.  At the
+// row's end load8 takes the row's last eight elements: one load for every lane and no
+// branch, so that no load waits for another (element by element, or with the end's
+// lanes in a branch of their own, each load of a wavefront at the end waited).
+template <typename T> __device__ __forceinline__ Vec8<T> load8(const T *row, uint32_t c, uint32_t cols) {
+  if (cols >= 8) return *reinterpret_cast<const Vec8<T> *>(row + (c + 8 <= cols ? c : cols - 8));
+  Vec8<T> x = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < (int)cols) x[i] = row[i];
+  return x;
+}
+
+template <typename T> __device__ __forceinline__ Vec8<T> settle8(Vec8<T> x, uint32_t c, uint32_t cols) {
+  if (c >= cols) return Vec8<T>{};
+  if (cols >= 8 && c + 8 > cols) return move_down<T>(x, c + 8 - cols);
+  return x;
+}
+
+template <typename T> __device__ __forceinline__ F8 widen(Vec8<T> x, uint32_t c, uint32_t cols) {
+  x = settle8<T>(x, c, cols);
   F8 r;
 #pragma unroll
   for (int i = 0; i < 8; ++i) r.v[i] = (float)x[i];
