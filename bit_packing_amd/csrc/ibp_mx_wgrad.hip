@@ -16,9 +16,10 @@ namespace {
 using namespace dev;
 
 typedef short v4s __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 
-constexpr uint32_t kT = 64;  // tokens per stage
+constexpr uint32_t kT = 32;  // tokens per stage: one matrix instruction deep
 
 // LDS byte of the 16-byte piece `c16` of row t of a tile of W columns.  The 32-byte
 // pieces of a row are permuted by the low bits of t: a transposing read takes 32 bytes
@@ -27,12 +28,12 @@ template <uint32_t W> __device__ __forceinline__ uint32_t tile_at(uint32_t t, ui
   return t * (W * 2) + ((((c16 >> 1) ^ (t & 7)) << 5) | ((c16 & 1) << 4));
 }
 
-// Eight BF16 of column block `col` (16 columns) of 32 rows from `t0` on, in the order of
-// the matrix instruction's k: lane group g takes rows 4 g .. 4 g + 3 and 16 + 4 g ..
-// 16 + 4 g + 3; both operands do, so the sum is over the same tokens.
-template <uint32_t W> __device__ __forceinline__ v8b fragment(const uint8_t *tile, uint32_t t0, uint32_t col, uint32_t lane) {
+// Eight BF16 of column block `col` (16 columns) of a stage, in the order of the matrix
+// instruction's k: lane group g takes rows 4 g .. 4 g + 3 and 16 + 4 g .. 16 + 4 g + 3;
+// both operands do, so the sum is over the same tokens.
+template <uint32_t W> __device__ __forceinline__ v8b fragment(const uint8_t *tile, uint32_t col, uint32_t lane) {
   const uint32_t t = (lane >> 4) * 4 + ((lane & 15) >> 2), sub = (lane & 3) * 8;
-  const uint8_t *at = tile + (t0 + t) * (W * 2) + ((col ^ (t & 7)) << 5) + sub;
+  const uint8_t *at = tile + t * (W * 2) + ((col ^ (t & 7)) << 5) + sub;
   using L = __attribute__((address_space(3))) v4s;
   const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L *)at);
   const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L *)(at + 16 * W * 2));
@@ -40,7 +41,7 @@ template <uint32_t W> __device__ __forceinline__ v8b fragment(const uint8_t *til
 }
 
 // Eight e4m3 codes of one block as BF16, exactly.
-__device__ __forceinline__ v8b decode8(uint2 q, float f) {
+__device__ __forceinline__ v8b decode8(v2u q, float f) {
   typedef __bf16 v2b __attribute__((ext_vector_type(2)));
   const v2b a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q.x, f, false);
   const v2b b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q.x, f, true);
@@ -49,19 +50,31 @@ __device__ __forceinline__ v8b decode8(uint2 q, float f) {
   return v8b{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// A load that the compiler knows to be of global memory: from a pointer chosen between a
+// matrix and kZeros it would make a flat load, which LDS waits count too.
+template <typename T> __device__ __forceinline__ T from_global(const uint8_t *p) {
+  return *reinterpret_cast<const __attribute__((address_space(1))) T *>((uintptr_t)p);
+}
+
 // A workgroup of WI x WO wavefronts computes 16 FI WI (i) by 16 FO WO (o) elements of dW
 // over the tokens [z * t_each, (z + 1) * t_each), z = blockIdx.y, into dst + z * N * K.
-// Two stages in LDS: while one is multiplied, the other's dY comes by direct
-// global-to-LDS loads (DIRECT: rows of dY aligned to 16 bytes) and its X through
-// registers, where it is decoded.
+//
+// Stages of 32 tokens lie in a ring of four.  dY comes by direct global-to-LDS loads three
+// stages ahead where its rows are aligned to 16 bytes (DIRECT), else through registers like
+// X, which is loaded four stages ahead and decoded into LDS two stages ahead.  As in the
+// 4-bit product, half of the eight wavefronts of a large tile read a stage while the other
+// half multiplies (PH us for 16384 x 4096 x 8192 in phases, ST us with all in step and two
+// stages of 64 tokens).
 template <int WI, int WO, int FI, int FO, bool DIRECT, int DO>
 __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *dst, uint64_t t_each, uint32_t tiles_o,
                                                            uint32_t tiles_i) {
   using TO = typename Num<DO>::T;
   constexpr uint32_t kWaves = WI * WO, kThreads = kWaves * 64, kWideI = 16 * FI * WI, kWideO = 16 * FO * WO;
   constexpr uint32_t kPiecesY = kT * kWideO / 8 / kThreads, kPiecesX = kT * kWideI / 8 / kThreads;
-  constexpr uint32_t kBytesY = kT * kWideO * 2, kStage = kBytesY + kT * kWideI * 2;
-  __shared__ __align__(1024) uint8_t stages[2 * kStage];
+  constexpr uint32_t kBytesY = kT * kWideO * 2, kStage = kBytesY + kT * kWideI * 2, kRing = 4;
+  constexpr uint32_t kStepY = kThreads / (kWideO / 8), kStepX = kThreads / (kWideI / 8);  // tokens between a thread's pieces
+  static_assert(kStepY % 8 == 0 && kStepX % 8 == 0, "the permutation goes by t & 7, the same for all pieces of a thread");
+  __shared__ __align__(1024) uint8_t ring[kRing * kStage];
   const uint32_t lane = lane_id(), wave = uniform(threadIdx.x / kWave);
   const TileId tile = tile_of(blockIdx.x, tiles_o, tiles_i);
   const uint32_t o0 = tile.row * kWideO, i0 = tile.col * kWideI;
@@ -70,85 +83,146 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
   const uint32_t cp = (uint32_t)mx_code_pitch(a.K, true), sp = (uint32_t)mx_scale_pitch(a.K);
   const __bf16 *dy = static_cast<const __bf16 *>(a.dy);
 
+  // A thread's pieces lie at one column, so a pointer each for dY, codes and scales walks
+  // over the tokens; past a row's end it stands still on zeros.
+  const uint32_t ty = threadIdx.x / (kWideO / 8), sy = threadIdx.x % (kWideO / 8);
+  const uint32_t tx = threadIdx.x / (kWideI / 8), sx = threadIdx.x % (kWideI / 8), cx = i0 + sx * 8;
+  // LDS takes dY's pieces in lane order; the permutation is made by their sources
+  const uint32_t cy = o0 + ((((sy >> 1) ^ (ty & 7)) << 1) | (sy & 1)) * 8;
+  const bool in_y = !DIRECT || cy < a.N, in_x = cx < cp;
+  // without DIRECT a piece past the row's end is the row's last eight elements (load8)
+  const uint64_t at_y = DIRECT ? cy : (a.N >= 8 ? (cy + 8 <= a.N ? cy : a.N - 8) : 0);
+  const uint8_t *py = in_y ? reinterpret_cast<const uint8_t *>(dy + (t0 + ty) * a.N + at_y) : kZeros;
+  const uint8_t *px = in_x ? a.x_codes + (t0 + tx) * cp + cx : kZeros;
+  const uint8_t *ps = in_x ? a.x_scales + (t0 + tx) * sp + cx / (4 * kMxBlock) * 4 : kZeros;  // its dword
+  const uint32_t scale_shift = cx / kMxBlock % 4 * 8;
+  const uint64_t go_y = in_y ? (uint64_t)kStepY * a.N * 2 : 0, go_x = in_x ? (uint64_t)kStepX * cp : 0;
+  const uint64_t go_s = in_x ? (uint64_t)kStepX * sp : 0;
+  const uint32_t at_x = kBytesY + tile_at<kWideI>(tx, sx);
+
   v4f acc[FI][FO];
 #pragma unroll
   for (int x = 0; x < FI; ++x)
 #pragma unroll
     for (int y = 0; y < FO; ++y) acc[x][y] = v4f{0, 0, 0, 0};
 
-  uint2 qx[kPiecesX];
-  uint32_t sx[kPiecesX];
-  Vec8<__bf16> vy[DIRECT ? 1 : kPiecesY];
-  // starts the loads of the stage that begins at token tb
-  auto fetch = [&](uint8_t *st, uint64_t tb) {
-#pragma unroll
-    for (uint32_t p = 0; p < kPiecesY; ++p) {
-      // LDS takes the pieces in lane order; the permutation is made by their sources
-      const uint32_t slot = p * kThreads + threadIdx.x, t = slot / (kWideO / 8), s16 = slot % (kWideO / 8);
-      const uint32_t c = o0 + ((((s16 >> 1) ^ (t & 7)) << 1) | (s16 & 1)) * 8;
-      if constexpr (DIRECT)
-        to_lds16(tb + t < t1 && c < a.N ? reinterpret_cast<const uint8_t *>(dy + (tb + t) * a.N + c) : kZeros,
-                 st + (p * kWaves + wave) * 1024);
-      else
-        vy[p] = load8<__bf16>(dy + (tb + t < t1 ? tb + t : t1 - 1) * a.N, c, a.N);
-    }
+  // An even number of stages, the last perhaps of zeros: the loop takes two at a time, so
+  // that the two sets of registers of loads in flight are known to the compiler.
+  const uint32_t steps = t0 < t1 ? (uint32_t)((t1 - t0 + 2 * kT - 1) / (2 * kT)) * 2 : 0;
+  const uint32_t tokens = t0 < t1 ? (uint32_t)(t1 - t0) : 0;
+  struct Set {
+    v2u q[kPiecesX];
+    uint32_t s[kPiecesX];
+    Vec8<__bf16> y[DIRECT ? 1 : kPiecesY];
+  } set[2];
+  // Loads of a stage; stages are asked for in order.  Their number never varies (zeros
+  // past the last token), as the waits below count them.
+  auto fetch = [&](Set &f, uint32_t stage) {
 #pragma unroll
     for (uint32_t p = 0; p < kPiecesX; ++p) {
-      const uint32_t slot = p * kThreads + threadIdx.x, t = slot / (kWideI / 8), c = i0 + slot % (kWideI / 8) * 8;
-      const bool in = tb + t < t1 && c < cp;
-      qx[p] = in ? *reinterpret_cast<const uint2 *>(a.x_codes + (tb + t) * cp + c) : make_uint2(0u, 0u);
-      sx[p] = in ? a.x_scales[(tb + t) * sp + c / kMxBlock] : 127u;
+      const bool in = stage * kT + tx + p * kStepX < tokens;
+      f.q[p] = from_global<v2u>(in ? px : kZeros);
+      f.s[p] = from_global<uint32_t>(in ? ps : kZeros);
+      px += go_x;
+      ps += go_s;
     }
-  };
-  // what came through registers goes to LDS
-  auto settle = [&](uint8_t *st, uint64_t tb) {
     if constexpr (!DIRECT) {
 #pragma unroll
       for (uint32_t p = 0; p < kPiecesY; ++p) {
-        const uint32_t slot = p * kThreads + threadIdx.x, t = slot / (kWideO / 8), s16 = slot % (kWideO / 8);
-        const uint32_t c = o0 + ((((s16 >> 1) ^ (t & 7)) << 1) | (s16 & 1)) * 8;
-        *reinterpret_cast<v8b *>(st + slot * 16) = (v8b)settle8<__bf16>(vy[p], tb + t < t1 ? c : a.N, a.N);
-      }
-    }
-#pragma unroll
-    for (uint32_t p = 0; p < kPiecesX; ++p) {
-      const uint32_t slot = p * kThreads + threadIdx.x, t = slot / (kWideI / 8), c16 = slot % (kWideI / 8);
-      *reinterpret_cast<v8b *>(st + kBytesY + tile_at<kWideI>(t, c16)) = decode8(qx[p], mx_factor(sx[p]));
-    }
-  };
-  auto multiply = [&](const uint8_t *st) {
-#pragma unroll
-    for (uint32_t t = 0; t < kT; t += 32) {
-      v8b fy[FO];
-#pragma unroll
-      for (int y = 0; y < FO; ++y) fy[y] = fragment<kWideO>(st, t, wo + y, lane);
-#pragma unroll
-      for (int x = 0; x < FI; ++x) {
-        const v8b fx = fragment<kWideI>(st + kBytesY, t, wi + x, lane);
-#pragma unroll
-        for (int y = 0; y < FO; ++y) acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx, fy[y], acc[x][y], 0, 0, 0);
+        const uint8_t *from = stage * kT + ty + p * kStepY < tokens ? py : kZeros;
+        f.y[p] = a.N >= 8 ? from_global<Vec8<__bf16>>(from) : load8<__bf16>(reinterpret_cast<const __bf16 *>(from), 0, a.N);
+        py += go_y;
       }
     }
   };
-  // the stages do not overlap, which __restrict__ tells the compiler: it would wait for
-  // the loads in flight before every LDS read
-  auto both = [&](uint8_t *__restrict__ next, const uint8_t *__restrict__ now, uint64_t tb) {
-    if (tb < t1) fetch(next, tb);
-    multiply(now);
-    if (tb < t1) settle(next, tb);
+  auto fetch_direct = [&](uint8_t *st, uint32_t stage) {
+    if constexpr (DIRECT) {
+#pragma unroll
+      for (uint32_t p = 0; p < kPiecesY; ++p) {
+        to_lds16(stage * kT + ty + p * kStepY < tokens ? py : kZeros, st + (p * kWaves + wave) * 1024);
+        py += go_y;
+      }
+    }
   };
-  uint32_t cur = 0;
-  if (t0 < t1) {
-    fetch(stages, t0);
-    settle(stages, t0);
+  // what came through registers goes to LDS
+  auto settle = [&](uint8_t *st, const Set &f) {
+    if constexpr (!DIRECT) {
+#pragma unroll
+      for (uint32_t p = 0; p < kPiecesY; ++p)
+        *reinterpret_cast<v8b *>(st + (p * kThreads + threadIdx.x) * 16) = (v8b)settle8<__bf16>(f.y[p], cy, a.N);
+    }
+#pragma unroll
+    for (uint32_t p = 0; p < kPiecesX; ++p)
+      *reinterpret_cast<v8b *>(st + at_x + p * kStepX * kWideI * 2) = decode8(f.q[p], mx_factor((f.s[p] >> scale_shift) & 0xFFu));
+  };
+  auto barrier = [&] {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+  };
+  // A turn is a reading phase and a multiplying phase with a barrier after each; with two
+  // wavefronts a SIMD the second half of them runs one phase behind the first.
+  constexpr bool kPingPong = kWaves == 8;
+  const bool behind = kPingPong && wave >= kWaves / 2;
+  constexpr uint32_t kLoads = 2 * kPiecesX + kPiecesY;  // a wavefront's per turn
+  static_assert(2 * kLoads < 16, "");
+  v8b fx[FI], fy[FO];
+  // What the loads in flight fill is not what is read; __restrict__ says so to the compiler,
+  // which otherwise would wait for all of them before an LDS read.
+  auto read = [&](uint8_t *__restrict__ filled, const uint8_t *__restrict__ now) {
+    (void)filled;
+#pragma unroll
+    for (int y = 0; y < FO; ++y) fy[y] = fragment<kWideO>(now, wo + y, lane);
+#pragma unroll
+    for (int x = 0; x < FI; ++x) fx[x] = fragment<kWideI>(now + kBytesY, wi + x, lane);
+  };
+  auto turn = [&](Set &f, uint32_t k) {
+    read(ring + ((k + 3) % kRing) * kStage, ring + (k % kRing) * kStage);
+    // Before the barrier after which stage k + 1 is read by the first half, every
+    // wavefront's direct loads of it (of turn k - 2) are done: the half behind waits in its
+    // reading phase, the first half in its multiplying phase.
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // LDS accesses
+    if (DIRECT && behind) __builtin_amdgcn_s_waitcnt(0x0F70 | kLoads);
+    barrier();
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int x = 0; x < FI; ++x) {
+#pragma unroll
+      for (int y = 0; y < FO; ++y) acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[x], fy[y], acc[x][y], 0, 0, 0);
+      if (x == 0) {
+        __builtin_amdgcn_sched_barrier(0);  // the compiler would put this before the matrix instructions
+        settle(ring + ((k + 2) % kRing) * kStage, f);
+        fetch(f, k + 4);
+        fetch_direct(ring + ((k + 3) % kRing) * kStage, k + 3);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(0);
+    if (DIRECT && !behind) __builtin_amdgcn_s_waitcnt(0x0F70 | 2 * kLoads);
+    barrier();
+  };
+  if (steps) {
+#pragma unroll
+    for (uint32_t k = 0; k < 3; ++k) fetch_direct(ring + k * kStage, k);
+#pragma unroll
+    for (uint32_t k = 0; k < 2; ++k) fetch(set[k], k);
+#pragma unroll
+    for (uint32_t k = 0; k < 2; ++k) settle(ring + k * kStage, set[k]);
+#pragma unroll
+    for (uint32_t k = 0; k < 2; ++k) fetch(set[k], k + 2);
+    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0 & ~0x0F00);  // and LDS writes
   }
+  barrier();
+  if (behind) barrier();
 #pragma unroll 1
-  for (uint64_t tb = t0; tb < t1; tb += kT) {
-    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);  // the direct loads of the stage
-    __syncthreads();
-    both(stages + (cur ^ 1) * kStage, stages + cur * kStage, tb + kT);
-    cur ^= 1;
+  for (uint32_t k = 0; k < steps; k += 2) {
+    turn(set[0], k);
+    turn(set[1], k + 1);
   }
+  if (kPingPong && !behind) barrier();
+  __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);  // no load into LDS outlives the workgroup
   // a lane has four consecutive i of one o
   TO *dw = static_cast<TO *>(dst) + (uint64_t)blockIdx.y * a.N * a.K;
 #pragma unroll

@@ -167,8 +167,10 @@ template <bool E4M3> __device__ __forceinline__ uint2 mx_encode(const F8 &x, uin
 // A block scale as a float factor; bytes below the smallest exponent the packer
 // writes are taken as they are (2^-127 is a subnormal float).
 __device__ __forceinline__ float mx_factor(uint32_t scale) {
-  if (scale == kMxNanScale) return __builtin_nanf("");
-  return scale ? __builtin_bit_cast(float, scale << 23) : 5.877471754111438e-39f;
+  uint32_t bits = scale << 23;
+  bits = scale == 0 ? 0x400000u : bits;
+  bits = scale == kMxNanScale ? 0x7FC00000u : bits;
+  return __builtin_bit_cast(float, bits);
 }
 
 // Values of eight codes (e4m3: eight bytes; e2m1: the nibbles of .x).
