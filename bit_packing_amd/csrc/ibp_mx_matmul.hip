@@ -276,10 +276,6 @@ __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, voi
   // the longer one, a third of its time); with three they would come too late there.
   constexpr bool kPingPong = kWaves == 8, kLateFill = kStages >= 4;
   const bool behind = kPingPong && wave >= kWaves / 2;
-  // vmcnt that leaves `stages` stages' loads in flight, and no LDS access
-  auto wait = [](auto stages) { __builtin_amdgcn_s_waitcnt(0x0070 | (stages.value * kLoads)); };
-  using Two = std::integral_constant<uint32_t, kStages - 2>;
-  using Three = std::integral_constant<uint32_t, kStages - 3>;
   // What is filled is not what is read; __restrict__ says so to the compiler, which
   // otherwise would wait for all loads in flight before an LDS read.
   auto load_phase = [&](uint8_t *__restrict__ next, uint8_t *__restrict__ next_scales, const uint8_t *__restrict__ now,
@@ -302,13 +298,10 @@ __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, voi
     load_phase(free_stage, scales + (odd ^ 1) * kScales, ring + now * kStage, scales + odd * kScales + k % kGroup * 4, k);
     next = now;
     now = now + 1 == kStages ? 0 : now + 1;
-    // Before the barrier after which stage k + 1 is read by the first half, every wavefront
-    // has waited for its loads of that stage: the half behind in its reading phase, the
-    // first half in its multiplying phase (loads of scales in between make a wait longer,
-    // never shorter, and are kGroup stages early).
-    if constexpr (!kLateFill) wait(Two{});
-    else if (behind) wait(Three{});
-    else __builtin_amdgcn_s_waitcnt(0xC07F);  // LDS reads only
+    // These reads are done, and this wavefront's loads of stage k + 1 (not those of the stages
+    // after it; loads of scales in between make the wait longer, never shorter, and are
+    // kGroup stages early): after one or two barriers the first half reads it.
+    __builtin_amdgcn_s_waitcnt(0x0070 | (kStages - (kLateFill ? 3 : 2)) * kLoads);
     barrier();
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
@@ -322,8 +315,6 @@ __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, voi
     }
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_setprio(0);
-    if constexpr (kLateFill)
-      if (!behind) wait(Two{});
     barrier();
   }
   if (kPingPong && wave < kWaves / 2) barrier();

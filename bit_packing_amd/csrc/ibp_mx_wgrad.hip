@@ -167,7 +167,7 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
   constexpr bool kPingPong = kWaves == 8;
   const bool behind = kPingPong && wave >= kWaves / 2;
   constexpr uint32_t kLoads = 2 * kPiecesX + kPiecesY;  // a wavefront's per turn
-  static_assert(2 * kLoads < 16, "");
+  static_assert(kLoads < 16, "");
   v8b fx[FI], fy[FO];
   // What the loads in flight fill is not what is read; __restrict__ says so to the compiler,
   // which otherwise would wait for all of them before an LDS read.
@@ -178,13 +178,17 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
 #pragma unroll
     for (int x = 0; x < FI; ++x) fx[x] = fragment<kWideI>(now + kBytesY, wi + x, lane);
   };
+  auto write = [&](uint8_t *__restrict__ filled, uint8_t *__restrict__ settled, Set &f, uint32_t k) {
+    settle(settled, f);
+    fetch(f, k + 4);
+    fetch_direct(filled, k + 3);
+  };
   auto turn = [&](Set &f, uint32_t k) {
     read(ring + ((k + 3) % kRing) * kStage, ring + (k % kRing) * kStage);
-    // Before the barrier after which stage k + 1 is read by the first half, every
-    // wavefront's direct loads of it (of turn k - 2) are done: the half behind waits in its
-    // reading phase, the first half in its multiplying phase.
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // LDS accesses
-    if (DIRECT && behind) __builtin_amdgcn_s_waitcnt(0x0F70 | kLoads);
+    // These reads are done, and this wavefront's direct loads of stage k + 1 (of turn k - 2;
+    // turn k - 1's are not waited for): after two barriers the first half reads it.
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    if constexpr (DIRECT) __builtin_amdgcn_s_waitcnt(0x0F70 | kLoads);
     barrier();
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
@@ -193,14 +197,11 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
       for (int y = 0; y < FO; ++y) acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[x], fy[y], acc[x][y], 0, 0, 0);
       if (x == 0) {
         __builtin_amdgcn_sched_barrier(0);  // the compiler would put this before the matrix instructions
-        settle(ring + ((k + 2) % kRing) * kStage, f);
-        fetch(f, k + 4);
-        fetch_direct(ring + ((k + 3) % kRing) * kStage, k + 3);
+        write(ring + ((k + 3) % kRing) * kStage, ring + ((k + 2) % kRing) * kStage, f, k);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_setprio(0);
-    if (DIRECT && !behind) __builtin_amdgcn_s_waitcnt(0x0F70 | 2 * kLoads);
     barrier();
   };
   if (steps) {
