@@ -2,7 +2,9 @@
 // scale per 32 elements, reading them back, and the gated activation silu(gate) * up
 // that keeps its inputs as e4m3 checkpoints, with its backward pass from them.
 //
-// All four are one pass over the data, bound by HBM.  A lane takes eight consecutive
+// All four are one pass over the data, bound by HBM: 16384 x 8192 in bf16 is packed to
+// e2m1 in 61 us (5.5 TB/s; a copy of 1 GiB reaches 5.2), to e4m3 in 73, read back in 59,
+// the gated activation takes 206 us forward (5.3 TB/s) and 191 back (5.7).  A lane takes eight consecutive
 // elements (16 bytes of a 16-bit type), so four lanes hold a block and share its
 // largest magnitude by two lane exchanges, and 16 lanes hold the four blocks whose
 // scale bytes make one dword.  A row is cut into strips of 8 times the smallest power of
@@ -63,8 +65,8 @@ template <bool E4M3> __device__ __forceinline__ uint2 load_codes(const uint8_t *
 // 1 / (1 + exp(-g)).  The 16-bit types take it from the hardware's exp2 and reciprocal
 // (1 unit of the last place each), the argument's rounding made good by a factor: 6 half
 // units in all, far below the result's own rounding, for a third of the instructions
-// (the kernels are bound by instructions otherwise: forward 16384 x 8192 in bf16 FWD us
-// against FWDL us).  32-bit results take the library's exp and a true quotient.
+// (forward of 16384 x 8192 in bf16 206 us against 245 with the library's exp and a true
+// quotient, which 32-bit results take).
 template <int D> __device__ __forceinline__ float sigmoid(float g) {
   if constexpr (D == IBP_F32) {
     return 1.0f / (1.0f + expf(-g));
@@ -106,15 +108,17 @@ template <int D, bool E4M3, uint32_t R> __global__ __launch_bounds__(kBlock) voi
   const uint32_t nblk = (uint32_t)mx_blocks(a.cols);
   const uint64_t cp = mx_code_pitch(a.cols, E4M3), sp = mx_scale_pitch(a.cols);
   const T *in = static_cast<const T *>(a.in);
-  for (uint32_t unit = blockIdx.x; unit < w.units; unit += gridDim.x) {
-    const Place<R> p(w, unit, a.rows);
-    Vec8<T> x[R];
+  by_width(a.cols, [&](auto wide) {
+    for (uint32_t unit = blockIdx.x; unit < w.units; unit += gridDim.x) {
+      const Place<R> p(w, unit, a.rows);
+      Vec8<T> x[R];
 #pragma unroll
-    for (uint32_t k = 0; k < R; ++k) x[k] = load8<T>(in + p.row[k] * a.cols, p.c, a.cols);
+      for (uint32_t k = 0; k < R; ++k) x[k] = load8<wide.value, T>(in + p.row[k] * a.cols, p.c, a.cols);
 #pragma unroll
-    for (uint32_t k = 0; k < R; ++k)
-      encode_lane<E4M3>(widen<T>(x[k], p.c, a.cols), a.codes + p.row[k] * cp, a.scales + p.row[k] * sp, p.c, nblk, p.ok[k]);
-  }
+      for (uint32_t k = 0; k < R; ++k)
+        encode_lane<E4M3>(widen<wide.value, T>(x[k], p.c, a.cols), a.codes + p.row[k] * cp, a.scales + p.row[k] * sp, p.c, nblk, p.ok[k]);
+    }
+  });
 }
 
 template <int D, bool E4M3, uint32_t R> __global__ __launch_bounds__(kBlock) void mx_unpack_kernel(MxArgs a, Walk w) {
@@ -144,25 +148,27 @@ template <int D, uint32_t R> __global__ __launch_bounds__(kBlock) void mx_swiglu
   const uint64_t cp = mx_code_pitch(a.cols, true), sp = mx_scale_pitch(a.cols);
   const T *gate = static_cast<const T *>(a.in), *up = static_cast<const T *>(a.in2);
   T *h = static_cast<T *>(a.out);
-  for (uint32_t unit = blockIdx.x; unit < w.units; unit += gridDim.x) {
-    const Place<R> p(w, unit, a.rows);
-    Vec8<T> vg[R], vu[R];
+  by_width(a.cols, [&](auto wide) {
+    for (uint32_t unit = blockIdx.x; unit < w.units; unit += gridDim.x) {
+      const Place<R> p(w, unit, a.rows);
+      Vec8<T> vg[R], vu[R];
 #pragma unroll
-    for (uint32_t k = 0; k < R; ++k) {
-      vg[k] = load8<T>(gate + p.row[k] * a.cols, p.c, a.cols);
-      vu[k] = load8<T>(up + p.row[k] * a.cols, p.c, a.cols);
+      for (uint32_t k = 0; k < R; ++k) {
+        vg[k] = load8<wide.value, T>(gate + p.row[k] * a.cols, p.c, a.cols);
+        vu[k] = load8<wide.value, T>(up + p.row[k] * a.cols, p.c, a.cols);
+      }
+#pragma unroll
+      for (uint32_t k = 0; k < R; ++k) {
+        const F8 g = widen<wide.value, T>(vg[k], p.c, a.cols), u = widen<wide.value, T>(vu[k], p.c, a.cols);
+        encode_lane<true>(g, a.codes + p.row[k] * cp, a.scales + p.row[k] * sp, p.c, nblk, p.ok[k]);
+        encode_lane<true>(u, a.codes2 + p.row[k] * cp, a.scales2 + p.row[k] * sp, p.c, nblk, p.ok[k]);
+        F8 o;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o.v[i] = g.v[i] * sigmoid<D>(g.v[i]) * u.v[i];
+        if (p.ok[k] && p.c < a.cols) store8<T>(h + p.row[k] * a.cols, p.c, a.cols, o);
+      }
     }
-#pragma unroll
-    for (uint32_t k = 0; k < R; ++k) {
-      const F8 g = widen<T>(vg[k], p.c, a.cols), u = widen<T>(vu[k], p.c, a.cols);
-      encode_lane<true>(g, a.codes + p.row[k] * cp, a.scales + p.row[k] * sp, p.c, nblk, p.ok[k]);
-      encode_lane<true>(u, a.codes2 + p.row[k] * cp, a.scales2 + p.row[k] * sp, p.c, nblk, p.ok[k]);
-      F8 o;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o.v[i] = g.v[i] * sigmoid<D>(g.v[i]) * u.v[i];
-      if (p.ok[k] && p.c < a.cols) store8<T>(h + p.row[k] * a.cols, p.c, a.cols, o);
-    }
-  }
+  });
 }
 
 // With s = sigmoid(g): dgate = dh u s (1 + g (1 - s)), dup = dh g s, g and u read back
@@ -172,35 +178,37 @@ template <int D, uint32_t R> __global__ __launch_bounds__(kBlock) void mx_swiglu
   const uint64_t cp = mx_code_pitch(a.cols, true), sp = mx_scale_pitch(a.cols);
   const T *dh = static_cast<const T *>(a.in2);
   T *dgate = static_cast<T *>(a.out), *dup = static_cast<T *>(a.out2);
-  for (uint32_t unit = blockIdx.x; unit < w.units; unit += gridDim.x) {
-    const Place<R> p(w, unit, a.rows);
-    if (p.c >= a.cols) continue;
-    uint2 qg[R], qu[R];
-    uint32_t sg[R], su[R];
-    Vec8<T> vd[R];
+  by_width(a.cols, [&](auto wide) {
+    for (uint32_t unit = blockIdx.x; unit < w.units; unit += gridDim.x) {
+      const Place<R> p(w, unit, a.rows);
+      if (p.c >= a.cols) continue;
+      uint2 qg[R], qu[R];
+      uint32_t sg[R], su[R];
+      Vec8<T> vd[R];
 #pragma unroll
-    for (uint32_t k = 0; k < R; ++k) {
-      qg[k] = load_codes<true>(a.codes + p.row[k] * cp, p.c);
-      qu[k] = load_codes<true>(a.codes2 + p.row[k] * cp, p.c);
-      sg[k] = a.scales[p.row[k] * sp + p.c / kMxBlock];
-      su[k] = a.scales2[p.row[k] * sp + p.c / kMxBlock];
-      vd[k] = load8<T>(dh + p.row[k] * a.cols, p.c, a.cols);
-    }
-#pragma unroll
-    for (uint32_t k = 0; k < R; ++k) {
-      if (!p.ok[k]) continue;
-      const F8 g = mx_decode<true>(qg[k], sg[k]), u = mx_decode<true>(qu[k], su[k]), d = widen<T>(vd[k], p.c, a.cols);
-      F8 og, ou;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float s = sigmoid<D>(g.v[i]), ds = d.v[i] * s;
-        og.v[i] = ds * u.v[i] * (1.0f + g.v[i] * (1.0f - s));
-        ou.v[i] = ds * g.v[i];
+      for (uint32_t k = 0; k < R; ++k) {
+        qg[k] = load_codes<true>(a.codes + p.row[k] * cp, p.c);
+        qu[k] = load_codes<true>(a.codes2 + p.row[k] * cp, p.c);
+        sg[k] = a.scales[p.row[k] * sp + p.c / kMxBlock];
+        su[k] = a.scales2[p.row[k] * sp + p.c / kMxBlock];
+        vd[k] = load8<wide.value, T>(dh + p.row[k] * a.cols, p.c, a.cols);
       }
-      store8<T>(dgate + p.row[k] * a.cols, p.c, a.cols, og);
-      store8<T>(dup + p.row[k] * a.cols, p.c, a.cols, ou);
+#pragma unroll
+      for (uint32_t k = 0; k < R; ++k) {
+        if (!p.ok[k]) continue;
+        const F8 g = mx_decode<true>(qg[k], sg[k]), u = mx_decode<true>(qu[k], su[k]), d = widen<wide.value, T>(vd[k], p.c, a.cols);
+        F8 og, ou;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float s = sigmoid<D>(g.v[i]), ds = d.v[i] * s;
+          og.v[i] = ds * u.v[i] * (1.0f + g.v[i] * (1.0f - s));
+          ou.v[i] = ds * g.v[i];
+        }
+        store8<T>(dgate + p.row[k] * a.cols, p.c, a.cols, og);
+        store8<T>(dup + p.row[k] * a.cols, p.c, a.cols, ou);
+      }
     }
-  }
+  });
 }
 
 constexpr uint32_t kMaxGrid = 1u << 22;

@@ -63,8 +63,9 @@ template <typename T> __device__ __forceinline__ T from_global(const uint8_t *p)
 // stages ahead where its rows are aligned to 16 bytes (DIRECT), else through registers like
 // X, which is loaded four stages ahead and decoded into LDS two stages ahead.  As in the
 // 4-bit product, half of the eight wavefronts of a large tile read a stage while the other
-// half multiplies (PH us for 16384 x 4096 x 8192 in phases, ST us with all in step and two
-// stages of 64 tokens).
+// half multiplies (16384 x 4096 x 8192: 863 us, 1.27 PFLOP/s, against 1090 with all in
+// step and two stages of 64 tokens).  Bound by the phases: the matrix units are busy half
+// of the time, LDS a quarter.
 template <int WI, int WO, int FI, int FO, bool DIRECT, int DO>
 __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *dst, uint64_t t_each, uint32_t tiles_o,
                                                            uint32_t tiles_i) {
@@ -91,7 +92,8 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
   const uint32_t cy = o0 + ((((sy >> 1) ^ (ty & 7)) << 1) | (sy & 1)) * 8;
   const bool in_y = !DIRECT || cy < a.N, in_x = cx < cp;
   // without DIRECT a piece past the row's end is the row's last eight elements (load8)
-  const uint64_t at_y = DIRECT ? cy : (a.N >= 8 ? (cy + 8 <= a.N ? cy : a.N - 8) : 0);
+  const bool wide = a.N >= 8;
+  const uint64_t at_y = DIRECT ? cy : (wide ? (cy + 8 <= a.N ? cy : a.N - 8) : 0);
   const uint8_t *py = in_y ? reinterpret_cast<const uint8_t *>(dy + (t0 + ty) * a.N + at_y) : kZeros;
   const uint8_t *px = in_x ? a.x_codes + (t0 + tx) * cp + cx : kZeros;
   const uint8_t *ps = in_x ? a.x_scales + (t0 + tx) * sp + cx / (4 * kMxBlock) * 4 : kZeros;  // its dword
@@ -130,7 +132,7 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
 #pragma unroll
       for (uint32_t p = 0; p < kPiecesY; ++p) {
         const uint8_t *from = stage * kT + ty + p * kStepY < tokens ? py : kZeros;
-        f.y[p] = a.N >= 8 ? from_global<Vec8<__bf16>>(from) : load8<__bf16>(reinterpret_cast<const __bf16 *>(from), 0, a.N);
+        f.y[p] = wide ? from_global<Vec8<__bf16>>(from) : load8<false, __bf16>(reinterpret_cast<const __bf16 *>(from), 0, a.N);
         py += go_y;
       }
     }
@@ -149,7 +151,7 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
     if constexpr (!DIRECT) {
 #pragma unroll
       for (uint32_t p = 0; p < kPiecesY; ++p)
-        *reinterpret_cast<v8b *>(st + (p * kThreads + threadIdx.x) * 16) = (v8b)settle8<__bf16>(f.y[p], cy, a.N);
+        *reinterpret_cast<v8b *>(st + (p * kThreads + threadIdx.x) * 16) = (v8b)(wide ? settle8<true, __bf16>(f.y[p], cy, a.N) : settle8<false, __bf16>(f.y[p], cy, a.N));
     }
 #pragma unroll
     for (uint32_t p = 0; p < kPiecesX; ++p)
@@ -248,9 +250,10 @@ template <int DO> __global__ __launch_bounds__(kBlock) void wgrad_join_kernel(Mx
 
 // Tile and ranges of tokens.  256 x 256 tiles read each operand half as often as 128 x
 // 128 ones, so they are taken where tiles and tokens give every CU 512 tokens of one
-// (16384 tokens: 2048 x 2048 171 us against 227, 512 x 512 42 against 36).  The tokens are
-// cut into ranges until there is a workgroup per CU (16384 tokens of 1024 x 1024: 556 us
-// in one range, 64 in sixteen): each range's sums are written and read once in 32 bits.
+// (16384 tokens: 2048 x 2048 140 us against 179, 512 x 512 38 against 31; 256 tokens of
+// 4096 x 4096 26 against 24).  The tokens are cut into ranges until there is a workgroup
+// per CU (16384 tokens of 1024 x 1024: 366 us in one range, 55 in sixteen), each of 256
+// tokens at least: a range's sums are written and read once in 32 bits.
 struct Plan {
   bool big;
   uint32_t tiles_o, tiles_i;
@@ -261,11 +264,11 @@ struct Plan {
 Plan plan_of(uint64_t T, uint32_t N, uint32_t K) {
   Plan p;
   const uint64_t big = (((uint64_t)N + 255) / 256) * (((uint64_t)K + 255) / 256);
-  p.big = big * ((T + 511) / 512) >= 256;
+  p.big = T >= 1024 && big * ((T + 511) / 512) >= 256;
   const uint32_t wide = p.big ? 256 : 128;
   p.tiles_o = (uint32_t)(((uint64_t)N + wide - 1) / wide);
   p.tiles_i = (uint32_t)(((uint64_t)K + wide - 1) / wide);
-  const uint64_t tiles = (uint64_t)p.tiles_o * p.tiles_i, least = p.big ? 512 : 128;
+  const uint64_t tiles = (uint64_t)p.tiles_o * p.tiles_i, least = p.big ? 512 : 256;
   const uint64_t want = 256 / tiles, most = (T + least - 1) / least;
   uint64_t n = want < most ? want : most;
   n = n < 1 ? 1 : (n > 32 ? 32 : n);

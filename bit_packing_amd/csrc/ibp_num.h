@@ -46,31 +46,41 @@ template <typename T> __device__ __forceinline__ Vec8<T> move_down(Vec8<T> x, ui
 }
 
 // Elements [c, c + 8) of a row of `cols` elements are loaded by load8 as they lie in
-// memory, and given zeros past the row's end by settle8 where they are used.  At the
-// row's end load8 takes the row's last eight elements: one load for every lane and no
-// branch, so that no load waits for another (element by element, or with the end's
-// lanes in a branch of their own, each load of a wavefront at the end waited).
-template <typename T> __device__ __forceinline__ Vec8<T> load8(const T *row, uint32_t c, uint32_t cols) {
-  if (cols >= 8) return *reinterpret_cast<const Vec8<T> *>(row + (c + 8 <= cols ? c : cols - 8));
-  Vec8<T> x = {};
+// memory, and given zeros past the row's end by widen where they are used.  At the row's
+// end load8 takes the row's last eight elements: one load for every lane and no branch,
+// so that no load waits for another (element by element, or with the end's lanes in a
+// branch of their own, each load of a wavefront at the end waited).  Rows of less than
+// eight elements (WIDE false) are loaded one by one; a kernel asks once which it has
+// (by_width), as even a uniform branch at each load makes the loads wait for each other.
+template <bool WIDE, typename T> __device__ __forceinline__ Vec8<T> load8(const T *row, uint32_t c, uint32_t cols) {
+  if constexpr (WIDE) {
+    return *reinterpret_cast<const Vec8<T> *>(row + (c + 8 <= cols ? c : cols - 8));
+  } else {
+    Vec8<T> x = {};
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < (int)cols) x[i] = row[i];
-  return x;
+    for (int i = 0; i < 7; ++i)
+      if (i < (int)cols) x[i] = row[i];
+    return x;
+  }
 }
 
-template <typename T> __device__ __forceinline__ Vec8<T> settle8(Vec8<T> x, uint32_t c, uint32_t cols) {
+template <bool WIDE, typename T> __device__ __forceinline__ Vec8<T> settle8(Vec8<T> x, uint32_t c, uint32_t cols) {
   if (c >= cols) return Vec8<T>{};
-  if (cols >= 8 && c + 8 > cols) return move_down<T>(x, c + 8 - cols);
+  if (WIDE && c + 8 > cols) return move_down<T>(x, c + 8 - cols);
   return x;
 }
 
-template <typename T> __device__ __forceinline__ F8 widen(Vec8<T> x, uint32_t c, uint32_t cols) {
-  x = settle8<T>(x, c, cols);
+template <bool WIDE, typename T> __device__ __forceinline__ F8 widen(Vec8<T> x, uint32_t c, uint32_t cols) {
+  x = settle8<WIDE, T>(x, c, cols);
   F8 r;
 #pragma unroll
   for (int i = 0; i < 8; ++i) r.v[i] = (float)x[i];
   return r;
+}
+
+template <typename F> __device__ __forceinline__ void by_width(uint32_t cols, F &&f) {
+  if (cols >= 8) f(std::true_type{});
+  else f(std::false_type{});
 }
 
 // The same elements written, each rounded once to T (nearest, ties to even).
