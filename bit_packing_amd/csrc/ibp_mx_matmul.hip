@@ -23,7 +23,24 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 constexpr uint32_t kStep = 16;  // blocks per step of the direct kernel: 512 elements
 
 // Scales are the low bytes of ws and xs; format codes: 0 e4m3, 4 e2m1.
-template <bool A8> __device__ __forceinline__ v4f mfma_mx(v8i w, v8i x, v4f acc, int ws, int xs) {
+//
+// Within a block the instruction adds products aligned to the largest and drops what lies
+// more than 13 binary places below it (measured: 256 * 1 + 2^-5 * 1 is kept, + 2^-6 is
+// not).  Products of e2m1 fit (36 down to 1/4), sums over blocks are 32-bit; products of
+// e4m3 span 22 places, and what is dropped comes to 4.5e-6 of the result (2-norm), far
+// below the rounding of a 16-bit one.  For 32-bit results (FINE) the elements of magnitude
+// 2 and more, whose codes have bit 6, and the rest go through an instruction each.
+template <bool A8, bool FINE> __device__ __forceinline__ v4f mfma_mx(v8i w, v8i x, v4f acc, int ws, int xs) {
+  if constexpr (A8 && FINE) {
+    v8i high;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t bit = ((uint32_t)x[i] >> 6) & 0x01010101u;
+      high[i] = x[i] & (int)((bit << 8) - bit);  // bytes with the bit
+      x[i] ^= high[i];
+    }
+    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, high, acc, 4, 0, 0, ws, 0, xs);
+  }
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, acc, 4, A8 ? 0 : 4, 0, ws, 0, xs);
 }
 
@@ -96,7 +113,7 @@ template <bool A8, int MI, int DO> __global__ void mx_direct_kernel(MxMatmulArgs
       const uint32_t xd[4] = {xsc4[i].x, xsc4[i].y, xsc4[i].z, xsc4[i].w};
 #pragma unroll
       for (int s = 0; s < 4; ++s)
-        acc[i] = mfma_mx<A8>(operand(w[s], make_uint4(0u, 0u, 0u, 0u)), operand(lo[i][s], hi[i][s]), acc[i],
+        acc[i] = mfma_mx<A8, DO == IBP_F32>(operand(w[s], make_uint4(0u, 0u, 0u, 0u)), operand(lo[i][s], hi[i][s]), acc[i],
                              (int)(wd[s] >> (8 * g)), (int)(xd[s] >> (8 * g)));
     }
   }
@@ -179,7 +196,7 @@ template <uint32_t ROWS, uint32_t PITCH, uint32_t WAVES> struct Tile {
   }
 };
 
-template <bool A8, int WM, int WN, int FM, int FN, int DO>
+template <bool A8, bool FINE, int WM, int WN, int FM, int FN, int DO>
 __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, void *dst, uint32_t tiles_m,
                                                              uint32_t tiles_n, uint32_t stages_each) {
   using TO = typename Num<DO>::T;
@@ -309,7 +326,7 @@ __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, voi
 #pragma unroll
     for (int m = 0; m < FM; ++m) {
 #pragma unroll
-      for (int n = 0; n < FN; ++n) acc[n][m] = mfma_mx<A8>(w[n], v[m], acc[n][m], ws[n], xs[m]);
+      for (int n = 0; n < FN; ++n) acc[n][m] = mfma_mx<A8, FINE>(w[n], v[m], acc[n][m], ws[n], xs[m]);
       if (kLateFill && m == 0) {
         __builtin_amdgcn_sched_barrier(0);  // the compiler would issue the loads first
         fill(free_stage, k + kStages - 1);
@@ -403,12 +420,12 @@ Plan plan_of(uint64_t M, uint64_t N, uint32_t K) {
   return p;
 }
 
-template <bool A8, int DO> hipError_t go_tile(const MxMatmulArgs &a, const Plan &p, void *dst, hipStream_t s) {
+template <bool A8, bool FINE, int DO> hipError_t go_tile(const MxMatmulArgs &a, const Plan &p, void *dst, hipStream_t s) {
   const dim3 grid(p.tiles_m * p.tiles_n, p.splits);
   if (p.kind == Plan::kBig)
-    mx_tile_kernel<A8, 2, 4, 8, 4, DO><<<grid, 512, 0, s>>>(a, dst, p.tiles_m, p.tiles_n, p.stages_each);
+    mx_tile_kernel<A8, FINE, 2, 4, 8, 4, DO><<<grid, 512, 0, s>>>(a, dst, p.tiles_m, p.tiles_n, p.stages_each);
   else
-    mx_tile_kernel<A8, 2, 2, 4, 4, DO><<<grid, 256, 0, s>>>(a, dst, p.tiles_m, p.tiles_n, p.stages_each);
+    mx_tile_kernel<A8, FINE, 2, 2, 4, 4, DO><<<grid, 256, 0, s>>>(a, dst, p.tiles_m, p.tiles_n, p.stages_each);
   return hipGetLastError();
 }
 
@@ -417,11 +434,12 @@ template <bool A8> hipError_t go(const MxMatmulArgs &a, hipStream_t s) {
   if (p.kind == Plan::kDirect) return go_direct<A8, 1>(a, s);
   if ((uint64_t)p.tiles_m * p.tiles_n > 0x7FFFFF) return hipErrorInvalidValue;
   if (p.splits > 1) {
-    const hipError_t e = go_tile<A8, IBP_F32>(a, p, a.ws, s);
+    const bool fine = A8 && a.dtype == IBP_F32;
+    const hipError_t e = fine ? go_tile<A8, A8, IBP_F32>(a, p, a.ws, s) : go_tile<A8, false, IBP_F32>(a, p, a.ws, s);
     if (e != hipSuccess) return e;
   }
   return with_dtype(a.dtype, [&](auto d) {
-    if (p.splits == 1) return go_tile<A8, d.value>(a, p, a.y, s);
+    if (p.splits == 1) return go_tile<A8, A8 && d.value == IBP_F32, d.value>(a, p, a.y, s);
     const uint64_t n = (a.M * a.N + kBlock * 4 - 1) / (kBlock * 4);
     mx_join_kernel<d.value><<<(uint32_t)(n < 4096 ? n : 4096), kBlock, 0, s>>>(a, p.splits);
     return hipGetLastError();

@@ -337,6 +337,23 @@ def test_matmul_nan_blocks_reach_their_rows_only(ibp, fmt, m):
     assert np.array_equal(np.isnan(y), bad)
 
 
+@pytest.mark.parametrize("m", [3, 300, 4000])
+def test_matmul_in_32_bits_keeps_small_products(ibp, m):
+    """One product of 256 and one of 2^(8 - k) in the same block: both fit 32 bits."""
+    cols, n = 160, 4000 if m == 4000 else 40
+    code = {v: c for c, v in enumerate(mx_ref.TABLE[mx_ref.E4M3])}
+    a = np.zeros((m, cols), np.uint8), np.zeros((m, mx_ref.scale_pitch(cols)), np.uint8)
+    b = np.zeros((n, cols // 2), np.uint8), np.zeros((n, mx_ref.scale_pitch(cols)), np.uint8)
+    a[1][:, :5], b[1][:, :5] = 127, 127
+    k = np.arange(m) % 18
+    a[0][:, 33] = code[256.0]
+    a[0][np.arange(m), 40 + k] = [code[2.0 ** (8 - j)] for j in k]
+    b[0][:] = 0x22  # ones
+    y = ibp.ibp_mx_matmul(device(ibp, *a, cols, mx_ref.E4M3), device(ibp, *b, cols, mx_ref.E2M1), dtype=torch.float32)
+    want = np.repeat((256 + 2.0 ** (8 - k))[:, None], n, 1)
+    assert np.array_equal(host(y), want)
+
+
 def test_matmul_of_nothing(ibp):
     for m, n, k in ((0, 5, 64), (5, 0, 64), (3, 4, 0)):
         a, b = ibp.make_mx(m, k, ibp.IBP_MX_E4M3, "cuda"), ibp.make_mx(n, k, ibp.IBP_MX_E2M1, "cuda")
