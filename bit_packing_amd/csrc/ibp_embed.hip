@@ -387,15 +387,19 @@ template <bool WIDE, typename TI, typename TO> __device__ __forceinline__ void s
   }
 }
 
-// The first zero_blocks workgroups write the rows without tokens, which they find by
-// search in the sorted tokens, a lane a row; the others sum.
+// zero_blocks workgroups write the rows without tokens, which they find by search in the
+// sorted tokens, a lane a row; the others sum.
 template <int DI, int DO> __global__ __launch_bounds__(kBlock) void grad_sum_kernel(SumArgs a) {
   using TI = typename Num<DI>::T;
   using TO = typename Num<DO>::T;
   const uint32_t tx = threadIdx.x & (a.lanes - 1), ty = threadIdx.x / a.lanes, groups = kBlock / a.lanes;
-  if (blockIdx.x < a.zero_blocks) {
+  // one of each in turn while there are both: reads and writes then share the memory
+  const uint32_t sum_blocks = gridDim.x - a.zero_blocks, both = 2 * (sum_blocks < a.zero_blocks ? sum_blocks : a.zero_blocks);
+  const bool zero = blockIdx.x < both ? blockIdx.x & 1 : sum_blocks < a.zero_blocks;
+  const uint32_t block = blockIdx.x < both ? blockIdx.x >> 1 : blockIdx.x - both / 2;
+  if (zero) {
     __shared__ uint64_t empty;
-    for (uint64_t r0 = (uint64_t)blockIdx.x * kWave; r0 < a.n_rows; r0 += (uint64_t)a.zero_blocks * kWave) {
+    for (uint64_t r0 = (uint64_t)block * kWave; r0 < a.n_rows; r0 += (uint64_t)a.zero_blocks * kWave) {
       if (threadIdx.x < kWave) {
         const uint64_t r = r0 + threadIdx.x;
         bool none = false;
@@ -416,9 +420,9 @@ template <int DI, int DO> __global__ __launch_bounds__(kBlock) void grad_sum_ker
     }
     return;
   }
-  const uint64_t units = (uint64_t)a.nchunks * a.slabs, step = (uint64_t)(gridDim.x - a.zero_blocks) * groups;
+  const uint64_t units = (uint64_t)a.nchunks * a.slabs, step = (uint64_t)sum_blocks * groups;
   by_width(a.dim, [&](auto wide) {
-    for (uint64_t unit = (uint64_t)(blockIdx.x - a.zero_blocks) * groups + ty; unit < units; unit += step) {
+    for (uint64_t unit = (uint64_t)block * groups + ty; unit < units; unit += step) {
       const uint32_t c = (uint32_t)(unit % a.slabs) * a.slab + tx * 8;
       if (c < a.dim) sum_chunk<wide.value, TI, TO>(a, (uint32_t)(unit / a.slabs), c);
     }
