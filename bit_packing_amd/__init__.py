@@ -224,7 +224,7 @@ def load_library() -> ctypes.CDLL:
         lib.ibp_mx_matmul.argtypes = [_mxp, _mxp, _vp, _int, _vp, _u64, _vp]
         lib.ibp_mx_matmul_workspace_bytes.argtypes = [_u64, _u64, _u64, _u32]
         lib.ibp_mx_linear_wgrad.argtypes = [_vp, _int, _u64, _mxp, _vp, _int, _vp, _u64, _vp]
-        lib.ibp_mx_linear_wgrad_workspace_bytes.argtypes = [_u64, _u64, _u64]
+        lib.ibp_mx_linear_wgrad_workspace_bytes.argtypes = [_u64, _u64, _u64, _int]
         for f in ("ibp_embedding_grad_workspace_bytes", "ibp_mx_codes_pitch", "ibp_mx_scales_pitch",
                   "ibp_mx_matmul_workspace_bytes", "ibp_mx_linear_wgrad_workspace_bytes"):
             getattr(lib, f).restype = _u64
@@ -556,6 +556,17 @@ def ibp_zip_decompress(z: ZipCompressed, out: torch.Tensor | None = None, err: t
 
 
 # ------------------------------------------------------------------ language-model operators
+#
+# With a stream given, a call runs as under ``torch.cuda.stream(stream)``: what it allocates
+# belongs to that stream, so its memory is not handed out again before the work there is
+# done.  Ordering that stream after the one that made the inputs is the caller's.
+
+
+def _stream_context(stream):
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return torch.cuda.stream(stream)
+
 
 _DTYPES = {torch.float32: IBP_F32, torch.float16: IBP_F16, torch.bfloat16: IBP_BF16}
 
@@ -594,13 +605,16 @@ def ibp_embedding_lookup(table: torch.Tensor, ids: torch.Tensor, scale: float = 
                          stream=None) -> torch.Tensor:
     """scale * table[ids], of out_dtype (the table's by default); table [rows, dim] may be
     pinned host memory.  Ids out of range give zero rows and set IBP_DEVERR_BAD_ID."""
+    if stream is not None:
+        with _stream_context(stream):
+            return ibp_embedding_lookup(table, ids, scale, out_dtype, out, err)
     if table.dim() != 2:
         raise ValueError("a table is [rows, dim]")
     rows, dim = table.shape
     out = _out(out, (*_ids(ids).shape, dim), out_dtype or (table.dtype if out is None else out.dtype),
                _device(ids, table))
     rc = load_library().ibp_embedding_lookup(_ptr(table), _dtype(table.dtype), rows, dim, _ptr(ids), ids.numel(),
-                                             scale, _ptr(out), _dtype(out.dtype), _ptr(err), _stream(stream))
+                                             scale, _ptr(out), _dtype(out.dtype), _ptr(err), _stream(None))
     _check(rc, "ibp_embedding_lookup")
     return out
 
@@ -611,6 +625,9 @@ def ibp_embedding_grad(dout: torch.Tensor, ids: torch.Tensor, n_rows: int, scale
     """Gradient [n_rows, dim] of ibp_embedding_lookup's table: scale times the sum of dout's
     rows of each id, in 32 bits, of grad_dtype (dout's by default).  Tokens with padding_id
     take no part."""
+    if stream is not None:
+        with _stream_context(stream):
+            return ibp_embedding_grad(dout, ids, n_rows, scale, padding_id, grad_dtype, grad, workspace, err)
     n, dim = _matrix(dout)
     if _ids(ids).numel() * dim != dout.numel() or tuple(dout.shape[:-1]) != tuple(ids.shape):
         raise ValueError("dout is [*ids.shape, dim]")
@@ -623,7 +640,7 @@ def ibp_embedding_grad(dout: torch.Tensor, ids: torch.Tensor, n_rows: int, scale
                                 dtype=torch.uint8, device=dev)
     rc = lib.ibp_embedding_grad(_ptr(dout), _dtype(dout.dtype), _ptr(ids), n, n_rows, dim, scale, padding_id,
                                 _ptr(grad), _dtype(grad.dtype), _ptr(workspace), _nbytes(workspace), _ptr(err),
-                                _stream(stream))
+                                _stream(None))
     _check(rc, "ibp_embedding_grad")
     return grad
 
@@ -640,8 +657,8 @@ def ibp_mx_matmul_workspace_bytes(m: int, n: int, k: int, a_format: int) -> int:
     return int(load_library().ibp_mx_matmul_workspace_bytes(m, n, k, a_format))
 
 
-def ibp_mx_linear_wgrad_workspace_bytes(tokens: int, outs: int, ins: int) -> int:
-    return int(load_library().ibp_mx_linear_wgrad_workspace_bytes(tokens, outs, ins))
+def ibp_mx_linear_wgrad_workspace_bytes(tokens: int, outs: int, ins: int, dy_dtype=torch.bfloat16) -> int:
+    return int(load_library().ibp_mx_linear_wgrad_workspace_bytes(tokens, outs, ins, _dtype(dy_dtype)))
 
 
 def ibp_embedding_grad_workspace_bytes(n_rows: int, n_ids: int, dim: int) -> int:
@@ -665,19 +682,25 @@ def _mx(m: MxTensor | None, rows: int, cols: int, format: int, device) -> MxTens
 
 def ibp_mx_pack(x: torch.Tensor, format: int, out: MxTensor | None = None, stream=None) -> MxTensor:
     """Pack the rows (last dimension) of x into IBP_MX_E4M3 or IBP_MX_E2M1 blocks of 32."""
+    if stream is not None:
+        with _stream_context(stream):
+            return ibp_mx_pack(x, format, out)
     if format not in (IBP_MX_E4M3, IBP_MX_E2M1):
         raise ValueError("a format is IBP_MX_E4M3 or IBP_MX_E2M1")
     rows, cols = _matrix(x)
     out = _mx(out, rows, cols, format, _device(x))
-    _check(load_library().ibp_mx_pack(_ptr(x), _dtype(x.dtype), ctypes.byref(out.struct()), _stream(stream)),
+    _check(load_library().ibp_mx_pack(_ptr(x), _dtype(x.dtype), ctypes.byref(out.struct()), _stream(None)),
            "ibp_mx_pack")
     return out
 
 
 def ibp_mx_unpack(m: MxTensor, dtype=torch.bfloat16, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The values [rows, cols] of a packed tensor."""
+    if stream is not None:
+        with _stream_context(stream):
+            return ibp_mx_unpack(m, dtype, out)
     out = _out(out, (m.rows, m.cols), dtype, m.device)
-    _check(load_library().ibp_mx_unpack(ctypes.byref(m.struct()), _ptr(out), _dtype(out.dtype), _stream(stream)),
+    _check(load_library().ibp_mx_unpack(ctypes.byref(m.struct()), _ptr(out), _dtype(out.dtype), _stream(None)),
            "ibp_mx_unpack")
     return out
 
@@ -686,6 +709,9 @@ def ibp_mx_swiglu(gate: torch.Tensor, up: torch.Tensor, h: torch.Tensor | None =
                   gate8: MxTensor | None = None, up8: MxTensor | None = None,
                   stream=None) -> tuple[torch.Tensor, MxTensor, MxTensor]:
     """(silu(gate) * up, and the e4m3 checkpoints of gate and up), in one pass."""
+    if stream is not None:
+        with _stream_context(stream):
+            return ibp_mx_swiglu(gate, up, h, gate8, up8)
     if gate.shape != up.shape or gate.dtype != up.dtype:
         raise ValueError("gate and up differ in shape or dtype")
     rows, cols = _matrix(gate)
@@ -693,7 +719,7 @@ def ibp_mx_swiglu(gate: torch.Tensor, up: torch.Tensor, h: torch.Tensor | None =
     h = torch.empty_like(gate) if h is None else _out(h, gate.shape, gate.dtype, dev)
     gate8, up8 = _mx(gate8, rows, cols, IBP_MX_E4M3, dev), _mx(up8, rows, cols, IBP_MX_E4M3, dev)
     rc = load_library().ibp_mx_swiglu(_ptr(gate), _ptr(up), _dtype(gate.dtype), _ptr(h),
-                                      ctypes.byref(gate8.struct()), ctypes.byref(up8.struct()), _stream(stream))
+                                      ctypes.byref(gate8.struct()), ctypes.byref(up8.struct()), _stream(None))
     _check(rc, "ibp_mx_swiglu")
     return h, gate8, up8
 
@@ -701,13 +727,16 @@ def ibp_mx_swiglu(gate: torch.Tensor, up: torch.Tensor, h: torch.Tensor | None =
 def ibp_mx_swiglu_backward(dh: torch.Tensor, gate8: MxTensor, up8: MxTensor, dgate: torch.Tensor | None = None,
                            dup: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """(dgate, dup) of ibp_mx_swiglu from its checkpoints."""
+    if stream is not None:
+        with _stream_context(stream):
+            return ibp_mx_swiglu_backward(dh, gate8, up8, dgate, dup)
     if _matrix(dh) != (gate8.rows, gate8.cols) and dh.numel():
         raise ValueError("dh and the checkpoints differ in shape")
     dev = _device(dh)
     dgate = torch.empty_like(dh) if dgate is None else _out(dgate, dh.shape, dh.dtype, dev)
     dup = torch.empty_like(dh) if dup is None else _out(dup, dh.shape, dh.dtype, dev)
     rc = load_library().ibp_mx_swiglu_backward(_ptr(dh), _dtype(dh.dtype), ctypes.byref(gate8.struct()),
-                                               ctypes.byref(up8.struct()), _ptr(dgate), _ptr(dup), _stream(stream))
+                                               ctypes.byref(up8.struct()), _ptr(dgate), _ptr(dup), _stream(None))
     _check(rc, "ibp_mx_swiglu_backward")
     return dgate, dup
 
@@ -721,11 +750,14 @@ def _workspace(workspace: torch.Tensor | None, need: int, device) -> torch.Tenso
 def ibp_mx_matmul(a: MxTensor, b: MxTensor, dtype=torch.bfloat16, out: torch.Tensor | None = None,
                   workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """[a.rows, b.rows] product of packed a with packed 4-bit b, both along their columns."""
+    if stream is not None:
+        with _stream_context(stream):
+            return ibp_mx_matmul(a, b, dtype, out, workspace)
     lib, dev = load_library(), a.device
     out = _out(out, (a.rows, b.rows), dtype, dev)
     workspace = _workspace(workspace, int(lib.ibp_mx_matmul_workspace_bytes(a.rows, b.rows, a.cols, a.format)), dev)
     rc = lib.ibp_mx_matmul(ctypes.byref(a.struct()), ctypes.byref(b.struct()), _ptr(out), _dtype(out.dtype),
-                           _ptr(workspace), 0 if workspace is None else _nbytes(workspace), _stream(stream))
+                           _ptr(workspace), 0 if workspace is None else _nbytes(workspace), _stream(None))
     _check(rc, "ibp_mx_matmul")
     return out
 
@@ -733,15 +765,19 @@ def ibp_mx_matmul(a: MxTensor, b: MxTensor, dtype=torch.bfloat16, out: torch.Ten
 def ibp_mx_linear_wgrad(dy: torch.Tensor, x8: MxTensor, dw_dtype=None, dw: torch.Tensor | None = None,
                         workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """[outs, x8.cols] weight gradient: the sum over tokens of dy's row times x8's row; dy
-    [x8.rows, outs] in bfloat16, x8 in e4m3."""
+    [x8.rows, outs] (in bfloat16 fastest), x8 in e4m3.  dw is of dw_dtype, dy's by default."""
+    if stream is not None:
+        with _stream_context(stream):
+            return ibp_mx_linear_wgrad(dy, x8, dw_dtype, dw, workspace)
     if dy.dim() != 2 or dy.shape[0] != x8.rows:
         raise ValueError("dy is [x8.rows, outs]")
     lib, dev = load_library(), _device(dy)
     outs = dy.shape[1]
     dw = _out(dw, (outs, x8.cols), dw_dtype or (dy.dtype if dw is None else dw.dtype), dev)
-    workspace = _workspace(workspace, int(lib.ibp_mx_linear_wgrad_workspace_bytes(x8.rows, outs, x8.cols)), dev)
+    workspace = _workspace(workspace, int(lib.ibp_mx_linear_wgrad_workspace_bytes(x8.rows, outs, x8.cols, _dtype(dy.dtype))),
+                           dev)
     rc = lib.ibp_mx_linear_wgrad(_ptr(dy), _dtype(dy.dtype), outs, ctypes.byref(x8.struct()), _ptr(dw),
                                  _dtype(dw.dtype), _ptr(workspace), 0 if workspace is None else _nbytes(workspace),
-                                 _stream(stream))
+                                 _stream(None))
     _check(rc, "ibp_mx_linear_wgrad")
     return dw

@@ -919,9 +919,9 @@ IBP_API uint64_t ibp_mx_matmul_workspace_bytes(uint64_t m, uint64_t n, uint64_t 
   return m && n ? mx_matmul_workspace(m, n, (uint32_t)k, a_format == IBP_MX_E4M3) : 0;
 }
 
-IBP_API uint64_t ibp_mx_linear_wgrad_workspace_bytes(uint64_t tokens, uint64_t outs, uint64_t ins) {
-  if (!product_rows_ok(outs) || ins > IBP_MAX_COLS) return 0;
-  return outs && ins ? mx_wgrad_workspace(tokens, (uint32_t)outs, (uint32_t)ins) : 0;
+IBP_API uint64_t ibp_mx_linear_wgrad_workspace_bytes(uint64_t tokens, uint64_t outs, uint64_t ins, int dy_dtype) {
+  if (!product_rows_ok(outs) || ins > IBP_MAX_COLS || !dtype_ok(dy_dtype)) return 0;
+  return outs && ins ? mx_wgrad_workspace(tokens, (uint32_t)outs, (uint32_t)ins, dy_dtype) : 0;
 }
 
 IBP_API int ibp_mx_matmul(const ibp_mx_t *a, const ibp_mx_t *b, void *d_y, int dtype, void *d_workspace,
@@ -959,17 +959,17 @@ IBP_API int ibp_mx_matmul(const ibp_mx_t *a, const ibp_mx_t *b, void *d_y, int d
 
 IBP_API int ibp_mx_linear_wgrad(const void *d_dy, int dy_dtype, uint64_t outs, const ibp_mx_t *x8, void *d_dw,
                                 int dw_dtype, void *d_workspace, uint64_t workspace_bytes, void *hip_stream) {
-  if (dy_dtype != IBP_BF16 || !dtype_ok(dw_dtype)) return IBP_ERR_INVALID_ARG;
+  if (!dtype_ok(dy_dtype) || !dtype_ok(dw_dtype)) return IBP_ERR_INVALID_ARG;
   if (const int rc = mx_check(x8)) return rc;
   if (x8->format != IBP_MX_E4M3) return IBP_ERR_INVALID_ARG;
   uint64_t yb, wgb;
-  if (!product_rows_ok(outs) || !matrix_bytes(x8->rows, outs, 2, &yb) ||
+  if (!product_rows_ok(outs) || !matrix_bytes(x8->rows, outs, dtype_size(dy_dtype), &yb) ||
       !matrix_bytes(outs, x8->cols, dtype_size(dw_dtype), &wgb))
     return IBP_ERR_SIZE;
   if (wgb == 0) return IBP_OK;
-  const uint64_t wb = mx_wgrad_workspace(x8->rows, (uint32_t)outs, (uint32_t)x8->cols);
+  const uint64_t wb = mx_wgrad_workspace(x8->rows, (uint32_t)outs, (uint32_t)x8->cols, dy_dtype);
   if (workspace_bytes < wb) return IBP_ERR_CAPACITY;
-  if (!d_dw || !aligned(d_dw, dtype_size(dw_dtype)) || (yb && !d_dy) || !aligned(d_dy, 2) || (wb && !d_workspace) ||
+  if (!d_dw || !aligned(d_dw, dtype_size(dw_dtype)) || (yb && !d_dy) || !aligned(d_dy, dtype_size(dy_dtype)) || (wb && !d_workspace) ||
       !aligned(d_workspace, 16))
     return IBP_ERR_INVALID_ARG;
   uint8_t *xc, *xs;
@@ -984,6 +984,7 @@ IBP_API int ibp_mx_linear_wgrad(const void *d_dy, int dy_dtype, uint64_t outs, c
   p.T = x8->rows;
   p.N = (uint32_t)outs;
   p.K = (uint32_t)x8->cols;
+  p.dy_dtype = dy_dtype;
   p.dtype = dw_dtype;
   return status_of(launch_mx_wgrad(p, static_cast<hipStream_t>(hip_stream)));
 }

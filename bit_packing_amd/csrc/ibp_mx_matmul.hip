@@ -143,7 +143,6 @@ template <bool A8, int MI> hipError_t go_direct(const MxMatmulArgs &a, hipStream
   const uint32_t steps = (uint32_t)((mx_blocks(a.K) + kStep - 1) / kStep);
   uint32_t waves = gx * gy < 512 ? 16 : 4;
   while (waves > 1 && waves > steps) waves /= 2;
-  if (gx > 0xFFFFFF || gy > 0xFFFF) return hipErrorInvalidValue;
   return with_dtype(a.dtype, [&](auto d) {
     mx_direct_kernel<A8, MI, d.value>
         <<<dim3((uint32_t)gx, (uint32_t)gy), waves * kWave, (waves - 1) * MI * 1024, s>>>(a);
@@ -398,7 +397,8 @@ Plan plan_of(uint64_t M, uint64_t N, uint32_t K) {
   Plan p{Plan::kDirect, 0, 0, 1, 1};
   // Few rows, or so few outputs that one round of the direct kernel's workgroups covers
   // them (8192 x 8192 weights: 16 rows 13 us against 15 for the tiles, 32 rows 21 against 15).
-  if (M <= 16 || ((M + 15) / 16) * ((N + 15) / 16) <= 512) return p;
+  const uint64_t blocks = ((M + 15) / 16) * ((N + 15) / 16);
+  if (blocks <= 512 || (M <= 16 && blocks <= 1u << 22)) return p;
   // Many rows: the larger tiles from 192 of them on (1536 x 8192 outputs, 4096 deep: 37 us
   // against 47; 1024 x 8192, 8192 deep, 128 large tiles: 62 against 56).
   const bool big = ((M + 255) / 256) * ((N + 255) / 256) >= 192;

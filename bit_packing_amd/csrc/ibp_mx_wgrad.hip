@@ -1,9 +1,11 @@
 // ibp_mx_wgrad.hip -- weight gradient of a linear layer from the 8-bit checkpoint of its
-// input: dW[o][i] = sum over tokens t of dY[t][o] X[t][i], dY in BF16, X packed as e4m3.
+// input: dW[o][i] = sum over tokens t of dY[t][o] X[t][i], X packed as e4m3.
 //
 // An e4m3 value times its power-of-two scale (at least 2^-117) is a BF16 number, so X
 // is decoded exactly to BF16 and the product runs on the BF16 matrix instruction with
-// 32-bit sums.  Both operands lie with t as the slow dimension, while the instruction
+// 32-bit sums.  A dY of another type is the sum of BF16 numbers, two for half precision's
+// 11 bits and three for single's 24, each the leading eight bits of what the ones before
+// leave; each part has its own ranges of the launch and is added like another range.  Both operands lie with t as the slow dimension, while the instruction
 // wants consecutive t in a lane: tiles are staged in LDS as they lie and read through
 // the transposing LDS read, which hands each of 16 lanes one column of a 4 x 16 block.
 #include "ibp_device.h"
@@ -50,6 +52,27 @@ __device__ __forceinline__ v8b decode8(v2u q, float f) {
   return v8b{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// Part `part` of eight elements as BF16: the leading eight bits of what the parts before
+// leave.  Cutting, not rounding, leaves the largest finite values finite, and the last
+// part holds all that is left.  Infinities and NaNs are in the first part alone.
+template <typename TY> __device__ __forceinline__ v8b part_of(Vec8<TY> y, uint32_t part) {
+  if constexpr (std::is_same<TY, __bf16>::value) {
+    return (v8b)y;
+  } else {
+    v8b out;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float rest = (float)y[i];
+      const bool finite = (__builtin_bit_cast(uint32_t, rest) & 0x7F800000u) != 0x7F800000u;
+      for (uint32_t p = 0; p < part; ++p) rest -= __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, rest) & 0xFFFF0000u);
+      // a NaN's payload may lie in the bits that are cut off
+      const float cut = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, rest) & 0xFFFF0000u);
+      out[i] = (__bf16)(finite ? cut : (part == 0 ? rest : 0.0f));
+    }
+    return out;
+  }
+}
+
 // A load that the compiler knows to be of global memory: from a pointer chosen between a
 // matrix and kZeros it would make a flat load, which LDS waits count too.
 template <typename T> __device__ __forceinline__ T from_global(const uint8_t *p) {
@@ -57,7 +80,8 @@ template <typename T> __device__ __forceinline__ T from_global(const uint8_t *p)
 }
 
 // A workgroup of WI x WO wavefronts computes 16 FI WI (i) by 16 FO WO (o) elements of dW
-// over the tokens [z * t_each, (z + 1) * t_each), z = blockIdx.y, into dst + z * N * K.
+// over the tokens [z * t_each, (z + 1) * t_each), z = blockIdx.y % splits, of part
+// blockIdx.y / splits of dY, into dst + blockIdx.y * N * K.
 //
 // Stages of 32 tokens lie in a ring of four.  dY comes by direct global-to-LDS loads three
 // stages ahead where its rows are aligned to 16 bytes (DIRECT), else through registers like
@@ -66,9 +90,11 @@ template <typename T> __device__ __forceinline__ T from_global(const uint8_t *p)
 // half multiplies (16384 x 4096 x 8192: 863 us, 1.27 PFLOP/s, against 1090 with all in
 // step and two stages of 64 tokens).  Bound by the phases: the matrix units are busy half
 // of the time, LDS a quarter.
-template <int WI, int WO, int FI, int FO, bool DIRECT, int DO>
+template <int WI, int WO, int FI, int FO, bool DIRECT, int DY, int DO>
 __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *dst, uint64_t t_each, uint32_t tiles_o,
-                                                           uint32_t tiles_i) {
+                                                           uint32_t tiles_i, uint32_t splits) {
+  using TY = typename Num<DY>::T;
+  static_assert(!DIRECT || DY == IBP_BF16, "");
   using TO = typename Num<DO>::T;
   constexpr uint32_t kWaves = WI * WO, kThreads = kWaves * 64, kWideI = 16 * FI * WI, kWideO = 16 * FO * WO;
   constexpr uint32_t kPiecesY = kT * kWideO / 8 / kThreads, kPiecesX = kT * kWideI / 8 / kThreads;
@@ -80,9 +106,10 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
   const TileId tile = tile_of(blockIdx.x, tiles_o, tiles_i);
   const uint32_t o0 = tile.row * kWideO, i0 = tile.col * kWideI;
   const uint32_t wi = (wave % WI) * FI, wo = (wave / WI) * FO;  // in blocks of 16
-  const uint64_t t0 = blockIdx.y * t_each, t1 = t0 + t_each < a.T ? t0 + t_each : a.T;
+  const uint32_t part = blockIdx.y / splits;
+  const uint64_t t0 = (blockIdx.y - part * splits) * t_each, t1 = t0 + t_each < a.T ? t0 + t_each : a.T;
   const uint32_t cp = (uint32_t)mx_code_pitch(a.K, true), sp = (uint32_t)mx_scale_pitch(a.K);
-  const __bf16 *dy = static_cast<const __bf16 *>(a.dy);
+  const TY *dy = static_cast<const TY *>(a.dy);
 
   // A thread's pieces lie at one column, so a pointer each for dY, codes and scales walks
   // over the tokens; past a row's end it stands still on zeros.
@@ -98,7 +125,7 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
   const uint8_t *px = in_x ? a.x_codes + (t0 + tx) * cp + cx : kZeros;
   const uint8_t *ps = in_x ? a.x_scales + (t0 + tx) * sp + cx / (4 * kMxBlock) * 4 : kZeros;  // its dword
   const uint32_t scale_shift = cx / kMxBlock % 4 * 8;
-  const uint64_t go_y = in_y ? (uint64_t)kStepY * a.N * 2 : 0, go_x = in_x ? (uint64_t)kStepX * cp : 0;
+  const uint64_t go_y = in_y ? (uint64_t)kStepY * a.N * sizeof(TY) : 0, go_x = in_x ? (uint64_t)kStepX * cp : 0;
   const uint64_t go_s = in_x ? (uint64_t)kStepX * sp : 0;
   const uint32_t at_x = kBytesY + tile_at<kWideI>(tx, sx);
 
@@ -115,7 +142,7 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
   struct Set {
     v2u q[kPiecesX];
     uint32_t s[kPiecesX];
-    Vec8<__bf16> y[DIRECT ? 1 : kPiecesY];
+    Vec8<TY> y[DIRECT ? 1 : kPiecesY];
   } set[2];
   // Loads of a stage; stages are asked for in order.  Their number never varies (zeros
   // past the last token), as the waits below count them.
@@ -132,7 +159,7 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
 #pragma unroll
       for (uint32_t p = 0; p < kPiecesY; ++p) {
         const uint8_t *from = stage * kT + ty + p * kStepY < tokens ? py : kZeros;
-        f.y[p] = wide ? from_global<Vec8<__bf16>>(from) : load8<false, __bf16>(reinterpret_cast<const __bf16 *>(from), 0, a.N);
+        f.y[p] = wide ? from_global<Vec8<TY>>(from) : load8<false, TY>(reinterpret_cast<const TY *>(from), 0, a.N);
         py += go_y;
       }
     }
@@ -151,7 +178,8 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
     if constexpr (!DIRECT) {
 #pragma unroll
       for (uint32_t p = 0; p < kPiecesY; ++p)
-        *reinterpret_cast<v8b *>(st + (p * kThreads + threadIdx.x) * 16) = (v8b)(wide ? settle8<true, __bf16>(f.y[p], cy, a.N) : settle8<false, __bf16>(f.y[p], cy, a.N));
+        *reinterpret_cast<v8b *>(st + (p * kThreads + threadIdx.x) * 16) =
+            part_of<TY>(wide ? settle8<true, TY>(f.y[p], cy, a.N) : settle8<false, TY>(f.y[p], cy, a.N), part);
     }
 #pragma unroll
     for (uint32_t p = 0; p < kPiecesX; ++p)
@@ -258,18 +286,21 @@ struct Plan {
   bool big;
   uint32_t tiles_o, tiles_i;
   uint32_t splits;
+  uint32_t parts;  // of dY
   uint64_t t_each;
 };
 
-Plan plan_of(uint64_t T, uint32_t N, uint32_t K) {
+Plan plan_of(uint64_t T, uint32_t N, uint32_t K, int dy_dtype) {
   Plan p;
+  p.parts = dy_dtype == IBP_BF16 ? 1 : dy_dtype == IBP_F16 ? 2 : 3;
   const uint64_t big = (((uint64_t)N + 255) / 256) * (((uint64_t)K + 255) / 256);
-  p.big = T >= 1024 && big * ((T + 511) / 512) >= 256;
+  // other types' pieces in flight leave no registers for the large tile
+  p.big = p.parts == 1 && T >= 1024 && big * ((T + 511) / 512) >= 256;
   const uint32_t wide = p.big ? 256 : 128;
   p.tiles_o = (uint32_t)(((uint64_t)N + wide - 1) / wide);
   p.tiles_i = (uint32_t)(((uint64_t)K + wide - 1) / wide);
   const uint64_t tiles = (uint64_t)p.tiles_o * p.tiles_i, least = p.big ? 512 : 256;
-  const uint64_t want = 256 / tiles, most = (T + least - 1) / least;
+  const uint64_t want = 256 / (tiles * p.parts), most = (T + least - 1) / least;
   uint64_t n = want < most ? want : most;
   n = n < 1 ? 1 : (n > 32 ? 32 : n);
   p.t_each = ((T + n - 1) / n + kT - 1) / kT * kT;
@@ -280,35 +311,42 @@ Plan plan_of(uint64_t T, uint32_t N, uint32_t K) {
 
 template <int DO> hipError_t go(const MxWgradArgs &a, const Plan &p, void *dst, hipStream_t s) {
   const bool direct = a.N % 8 == 0 && (uintptr_t)a.dy % 16 == 0;
-  const dim3 grid(p.tiles_o * p.tiles_i, p.splits);
-  if (p.big && direct)
-    wgrad_kernel<2, 4, 8, 4, true, DO><<<grid, 512, 0, s>>>(a, dst, p.t_each, p.tiles_o, p.tiles_i);
-  else if (p.big)
-    wgrad_kernel<2, 4, 8, 4, false, DO><<<grid, 512, 0, s>>>(a, dst, p.t_each, p.tiles_o, p.tiles_i);
-  else if (direct)
-    wgrad_kernel<2, 2, 4, 4, true, DO><<<grid, 256, 0, s>>>(a, dst, p.t_each, p.tiles_o, p.tiles_i);
-  else
-    wgrad_kernel<2, 2, 4, 4, false, DO><<<grid, 256, 0, s>>>(a, dst, p.t_each, p.tiles_o, p.tiles_i);
-  return hipGetLastError();
+  const dim3 grid(p.tiles_o * p.tiles_i, p.splits * p.parts);
+  auto launch = [&](auto kernel, uint32_t threads) {
+    kernel<<<grid, threads, 0, s>>>(a, dst, p.t_each, p.tiles_o, p.tiles_i, p.splits);
+    return hipGetLastError();
+  };
+  if constexpr (DO == IBP_F32) {  // parts are always joined
+    if (a.dy_dtype == IBP_F16) return launch(wgrad_kernel<2, 2, 4, 4, false, IBP_F16, DO>, 256);
+    if (a.dy_dtype == IBP_F32) return launch(wgrad_kernel<2, 2, 4, 4, false, IBP_F32, DO>, 256);
+  }
+  if (p.big)
+    return direct ? launch(wgrad_kernel<2, 4, 8, 4, true, IBP_BF16, DO>, 512)
+                  : launch(wgrad_kernel<2, 4, 8, 4, false, IBP_BF16, DO>, 512);
+  return direct ? launch(wgrad_kernel<2, 2, 4, 4, true, IBP_BF16, DO>, 256)
+                : launch(wgrad_kernel<2, 2, 4, 4, false, IBP_BF16, DO>, 256);
 }
 
 }  // namespace
 
-uint64_t mx_wgrad_workspace(uint64_t T, uint32_t N, uint32_t K) {
-  const Plan p = plan_of(T, N, K);
-  return p.splits > 1 ? (uint64_t)p.splits * N * K * 4 : 0;
+uint64_t mx_wgrad_workspace(uint64_t T, uint32_t N, uint32_t K, int dy_dtype) {
+  const Plan p = plan_of(T, N, K, dy_dtype);
+  const uint64_t n = (uint64_t)p.splits * p.parts;
+  return n > 1 ? n * N * K * 4 : 0;
 }
 
 hipError_t launch_mx_wgrad(const MxWgradArgs &a, hipStream_t s) {
-  const Plan p = plan_of(a.T, a.N, a.K);
-  if (p.splits > 1) {
+  const Plan p = plan_of(a.T, a.N, a.K, a.dy_dtype);
+  if (p.t_each > 0x7FFFFFFFull) return hipErrorInvalidValue;
+  const uint32_t pieces = p.splits * p.parts;
+  if (pieces > 1) {
     const hipError_t e = go<IBP_F32>(a, p, a.ws, s);
     if (e != hipSuccess) return e;
   }
   return with_dtype(a.dtype, [&](auto d) {
-    if (p.splits == 1) return go<d.value>(a, p, a.dw, s);
+    if (pieces == 1) return go<d.value>(a, p, a.dw, s);
     const uint64_t n = ((uint64_t)a.N * a.K + kBlock * 4 - 1) / (kBlock * 4);
-    wgrad_join_kernel<d.value><<<(uint32_t)(n < 4096 ? n : 4096), kBlock, 0, s>>>(a, p.splits);
+    wgrad_join_kernel<d.value><<<(uint32_t)(n < 4096 ? n : 4096), kBlock, 0, s>>>(a, pieces);
     return hipGetLastError();
   });
 }

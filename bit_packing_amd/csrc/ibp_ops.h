@@ -70,15 +70,16 @@ struct MxMatmulArgs {
 uint64_t mx_matmul_workspace(uint64_t M, uint64_t N, uint32_t K, bool a_e4m3);
 
 struct MxWgradArgs {
-  const void *dy;                     // T x N, BF16
+  const void *dy;                     // T x N
   const uint8_t *x_codes, *x_scales;  // T rows of K, e4m3
   void *dw;                           // N x K
   float *ws;
   uint64_t T;
   uint32_t N, K;
+  int dy_dtype;
   int dtype;
 };
-uint64_t mx_wgrad_workspace(uint64_t T, uint32_t N, uint32_t K);
+uint64_t mx_wgrad_workspace(uint64_t T, uint32_t N, uint32_t K, int dy_dtype);
 
 // Launchers.  Each returns the hipError_t of its launch(es).
 hipError_t launch_lookup(const LookupArgs &a, hipStream_t s);  // ibp_embed.hip

@@ -7,8 +7,9 @@
 namespace ibp {
 namespace dev {
 
-// Source of the loads that stand for bytes past a row's or a matrix's end.
-static __device__ __align__(16) const uint8_t kZeros[16] = {};
+// Source of the loads that stand for bytes past a row's or a matrix's end, as long as the
+// longest of them (eight floats).
+static __device__ __align__(32) const uint8_t kZeros[32] = {};
 
 typedef __attribute__((address_space(3))) void lds_void;
 typedef const __attribute__((address_space(1))) void global_void;

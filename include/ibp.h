@@ -431,11 +431,13 @@ IBP_API int ibp_mx_swiglu_backward(const void *d_dh, int dtype, const ibp_mx_t *
 
 /* Workspaces of the two products (0 where the shape needs none). */
 IBP_API uint64_t ibp_mx_matmul_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, uint32_t a_format);
-IBP_API uint64_t ibp_mx_linear_wgrad_workspace_bytes(uint64_t tokens, uint64_t outs, uint64_t ins);
+IBP_API uint64_t ibp_mx_linear_wgrad_workspace_bytes(uint64_t tokens, uint64_t outs, uint64_t ins, int dy_dtype);
 
 /*
  * Product with packed weights: d_y[i][j] = sum over k of a[i][k] * b[j][k], a of M rows
- * (e4m3 or e2m1), b of N rows (e2m1), a->cols == b->cols, d_y M x N of dtype.
+ * (e4m3 or e2m1), b of N rows (e2m1), a->cols == b->cols, d_y M x N of dtype.  Sums
+ * are held in 32 bits; for a 16-bit d_y the products of an e4m3 block are added with
+ * what lies 14 binary places below the block's largest cut off (4.5e-6 of the result).
  * d_workspace may be NULL when the query says 0; aligned to 16.  Asynchronous.
  */
 IBP_API int ibp_mx_matmul(const ibp_mx_t *a, const ibp_mx_t *b, void *d_y, int dtype, void *d_workspace,
@@ -443,9 +445,10 @@ IBP_API int ibp_mx_matmul(const ibp_mx_t *a, const ibp_mx_t *b, void *d_y, int d
 
 /*
  * Weight gradient of a linear layer from the 8-bit checkpoint of its input:
- * d_dw[o][i] = sum over t of d_dy[t][o] * x8[t][i], d_dy x8->rows x outs of dy_dtype
- * (IBP_BF16), x8 in e4m3, d_dw outs x x8->cols of dw_dtype.  x8 is decoded exactly
- * (every e4m3 value times its scale is a BF16 number for scale bytes of 10 to 246).
+ * d_dw[o][i] = sum over t of d_dy[t][o] * x8[t][i], d_dy x8->rows x outs of dy_dtype,
+ * x8 in e4m3, d_dw outs x x8->cols of dw_dtype.  Both are taken exactly (every e4m3
+ * value times its scale is a BF16 number for scale bytes of 10 to 246; a half or single
+ * precision d_dy is two or three BF16 numbers, and takes that much longer).
  * Asynchronous.
  */
 IBP_API int ibp_mx_linear_wgrad(const void *d_dy, int dy_dtype, uint64_t outs, const ibp_mx_t *x8, void *d_dw,

@@ -380,15 +380,29 @@ def test_wgrad_is_exact_where_32_bits_are(ibp, t, n, k):
     assert np.array_equal(host(dw), want)
 
 
+@pytest.mark.parametrize("ty", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("to", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("t,n,k", [(50, 70, 90), (2000, 130, 100)])
-def test_wgrad(ibp, to, t, n, k):
+@pytest.mark.parametrize("t,n,k", [(50, 70, 90), (2000, 130, 100), (37, 5, 64)])
+def test_wgrad(ibp, ty, to, t, n, k):
     rng = np.random.default_rng(t)
-    dy, x = gpu(rng.standard_normal((t, n)) * 0.1, "bf16"), packed(ibp, rng.standard_normal((t, k)) * 3, mx_ref.E4M3)
+    dy, x = gpu(rng.standard_normal((t, n)) * 0.1, ty), packed(ibp, rng.standard_normal((t, k)) * 3, mx_ref.E4M3)
     v = mx_ref.unpack(x.codes.cpu().numpy(), x.scales.cpu().numpy(), k, mx_ref.E4M3)
     want, mag = host(dy).T @ v, np.abs(host(dy)).T @ np.abs(v)
     got = ibp.ibp_mx_linear_wgrad(dy, x, dw_dtype=DT[to])
     within(host(got), want, np.abs(want) * half(to) + mag * t * U + TINY[to])
+
+
+def test_wgrad_takes_single_precision_whole(ibp):
+    """One token: each output is one product of 24 and 4 bits, rounded to 32; the largest
+    values, infinities and NaNs (whatever bits they carry) stay what they are."""
+    x = packed(ibp, np.array([[1.0, 1.875, -0.5] + [0.0] * 29]), mx_ref.E4M3)
+    dy = torch.tensor([[1 + 2.0 ** -23, 3.0e38, -torch.finfo(torch.float32).max, 2.0 ** -100, float("inf"), float("nan")]])
+    dy = torch.cat([dy, torch.tensor([0x7F800001], dtype=torch.int32).view(torch.float32)[None]], 1).cuda()
+    got = host(ibp.ibp_mx_linear_wgrad(dy, x))[:, :3]
+    want = (dy[0, :, None] * torch.tensor([1.0, 1.875, -0.5], device="cuda")).double().cpu().numpy()
+    fine = np.isfinite(want)
+    assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(got[np.isinf(want)], want[np.isinf(want)])
+    assert np.all(np.abs(got[fine] - want[fine]) <= 4 * U * np.abs(want[fine]))
 
 
 def test_wgrad_of_small_and_nan_values(ibp):
@@ -449,6 +463,22 @@ def test_side_stream_and_graph_replays(ibp, n):
         want = step(ibp, s)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want)), k
+
+
+def test_the_stream_argument(ibp):
+    """A call given a stream runs there and its outputs belong there."""
+    s = state(ibp, 700, 4)
+    want = ibp.ibp_embedding_grad(ibp.ibp_embedding_lookup(s["table"], s["ids"]), s["ids"], 500)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (side, side.cuda_stream):
+        x = ibp.ibp_embedding_lookup(s["table"], s["ids"], stream=stream)
+        got = ibp.ibp_embedding_grad(x, s["ids"], 500, stream=stream)
+        m = ibp.ibp_mx_pack(x, ibp.IBP_MX_E2M1, stream=stream)
+        y = ibp.ibp_mx_matmul(m, m, stream=stream)
+        side.synchronize()
+        assert torch.equal(got, want)
+        assert torch.equal(y, ibp.ibp_mx_matmul(m, m))
 
 
 def test_device_refusals(ibp):

@@ -49,6 +49,11 @@ def test_workspace_queries(ibp):
     assert ibp.ibp_mx_matmul_workspace_bytes(0, 10, 32, 0) == 0
     assert ibp.ibp_mx_matmul_workspace_bytes(10, 10, 32, 7) == 0
     assert ibp.ibp_mx_linear_wgrad_workspace_bytes(10, 0, 32) == 0
+    lib = ibp.load_library()
+    assert lib.ibp_mx_linear_wgrad_workspace_bytes(10, 8, 32, 7) == 0
+    assert lib.ibp_mx_linear_wgrad_workspace_bytes(10, 8, 32, BF16) == 0  # one range, written as it is
+    assert lib.ibp_mx_linear_wgrad_workspace_bytes(10, 8, 32, F16) == 2 * 8 * 32 * 4
+    assert lib.ibp_mx_linear_wgrad_workspace_bytes(10, 8, 32, F32) == 3 * 8 * 32 * 4
 
 
 def test_lookup_refusals(ibp):
@@ -135,7 +140,9 @@ def test_product_refusals(ibp):
     assert lib.ibp_mx_matmul(ref(a), ref(w), None, F32, None, 0, None) == ibp.IBP_ERR_INVALID_ARG
     assert lib.ibp_mx_matmul(ref(a), ref(w), FAKE, F32, FAKE + 4, 0, None) == ibp.IBP_ERR_INVALID_ARG
     assert lib.ibp_mx_matmul(ref(mx(ibp, rows=(1 << 30) + 1)), ref(w), FAKE, F32, None, 0, None) == ibp.IBP_ERR_SIZE
-    assert lib.ibp_mx_linear_wgrad(FAKE, F32, 8, ref(a), FAKE, F32, None, 0, None) == ibp.IBP_ERR_INVALID_ARG  # dy not bf16
+    assert lib.ibp_mx_linear_wgrad(FAKE, 3, 8, ref(a), FAKE, F32, None, 0, None) == ibp.IBP_ERR_INVALID_ARG
+    assert lib.ibp_mx_linear_wgrad(FAKE, F32, 8, ref(a), FAKE, F32, None, 0, None) == ibp.IBP_ERR_CAPACITY  # its parts are joined
+    assert lib.ibp_mx_linear_wgrad(FAKE + 1, BF16, 8, ref(a), FAKE, F32, None, 0, None) == ibp.IBP_ERR_INVALID_ARG
     assert lib.ibp_mx_linear_wgrad(FAKE, BF16, 8, ref(w), FAKE, F32, None, 0, None) == ibp.IBP_ERR_INVALID_ARG  # x8 not e4m3
     assert lib.ibp_mx_linear_wgrad(FAKE, BF16, (1 << 30) + 1, ref(a), FAKE, F32, None, 0, None) == ibp.IBP_ERR_SIZE
     assert lib.ibp_mx_linear_wgrad(None, BF16, 8, ref(a), FAKE, F32, None, 0, None) == ibp.IBP_ERR_INVALID_ARG
