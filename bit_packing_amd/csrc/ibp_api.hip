@@ -916,7 +916,7 @@ static bool product_rows_ok(uint64_t n) { return n <= IBP_MAX_COLS; }
 
 IBP_API uint64_t ibp_mx_matmul_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, uint32_t a_format) {
   if (!product_rows_ok(m) || !product_rows_ok(n) || k > IBP_MAX_COLS || a_format > IBP_MX_E2M1) return 0;
-  return m && n ? mx_matmul_workspace(m, n, (uint32_t)k, a_format == IBP_MX_E4M3) : 0;
+  return m && n ? mx_matmul_workspace(m, n, (uint32_t)k) : 0;
 }
 
 IBP_API uint64_t ibp_mx_linear_wgrad_workspace_bytes(uint64_t tokens, uint64_t outs, uint64_t ins, int dy_dtype) {
@@ -935,7 +935,7 @@ IBP_API int ibp_mx_matmul(const ibp_mx_t *a, const ibp_mx_t *b, void *d_y, int d
       !matrix_bytes(a->rows, b->rows, dtype_size(dtype), &yb))
     return IBP_ERR_SIZE;
   if (yb == 0) return IBP_OK;
-  const uint64_t wb = mx_matmul_workspace(a->rows, b->rows, (uint32_t)a->cols, a->format == IBP_MX_E4M3);
+  const uint64_t wb = mx_matmul_workspace(a->rows, b->rows, (uint32_t)a->cols);
   if (workspace_bytes < wb) return IBP_ERR_CAPACITY;
   if (!d_y || !aligned(d_y, dtype_size(dtype)) || (wb && !d_workspace) || !aligned(d_workspace, 16))
     return IBP_ERR_INVALID_ARG;

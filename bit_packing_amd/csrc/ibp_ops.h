@@ -67,7 +67,7 @@ struct MxMatmulArgs {
   bool a_e4m3;
   int dtype;
 };
-uint64_t mx_matmul_workspace(uint64_t M, uint64_t N, uint32_t K, bool a_e4m3);
+uint64_t mx_matmul_workspace(uint64_t M, uint64_t N, uint32_t K);
 
 struct MxWgradArgs {
   const void *dy;                     // T x N
