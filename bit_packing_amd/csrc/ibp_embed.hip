@@ -92,7 +92,7 @@ template <int DI, int DO, uint32_t R> __global__ __launch_bounds__(kBlock) void 
 constexpr uint32_t kDigitBits = 9, kBins = 1u << kDigitBits;
 constexpr uint32_t kSortBlocks = 256;     // at most this many workgroups a pass
 constexpr uint32_t kSortMin = 1024;       // tokens per workgroup at least
-constexpr uint32_t kSmallTokens = 4096;   // sorted by one workgroup in LDS
+constexpr uint32_t kSmallTokens = 8192;   // sorted by one workgroup in LDS
 constexpr uint32_t kSmallThreads = 1024;
 
 struct Pair { uint32_t key, pos; };
@@ -223,8 +223,8 @@ template <bool FIRST> __global__ __launch_bounds__(kBlock) void sort_scatter_ker
   }
 }
 
-// The whole sort of up to kSmallTokens tokens in one workgroup, pairs in LDS.  Further
-// workgroups clear `clear` (n_clear elements) meanwhile.
+// The whole sort of up to kSmallTokens tokens in one workgroup, keys and positions in LDS.
+// Further workgroups clear `clear` (n_clear elements) meanwhile.
 template <int DO>
 __global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(SortArgs a, uint32_t passes, uint32_t total_bits,
                                                                    void *clear, uint64_t n_clear) {
@@ -244,19 +244,24 @@ __global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(SortArgs a, u
     return;
   }
   constexpr uint32_t kWaves = kSmallThreads / kWave;
-  __shared__ Pair buf[2][kSmallTokens];
+  __shared__ uint32_t keys[2][kSmallTokens];
+  __shared__ uint16_t pos[2][kSmallTokens];
+  static_assert(kSmallTokens <= 1u << 16, "positions in 16 bits");
   __shared__ uint32_t off[kWaves][kBins];
   __shared__ uint32_t wave_total[kWaves];
   const uint32_t t = threadIdx.x, wave = uniform(t / kWave), lane = lane_id();
   if (t == 0) a.crossing[0] = 0;
-  for (uint32_t j = t; j < a.n; j += kSmallThreads) buf[0][j] = Pair{key_of(a, j), j};
+  for (uint32_t j = t; j < a.n; j += kSmallThreads) {
+    keys[0][j] = key_of(a, j);
+    pos[0][j] = (uint16_t)j;
+  }
   const uint32_t w0 = wave * a.per_wave, w1 = w0 + a.per_wave, end = w1 < a.n ? w1 : a.n;
   uint32_t shift = 0, cur = 0;
   for (uint32_t pass = 0; pass < passes; ++pass) {
     const uint32_t bits = total_bits - shift < a.bits ? total_bits - shift : a.bits, dm = (1u << bits) - 1u;
     for (uint32_t i = t; i < kBins * kWaves; i += kSmallThreads) (&off[0][0])[i] = 0;
     __syncthreads();
-    for (uint32_t j = w0 + lane; j < end; j += kWave) atomicAdd(&off[wave][(buf[cur][j].key >> shift) & dm], 1u);
+    for (uint32_t j = w0 + lane; j < end; j += kWave) atomicAdd(&off[wave][(keys[cur][j] >> shift) & dm], 1u);
     __syncthreads();
     // thread d < kBins owns digit d
     uint32_t mine = 0;
@@ -278,8 +283,9 @@ __global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(SortArgs a, u
     for (uint32_t j0 = w0; j0 < end; j0 += kWave) {
       const uint32_t j = j0 + lane;
       const bool live = j < end;
-      const Pair p = live ? buf[cur][j] : Pair{0u, 0u};
-      const uint32_t d = (p.key >> shift) & dm;
+      const uint32_t key = live ? keys[cur][j] : 0u;
+      const uint16_t at_j = live ? pos[cur][j] : 0;
+      const uint32_t d = (key >> shift) & dm;
       const uint64_t same = same_digit(d, bits, ballot(live));
       const uint32_t rank = count_below(same);
       uint32_t at = 0;
@@ -287,13 +293,16 @@ __global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(SortArgs a, u
       wave_lds_sync();
       if (live && rank == 0) off[wave][d] += popc(same);
       wave_lds_sync();
-      if (live) buf[cur ^ 1][at] = p;
+      if (live) {
+        keys[cur ^ 1][at] = key;
+        pos[cur ^ 1][at] = at_j;
+      }
     }
     __syncthreads();
     cur ^= 1;
     shift += bits;
   }
-  for (uint32_t j = t; j < a.n; j += kSmallThreads) a.to[j] = buf[cur][j];
+  for (uint32_t j = t; j < a.n; j += kSmallThreads) a.to[j] = Pair{keys[cur][j], pos[cur][j]};
 }
 
 // ------------------------------------------------------------------ sums of the sorted rows
@@ -486,7 +495,7 @@ template <int DO> __global__ __launch_bounds__(kBlock) void grad_join_kernel(Sum
 // after another; long ones amortise the partial rows (two 32-bit rows a chunk at most).
 // Chunks of 8, 16 and 32, frequent ids, 32000 rows, single precision gradients: 4000 tokens
 // of 1000 31.1, 33.2 and 38.7 us; 16384 of 1024 73.9, 70.2, 75.1; 32768 of 4096 250, 229, 215.
-uint32_t grad_chunk(uint64_t n) { return n <= kSmallTokens ? 8 : n < 32768 ? 16 : 32; }
+uint32_t grad_chunk(uint64_t n) { return n <= 4096 ? 8 : n < 32768 ? 16 : 32; }
 
 uint64_t up16(uint64_t v) { return (v + 15) & ~15ull; }
 
@@ -548,20 +557,22 @@ hipError_t launch_embed_grad(const EmbedGradArgs &a, hipStream_t s) {
   const uint32_t passes = (total_bits + kDigitBits - 1) / kDigitBits;
   so.bits = (total_bits + passes - 1) / passes;
   so.shift = 0;
-  // With few tokens for the rows, the sort (one workgroup) hides behind clearing every
-  // row, at the cost of writing the tokens' rows twice; else only rows without tokens
-  // are cleared, by the summing kernel.
-  const bool clear_first = a.n_ids <= kSmallTokens && a.n_ids * 4 <= a.n_rows;
+  // One workgroup can sort up to kSmallTokens while others clear every row: that writes the
+  // tokens' rows twice, but takes one kernel and hides the sort.  Else the summing kernel
+  // clears the rows without tokens.  4000 tokens of 1000, frequent ids, 16000 rows: 28 us, with
+  // this sort and clearing by sums 42, with many workgroups' sort 47; 4000 rows: 26, 29, 33.
+  // Above 4096 tokens one workgroup sorts slower than many, so there has to be enough to
+  // clear: 8192 tokens of 4096, 8000 rows (131 MB): 70 us against 84 by many, of 1000, 8000
+  // rows (32 MB): 40 against 40, of 64, 32000 rows (8 MB): 40 against 36.
+  const uint64_t grad_bytes = a.n_rows * a.dim * (a.out_dtype == IBP_F32 ? 4 : 2);
+  const bool clear_first = a.n_ids <= 4096 || (a.n_ids <= kSmallTokens && grad_bytes >= 32u << 20);
   hipError_t e = hipSuccess;
   const Pair *sorted = pa;
-  if (a.n_ids <= kSmallTokens) {
+  if (clear_first) {
     const uint32_t per = (so.n + kSmallThreads - 1) / kSmallThreads;
     so.per_wave = (per ? per : 1) * kWave;
-    uint32_t clearers = 0;
-    if (clear_first) {
-      const uint64_t want = (a.n_rows * a.dim + kSmallThreads * 8 - 1) / (kSmallThreads * 8);
-      clearers = (uint32_t)(want < 512 ? want : 512);
-    }
+    const uint64_t want = (a.n_rows * a.dim + kSmallThreads * 8 - 1) / (kSmallThreads * 8);
+    const uint32_t clearers = (uint32_t)(want < 512 ? want : 512);
     e = with_dtype(a.out_dtype, [&](auto d) {
       sort_small_kernel<d.value><<<1 + clearers, kSmallThreads, 0, s>>>(so, passes, total_bits, a.grad, a.n_rows * a.dim);
       return hipGetLastError();

@@ -122,6 +122,7 @@ def check_grad(ibp, ids, rows, dim, ti="f32", to="f32", scale=1.0, padding=-1, s
 
 @pytest.mark.parametrize("n,rows,dim", [(1, 1, 1), (1, 500, 8), (63, 7, 5), (64, 64, 64), (65, 3, 130), (1000, 511, 24),
                                         (2047, 512, 40), (4096, 513, 16), (4097, 100000, 9), (5000, 1, 33),
+                                        (8192, 100000, 96), (8191, 90000, 101), (8193, 90000, 101), (20000, 777, 65),
                                         (33000, 40, 17), (40000, 300000, 8), (3, 5, 4100)])
 def test_grad_sizes(ibp, n, rows, dim):
     rng = np.random.default_rng(n + rows)
