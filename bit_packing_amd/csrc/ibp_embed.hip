@@ -93,7 +93,7 @@ constexpr uint32_t kDigitBits = 9, kBins = 1u << kDigitBits;
 constexpr uint32_t kSortBlocks = 256;     // at most this many workgroups a pass
 constexpr uint32_t kSortMin = 1024;       // tokens per workgroup at least
 constexpr uint32_t kSmallTokens = 8192;   // sorted by one workgroup in LDS
-constexpr uint32_t kSmallThreads = 1024;
+constexpr uint32_t kSortThreads = 1024, kSortWaves = kSortThreads / kWave;
 
 struct Pair { uint32_t key, pos; };
 
@@ -131,110 +131,125 @@ __device__ __forceinline__ uint64_t same_digit(uint32_t d, uint32_t bits, uint64
 }
 
 // Per workgroup, how many of its tokens have each digit.
-template <bool FIRST> __global__ __launch_bounds__(kBlock) void sort_count_kernel(SortArgs a) {
+template <bool FIRST> __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
   __shared__ uint32_t hist[kBins];
-  for (uint32_t i = threadIdx.x; i < kBins; i += kBlock) hist[i] = 0;
+  if (threadIdx.x < kBins) hist[threadIdx.x] = 0;
   if constexpr (FIRST) {
     if (blockIdx.x == 0 && threadIdx.x == 0) a.crossing[0] = 0;
   }
   __syncthreads();
-  const uint64_t b0 = (uint64_t)blockIdx.x * a.per_wave * kWavesPerBlock;
-  const uint64_t b1 = b0 + (uint64_t)a.per_wave * kWavesPerBlock;
+  const uint64_t b0 = (uint64_t)blockIdx.x * a.per_wave * kSortWaves;
+  const uint64_t b1 = b0 + (uint64_t)a.per_wave * kSortWaves;
   const uint32_t end = (uint32_t)(b1 < a.n ? b1 : a.n);
-  for (uint64_t j = b0 + threadIdx.x; j < end; j += kBlock) {
+  for (uint64_t j = b0 + threadIdx.x; j < end; j += kSortThreads) {
     const uint32_t key = FIRST ? key_of(a, (uint32_t)j) : a.from[j].key;
     atomicAdd(&hist[(key >> a.shift) & ((1u << a.bits) - 1u)], 1u);
   }
   __syncthreads();
-  for (uint32_t i = threadIdx.x; i < kBins; i += kBlock) a.counts[blockIdx.x * kBins + i] = hist[i];
+  if (threadIdx.x < kBins) a.counts[blockIdx.x * kBins + threadIdx.x] = hist[threadIdx.x];
 }
 
 // Moves each token to its place: the tokens of smaller digits, then those of the same
-// digit in earlier workgroups, earlier wavefronts and earlier in the wavefront.
-template <bool FIRST> __global__ __launch_bounds__(kBlock) void sort_scatter_kernel(SortArgs a) {
-  __shared__ uint32_t off[kWavesPerBlock][kBins];
-  __shared__ uint32_t wave_total[kWavesPerBlock];
-  const uint32_t wave = uniform(threadIdx.x / kWave), lane = lane_id();
-  for (uint32_t i = threadIdx.x; i < kBins * kWavesPerBlock; i += kBlock) (&off[0][0])[i] = 0;
-  __syncthreads();
-  const uint64_t w0 = ((uint64_t)blockIdx.x * kWavesPerBlock + wave) * a.per_wave;
+// digit in earlier workgroups, earlier wavefronts and earlier in the wavefront.  Sixteen
+// wavefronts a workgroup, for a wavefront's tokens go 64 at a time, one after another, and
+// the workgroups' counts are added by four threads a pair of digits.
+template <bool FIRST> __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortArgs a) {
+  constexpr uint32_t kPairs = kBins / 2, kShares = kSortThreads / kPairs;
+  __shared__ uint32_t off[kSortWaves][kBins];
+  __shared__ uint32_t total[kShares][kBins], before[kShares][kBins];
+  __shared__ uint32_t wave_total[kSortWaves];
+  const uint32_t t = threadIdx.x, wave = uniform(t / kWave), lane = lane_id();
+  const uint64_t w0 = ((uint64_t)blockIdx.x * kSortWaves + wave) * a.per_wave;
   const uint64_t w1 = w0 + a.per_wave;
   const uint64_t end = w1 < a.n ? w1 : a.n;
   const uint32_t dm = (1u << a.bits) - 1u;
-  for (uint64_t j = w0 + lane; j < end; j += kWave) {
-    const uint32_t key = FIRST ? key_of(a, (uint32_t)j) : a.from[j].key;
-    atomicAdd(&off[wave][(key >> a.shift) & dm], 1u);
+  auto load = [&](uint64_t j) {
+    Pair p{0u, (uint32_t)j};
+    if (j < end) {
+      if constexpr (FIRST) p.key = key_of(a, (uint32_t)j);
+      else p = a.from[j];
+    }
+    return p;
+  };
+  const Pair first = load(w0 + lane);
+  {
+    // tokens of each digit in all workgroups and in earlier ones, a share of the workgroups
+    uint2 sum = make_uint2(0u, 0u), early = make_uint2(0u, 0u);
+    const uint32_t pair = t % kPairs, share = t / kPairs;
+    const uint2 *counts = reinterpret_cast<const uint2 *>(a.counts) + pair;
+    constexpr uint32_t kFlight = 16;  // loads in flight: the counts come from L2
+    for (uint32_t b0 = share; b0 < gridDim.x; b0 += kFlight * kShares) {
+      uint2 v[kFlight];
+#pragma unroll
+      for (uint32_t k = 0; k < kFlight; ++k)
+        v[k] = b0 + k * kShares < gridDim.x ? counts[(b0 + k * kShares) * kPairs] : make_uint2(0u, 0u);
+#pragma unroll
+      for (uint32_t k = 0; k < kFlight; ++k) {
+        sum.x += v[k].x;
+        sum.y += v[k].y;
+        early.x += b0 + k * kShares < blockIdx.x ? v[k].x : 0u;
+        early.y += b0 + k * kShares < blockIdx.x ? v[k].y : 0u;
+      }
+    }
+    *reinterpret_cast<uint2 *>(&total[share][pair * 2]) = sum;
+    *reinterpret_cast<uint2 *>(&before[share][pair * 2]) = early;
   }
-  // totals of each digit, and its tokens in earlier workgroups; two digits a thread
-  constexpr uint32_t kEach = kBins / kBlock;
-  static_assert(kEach == 2, "a thread reads its digits' counts as pairs");
-  uint32_t total[kEach] = {}, before[kEach] = {};
-  const uint2 *counts = reinterpret_cast<const uint2 *>(a.counts) + threadIdx.x;
-  constexpr uint32_t kFlight = 16;  // loads in flight: the counts come from L2
-  for (uint32_t b0 = 0; b0 < gridDim.x; b0 += kFlight) {
-    uint2 v[kFlight];
+  for (uint32_t i = t; i < kBins * kSortWaves; i += kSortThreads) (&off[0][0])[i] = 0;
+  __syncthreads();
+  if (w0 + lane < end) atomicAdd(&off[wave][(first.key >> a.shift) & dm], 1u);
+  for (uint64_t j = w0 + kWave + lane; j < end; j += kWave) atomicAdd(&off[wave][(load(j).key >> a.shift) & dm], 1u);
+  // thread d < kBins owns digit d
+  uint32_t mine = 0, at = 0;
+  if (t < kBins) {
 #pragma unroll
-    for (uint32_t k = 0; k < kFlight; ++k)
-      v[k] = b0 + k < gridDim.x ? counts[(b0 + k) * (kBins / 2)] : make_uint2(0u, 0u);
-#pragma unroll
-    for (uint32_t k = 0; k < kFlight; ++k) {
-      total[0] += v[k].x;
-      total[1] += v[k].y;
-      before[0] += b0 + k < blockIdx.x ? v[k].x : 0u;
-      before[1] += b0 + k < blockIdx.x ? v[k].y : 0u;
+    for (uint32_t k = 0; k < kShares; ++k) {
+      mine += total[k][t];
+      at += before[k][t];
     }
   }
-  uint32_t mine = 0;
-#pragma unroll
-  for (uint32_t e = 0; e < kEach; ++e) mine += total[e];
   const uint32_t incl = wave_incl_scan(mine);
   if (lane == kWave - 1) wave_total[wave] = incl;
   __syncthreads();
-  uint32_t base = incl - mine;
-  for (uint32_t w = 0; w < wave; ++w) base += wave_total[w];
+  if (t < kBins) {
+    at += incl - mine;
+    for (uint32_t w = 0; w < wave; ++w) at += wave_total[w];
+    uint32_t c[kSortWaves];
 #pragma unroll
-  for (uint32_t e = 0; e < kEach; ++e) {
-    uint32_t at = base + before[e];
-    base += total[e];
-    for (uint32_t w = 0; w < kWavesPerBlock; ++w) {
-      const uint32_t c = off[w][threadIdx.x * kEach + e];
-      off[w][threadIdx.x * kEach + e] = at;
-      at += c;
+    for (uint32_t w = 0; w < kSortWaves; ++w) c[w] = off[w][t];
+#pragma unroll
+    for (uint32_t w = 0; w < kSortWaves; ++w) {
+      off[w][t] = at;
+      at += c[w];
     }
   }
   __syncthreads();
   for (uint64_t j0 = w0; j0 < end; j0 += kWave) {
-    const uint64_t j = j0 + lane;
-    const bool live = j < end;
-    Pair p{0u, (uint32_t)j};
-    if (live) {
-      if constexpr (FIRST) p.key = key_of(a, (uint32_t)j);
-      else p = a.from[j];
-    }
+    const bool live = j0 + lane < end;
+    const Pair p = j0 == w0 ? first : load(j0 + lane);
     const uint32_t d = (p.key >> a.shift) & dm;
     const uint64_t same = same_digit(d, a.bits, ballot(live));
     const uint32_t rank = count_below(same);
-    uint32_t at = 0;
-    if (live) at = off[wave][d] + rank;
+    uint32_t to = 0;
+    if (live) to = off[wave][d] + rank;
     wave_lds_sync();
     if (live && rank == 0) off[wave][d] += popc(same);
     wave_lds_sync();
-    if (live && at < a.n) a.to[at] = p;  // always, unless the ids change while the call runs
+    if (live && to < a.n) a.to[to] = p;  // always, unless the ids change while the call runs
   }
 }
 
 // The whole sort of up to kSmallTokens tokens in one workgroup, keys and positions in LDS.
 // Further workgroups clear `clear` (n_clear elements) meanwhile.
 template <int DO>
-__global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(SortArgs a, uint32_t passes, uint32_t total_bits,
+__global__ __launch_bounds__(kSortThreads) void sort_small_kernel(SortArgs a, uint32_t passes, uint32_t total_bits,
                                                                    void *clear, uint64_t n_clear) {
   if (blockIdx.x > 0) {
     using TO = typename Num<DO>::T;
     TO *p = static_cast<TO *>(clear);
     constexpr uint32_t kEach = 16 / sizeof(TO);
     typedef TO V __attribute__((ext_vector_type(kEach), aligned(sizeof(TO))));
-    const uint64_t step = (uint64_t)(gridDim.x - 1) * kSmallThreads * kEach;
-    for (uint64_t i = ((uint64_t)(blockIdx.x - 1) * kSmallThreads + threadIdx.x) * kEach; i < n_clear; i += step) {
+    const uint64_t step = (uint64_t)(gridDim.x - 1) * kSortThreads * kEach;
+    for (uint64_t i = ((uint64_t)(blockIdx.x - 1) * kSortThreads + threadIdx.x) * kEach; i < n_clear; i += step) {
       if (i + kEach <= n_clear) {
         *reinterpret_cast<V *>(p + i) = V{};
       } else {
@@ -243,15 +258,14 @@ __global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(SortArgs a, u
     }
     return;
   }
-  constexpr uint32_t kWaves = kSmallThreads / kWave;
   __shared__ uint32_t keys[2][kSmallTokens];
   __shared__ uint16_t pos[2][kSmallTokens];
   static_assert(kSmallTokens <= 1u << 16, "positions in 16 bits");
-  __shared__ uint32_t off[kWaves][kBins];
-  __shared__ uint32_t wave_total[kWaves];
+  __shared__ uint32_t off[kSortWaves][kBins];
+  __shared__ uint32_t wave_total[kSortWaves];
   const uint32_t t = threadIdx.x, wave = uniform(t / kWave), lane = lane_id();
   if (t == 0) a.crossing[0] = 0;
-  for (uint32_t j = t; j < a.n; j += kSmallThreads) {
+  for (uint32_t j = t; j < a.n; j += kSortThreads) {
     keys[0][j] = key_of(a, j);
     pos[0][j] = (uint16_t)j;
   }
@@ -259,24 +273,27 @@ __global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(SortArgs a, u
   uint32_t shift = 0, cur = 0;
   for (uint32_t pass = 0; pass < passes; ++pass) {
     const uint32_t bits = total_bits - shift < a.bits ? total_bits - shift : a.bits, dm = (1u << bits) - 1u;
-    for (uint32_t i = t; i < kBins * kWaves; i += kSmallThreads) (&off[0][0])[i] = 0;
+    for (uint32_t i = t; i < kBins * kSortWaves; i += kSortThreads) (&off[0][0])[i] = 0;
     __syncthreads();
     for (uint32_t j = w0 + lane; j < end; j += kWave) atomicAdd(&off[wave][(keys[cur][j] >> shift) & dm], 1u);
     __syncthreads();
     // thread d < kBins owns digit d
-    uint32_t mine = 0;
-    if (t < kBins)
-      for (uint32_t w = 0; w < kWaves; ++w) mine += off[w][t];
+    uint32_t c[kSortWaves], mine = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < kSortWaves; ++w) {
+      c[w] = t < kBins ? off[w][t] : 0u;
+      mine += c[w];
+    }
     const uint32_t incl = wave_incl_scan(mine);
     if (lane == kWave - 1) wave_total[wave] = incl;
     __syncthreads();
     if (t < kBins) {
       uint32_t at = incl - mine;
       for (uint32_t w = 0; w < wave; ++w) at += wave_total[w];
-      for (uint32_t w = 0; w < kWaves; ++w) {
-        const uint32_t c = off[w][t];
+#pragma unroll
+      for (uint32_t w = 0; w < kSortWaves; ++w) {
         off[w][t] = at;
-        at += c;
+        at += c[w];
       }
     }
     __syncthreads();
@@ -302,7 +319,7 @@ __global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(SortArgs a, u
     cur ^= 1;
     shift += bits;
   }
-  for (uint32_t j = t; j < a.n; j += kSmallThreads) a.to[j] = Pair{keys[cur][j], pos[cur][j]};
+  for (uint32_t j = t; j < a.n; j += kSortThreads) a.to[j] = Pair{keys[cur][j], pos[cur][j]};
 }
 
 // ------------------------------------------------------------------ sums of the sorted rows
@@ -569,18 +586,18 @@ hipError_t launch_embed_grad(const EmbedGradArgs &a, hipStream_t s) {
   hipError_t e = hipSuccess;
   const Pair *sorted = pa;
   if (clear_first) {
-    const uint32_t per = (so.n + kSmallThreads - 1) / kSmallThreads;
+    const uint32_t per = (so.n + kSortThreads - 1) / kSortThreads;
     so.per_wave = (per ? per : 1) * kWave;
-    const uint64_t want = (a.n_rows * a.dim + kSmallThreads * 8 - 1) / (kSmallThreads * 8);
+    const uint64_t want = (a.n_rows * a.dim + kSortThreads * 8 - 1) / (kSortThreads * 8);
     const uint32_t clearers = (uint32_t)(want < 512 ? want : 512);
     e = with_dtype(a.out_dtype, [&](auto d) {
-      sort_small_kernel<d.value><<<1 + clearers, kSmallThreads, 0, s>>>(so, passes, total_bits, a.grad, a.n_rows * a.dim);
+      sort_small_kernel<d.value><<<1 + clearers, kSortThreads, 0, s>>>(so, passes, total_bits, a.grad, a.n_rows * a.dim);
       return hipGetLastError();
     });
   } else {
     const uint64_t want = (a.n_ids + kSortMin - 1) / kSortMin;
     const uint32_t blocks = (uint32_t)(want < kSortBlocks ? want : kSortBlocks);
-    const uint64_t per = (a.n_ids + (uint64_t)blocks * kBlock - 1) / ((uint64_t)blocks * kBlock);
+    const uint64_t per = (a.n_ids + (uint64_t)blocks * kSortThreads - 1) / ((uint64_t)blocks * kSortThreads);
     so.per_wave = (uint32_t)per * kWave;
     for (uint32_t p = 0; p < passes && e == hipSuccess; ++p) {
       SortArgs q = so;
@@ -588,12 +605,12 @@ hipError_t launch_embed_grad(const EmbedGradArgs &a, hipStream_t s) {
       q.bits = total_bits - q.shift < so.bits ? total_bits - q.shift : so.bits;
       q.to = p & 1 ? pb : pa;
       q.from = p & 1 ? pa : pb;
-      if (p == 0) sort_count_kernel<true><<<blocks, kBlock, 0, s>>>(q);
-      else sort_count_kernel<false><<<blocks, kBlock, 0, s>>>(q);
+      if (p == 0) sort_count_kernel<true><<<blocks, kSortThreads, 0, s>>>(q);
+      else sort_count_kernel<false><<<blocks, kSortThreads, 0, s>>>(q);
       e = hipGetLastError();
       if (e != hipSuccess) break;
-      if (p == 0) sort_scatter_kernel<true><<<blocks, kBlock, 0, s>>>(q);
-      else sort_scatter_kernel<false><<<blocks, kBlock, 0, s>>>(q);
+      if (p == 0) sort_scatter_kernel<true><<<blocks, kSortThreads, 0, s>>>(q);
+      else sort_scatter_kernel<false><<<blocks, kSortThreads, 0, s>>>(q);
       e = hipGetLastError();
       sorted = q.to;
     }
