@@ -508,11 +508,18 @@ template <int DO> __global__ __launch_bounds__(kBlock) void grad_join_kernel(Sum
 
 // ------------------------------------------------------------------ host side
 
-// Tokens per chunk: short sequences take short chunks, or too few groups would work, one
-// after another; long ones amortise the partial rows (two 32-bit rows a chunk at most).
-// Chunks of 8, 16 and 32, frequent ids, 32000 rows, single precision gradients: 4000 tokens
-// of 1000 31.1, 33.2 and 38.7 us; 16384 of 1024 73.9, 70.2, 75.1; 32768 of 4096 250, 229, 215.
-uint32_t grad_chunk(uint64_t n) { return n <= 4096 ? 8 : n < 32768 ? 16 : 32; }
+// Tokens per chunk.  Where the elements are few, short chunks: a group of lanes takes a
+// chunk's tokens one after another, and more groups work.  Where they or the tokens are many,
+// long ones: each chunk may leave two 32-bit partial rows.  Chunks of 4, 8, 16 and 32, frequent
+// ids: 7744 tokens of 21 30.1, 32.2, 38.5, 49.6 us; 8192 of 256 33.5, 31.8, 33.8, 39.0; 65536
+// of 64 55.2, 46.5, 43.8, 46.5; 16384 of 1024 75.2, 67.3, 62.5, 53.7; 1000000 of 64 356, 219,
+// 173, 144.
+uint32_t grad_chunk(uint64_t n, uint32_t dim) {
+  const uint64_t elements = n * dim;
+  if (elements >= 1u << 24 || n >= 131072) return 32;
+  if (elements >= 1u << 23 || n >= 65536) return 16;
+  return elements >= 1u << 20 || n >= 16384 ? 8 : 4;
+}
 
 uint64_t up16(uint64_t v) { return (v + 15) & ~15ull; }
 
@@ -525,7 +532,7 @@ GradLayout grad_layout(uint64_t n, uint32_t dim) {
   l.pairs = 0;
   l.counts = up16(2 * n * sizeof(Pair));
   l.crossing = l.counts + kSortBlocks * kBins * 4;
-  const uint64_t ck = grad_chunk(n), chunks = (n + ck - 1) / ck;
+  const uint64_t ck = grad_chunk(n, dim), chunks = (n + ck - 1) / ck;
   l.part = l.crossing + up16(4 * (chunks + 1));
   l.bytes = l.part + chunks * 2 * dim * 4;
   return l;
@@ -625,7 +632,7 @@ hipError_t launch_embed_grad(const EmbedGradArgs &a, hipStream_t s) {
   m.n_rows = a.n_rows;
   m.n = so.n;
   m.dim = a.dim;
-  m.chunk = grad_chunk(a.n_ids);
+  m.chunk = grad_chunk(a.n_ids, a.dim);
   m.nchunks = (m.n + m.chunk - 1) / m.chunk;
   m.lanes = pow2_lanes(a.dim);
   m.slab = m.lanes * 8;
