@@ -421,6 +421,57 @@ def test_wgrad_of_small_and_nan_values(ibp):
     assert not got.any()
 
 
+# ---------------------------------------------------------------- gradients against differences
+
+def test_embedding_grad_is_the_difference_of_lookups(ibp):
+    """Whole values: sum(dout * lookup(table)) changes by exactly the gradient when an element
+    of the table grows by one."""
+    rng = np.random.default_rng(21)
+    rows, dim, n = 7, 33, 200
+    table, dout = rng.integers(-9, 10, (rows, dim)), rng.integers(-4, 5, (n, dim))
+    ids = torch.from_numpy(rng.integers(0, rows - 1, n)).cuda()  # the last row has no token
+    loss = lambda t: (host(ibp.ibp_embedding_lookup(gpu(t, "f32"), ids, scale=2.0)) * dout).sum()  # noqa: E731
+    grad = host(ibp.ibp_embedding_grad(gpu(dout, "f32"), ids, rows, scale=2.0))
+    base = loss(table)
+    for v, c in ((0, 0), (1, 32), (3, 7), (5, 20), (rows - 1, 5)):
+        more = table.copy()
+        more[v, c] += 1
+        assert loss(more) - base == grad[v, c]
+
+
+def test_swiglu_backward_is_the_difference(ibp):
+    """Central differences of the activation in 64 bits, at the checkpoints' values.  Step e:
+    cut off after e^2 / 6 of a third derivative below 1, rounding 2^-52 of values below 2^8 over e."""
+    rng = np.random.default_rng(22)
+    g, u, dh = (gpu(rng.standard_normal((40, 200)) * 3, "f32") for _ in range(3))
+    _, g8, u8 = ibp.ibp_mx_swiglu(g, u)
+    dg, du = ibp.ibp_mx_swiglu_backward(dh, g8, u8)
+    kg, ku, d, e = host(ibp.ibp_mx_unpack(g8, torch.float32)), host(ibp.ibp_mx_unpack(u8, torch.float32)), host(dh), 2.0 ** -15
+    both = lambda f: (f(e) - f(-e)) / (2 * e)  # noqa: E731
+    wg, wu = (both(f) * d for f in (lambda x: mx_ref.swiglu(kg + x, ku), lambda x: mx_ref.swiglu(kg, ku + x)))
+    slack = np.abs(d) * (np.abs(ku) + 1) * (e * e / 6 + 2.0 ** -44 / e)
+    within(host(dg), wg, np.abs(d * ku) * (1 + np.abs(kg)) * 13 * U + slack)
+    within(host(du), wu, np.abs(wu) * 9 * U + slack)
+
+
+def test_wgrad_is_the_difference_of_products(ibp):
+    """Whole values: sum(dy * (x w^T)) changes by exactly the gradient when a weight grows by one."""
+    rng = np.random.default_rng(23)
+    t, o, i = 70, 40, 96
+    x, w, dy = rng.integers(-8, 9, (t, i)).astype(float), rng.integers(0, 3, (o, i)).astype(float), rng.integers(-4, 5, (t, o)).astype(float)
+    w[:, ::32] = 6  # every block keeps the scale 1, so 0 to 4 are codes
+    x[:, ::32] = 256  # and of x, whose whole values up to 16 are codes then
+    x8 = packed(ibp, x, mx_ref.E4M3)
+    assert np.array_equal(host(ibp.ibp_mx_unpack(x8, torch.float32)), x)
+    loss = lambda w: (host(ibp.ibp_mx_matmul(x8, packed(ibp, w, mx_ref.E2M1), torch.float32)) * dy).sum()  # noqa: E731
+    dw = host(ibp.ibp_mx_linear_wgrad(gpu(dy, "bf16"), x8, dw_dtype=torch.float32))
+    base = loss(w)
+    for a, b in ((0, 1), (7, 33), (39, 95), (20, 50)):
+        more = w.copy()
+        more[a, b] += 1
+        assert loss(more) - base == dw[a, b]
+
+
 # ---------------------------------------------------------------- streams and graphs
 
 def step(ibp, s):
