@@ -2,14 +2,14 @@
 // scale per 32 elements, reading them back, and the gated activation silu(gate) * up
 // that keeps its inputs as e4m3 checkpoints, with its backward pass from them.
 //
-// All four are one pass over the data, bound by HBM: 16384 x 8192 in bf16 is packed to
-// e2m1 in 61 us (5.5 TB/s; a copy of 1 GiB reaches 5.2), to e4m3 in 73, read back in 59,
-// the gated activation takes 206 us forward (5.3 TB/s) and 191 back (5.7).  A lane takes eight consecutive
-// elements (16 bytes of a 16-bit type), so four lanes hold a block and share its
-// largest magnitude by two lane exchanges, and 16 lanes hold the four blocks whose
-// scale bytes make one dword.  A row is cut into strips of 8 times the smallest power of
-// two of lanes, from 16 to the workgroup, that covers it; a workgroup step is one strip
-// of R * 256 / lanes rows, R of them per lane, loaded before any is worked on.
+// All four are one pass over the data, bound by HBM: 16384 x 8192 in bf16 is packed to e2m1
+// and read back in 137 us (5.0 TB/s; a copy of 1 GiB reaches 5.2), packed to e4m3 in 73; the
+// gated activation takes 204 us forward (5.4 TB/s) and 191 back (5.7).  A lane takes eight
+// consecutive elements (16 bytes of a 16-bit type), so four lanes hold a block and share its
+// largest magnitude by two lane exchanges, and 16 lanes hold the four blocks whose scale
+// bytes make one dword.  A row is cut into strips of 8 times the smallest power of two of
+// lanes, from 16 to the workgroup, that covers it; a workgroup step is one strip of R * 256
+// / lanes rows, R of them per lane, loaded before any is worked on.
 #include "ibp_device.h"
 #include "ibp_num.h"
 
@@ -65,7 +65,7 @@ template <bool E4M3> __device__ __forceinline__ uint2 load_codes(const uint8_t *
 // 1 / (1 + exp(-g)).  The 16-bit types take it from the hardware's exp2 and reciprocal
 // (1 unit of the last place each), the argument's rounding made good by a factor: 6 half
 // units in all, far below the result's own rounding, for a third of the instructions
-// (forward of 16384 x 8192 in bf16 206 us against 245 with the library's exp and a true
+// (forward of 16384 x 8192 in bf16 204 us against 245 with the library's exp and a true
 // quotient, which 32-bit results take).
 template <int D> __device__ __forceinline__ float sigmoid(float g) {
   if constexpr (D == IBP_F32) {

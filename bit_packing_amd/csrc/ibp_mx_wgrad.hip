@@ -1,13 +1,14 @@
 // ibp_mx_wgrad.hip -- weight gradient of a linear layer from the 8-bit checkpoint of its
 // input: dW[o][i] = sum over tokens t of dY[t][o] X[t][i], X packed as e4m3.
 //
-// An e4m3 value times its power-of-two scale (at least 2^-117) is a BF16 number, so X
-// is decoded exactly to BF16 and the product runs on the BF16 matrix instruction with
-// 32-bit sums.  A dY of another type is the sum of BF16 numbers, two for half precision's
-// 11 bits and three for single's 24, each the leading eight bits of what the ones before
-// leave; each part has its own ranges of the launch and is added like another range.  Both operands lie with t as the slow dimension, while the instruction
-// wants consecutive t in a lane: tiles are staged in LDS as they lie and read through
-// the transposing LDS read, which hands each of 16 lanes one column of a 4 x 16 block.
+// An e4m3 value times its power-of-two scale (at least 2^-117) is a BF16 number, so X is
+// decoded exactly to BF16 and the product runs on the BF16 matrix instruction with 32-bit
+// sums.  A dY of another type is the sum of BF16 numbers, two for half precision's 11 bits
+// and three for single's 24, each the leading eight bits of what the ones before leave; each
+// part has its own ranges of the launch and is added like another range.  Both operands lie
+// with t as the slow dimension, while the instruction wants consecutive t in a lane: tiles
+// are staged in LDS as they lie and read through the transposing LDS read, which hands each
+// of 16 lanes one column of a 4 x 16 block.
 #include "ibp_device.h"
 #include "ibp_num.h"
 #include "ibp_tile.h"
@@ -87,7 +88,7 @@ template <typename T> __device__ __forceinline__ T from_global(const uint8_t *p)
 // stages ahead where its rows are aligned to 16 bytes (DIRECT), else through registers like
 // X, which is loaded four stages ahead and decoded into LDS two stages ahead.  As in the
 // 4-bit product, half of the eight wavefronts of a large tile read a stage while the other
-// half multiplies (16384 x 4096 x 8192: 863 us, 1.27 PFLOP/s, against 1090 with all in
+// half multiplies (16384 x 4096 x 8192: 890 us, 1.23 PFLOP/s, against 1090 with all in
 // step and two stages of 64 tokens).  Bound by the phases: the matrix units are busy half
 // of the time, LDS a quarter.
 template <int WI, int WO, int FI, int FO, bool DIRECT, int DY, int DO>
