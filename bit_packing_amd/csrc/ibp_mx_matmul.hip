@@ -130,7 +130,9 @@ template <bool A8> hipError_t go_direct(const MxMatmulArgs &a, hipStream_t s) {
 // 279 us, 3.9 PFLOP/s (310 us with two stages of 256 elements and all wavefronts in step);
 // with the loads left out 80% of that, with the matrix instructions left out as long: it
 // is bound by a turn's two phases, reading LDS and issuing loads in one, multiplying in
-// the other.
+// the other, and by power: the clock falls to 2.0 GHz.  The 32 x 32 x 64 matrix instruction
+// takes 2% fewer cycles at a clock 5% lower (with packing 330 us against 320); without
+// phases, reading each fragment's successor once it is used, 331 against 327.
 //
 // LDS rows are 128 (e4m3) or 64 bytes (e2m1).  The 16-byte pieces of a row are permuted by
 // the row number, so that eight rows read at one piece lie in different banks: a read
