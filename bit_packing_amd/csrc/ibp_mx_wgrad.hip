@@ -21,25 +21,31 @@ using namespace dev;
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+typedef float v16f __attribute__((ext_vector_type(16)));
 
-constexpr uint32_t kT = 32;  // tokens per stage: one matrix instruction deep
+constexpr uint32_t kT = 32;  // tokens per stage
 
-// LDS byte of the 16-byte piece `c16` of row t of a tile of W columns.  The 32-byte
-// pieces of a row are permuted by the low bits of t: a transposing read takes 32 bytes
-// of each of eight rows at a time, which then fall into all 64 banks.
-template <uint32_t W> __device__ __forceinline__ uint32_t tile_at(uint32_t t, uint32_t c16) {
-  return t * (W * 2) + ((((c16 >> 1) ^ (t & 7)) << 5) | ((c16 & 1) << 4));
+// The 32-byte pieces of row t of a tile are permuted by three bits of t, so that what half a
+// wavefront reads at a time falls into all 64 banks: for fragments of F = 16 columns a piece
+// of each of eight rows, for F = 32 two neighbouring pieces of each of four.
+template <int F> __device__ __forceinline__ uint32_t permute(uint32_t piece, uint32_t t) {
+  return piece ^ (F == 16 ? t & 7 : (t & 3) << 1 | (t >> 2 & 1));
 }
 
-// Eight BF16 of column block `col` (16 columns) of a stage, in the order of the matrix
-// instruction's k: lane group g takes rows 4 g .. 4 g + 3 and 16 + 4 g .. 16 + 4 g + 3;
-// both operands do, so the sum is over the same tokens.
-template <uint32_t W> __device__ __forceinline__ v8b fragment(const uint8_t *tile, uint32_t col, uint32_t lane) {
-  const uint32_t t = (lane >> 4) * 4 + ((lane & 15) >> 2), sub = (lane & 3) * 8;
-  const uint8_t *at = tile + t * (W * 2) + ((col ^ (t & 7)) << 5) + sub;
+// LDS byte of the 16-byte piece `c16` of row t of a tile of W columns.
+template <uint32_t W, int F> __device__ __forceinline__ uint32_t tile_at(uint32_t t, uint32_t c16) {
+  return t * (W * 2) + (permute<F>(c16 >> 1, t) << 5 | (c16 & 1) << 4);
+}
+
+// Eight BF16 of column block `col` (F columns) of a stage's tokens from 16 s on, in the order
+// of the matrix instruction's k: lane group g of F lanes takes rows 4 g .. 4 g + 3 and as many
+// 16 (F = 16) or 8 rows further on; both operands do, so the sum is over the same tokens.
+template <uint32_t W, int F> __device__ __forceinline__ v8b fragment(const uint8_t *tile, uint32_t col, uint32_t s, uint32_t lane) {
+  const uint32_t t = lane / F * 4 + ((lane & 15) >> 2), piece = F == 16 ? col : col * 2 + (lane >> 4 & 1);
+  const uint8_t *at = tile + (16 * s + t) * (W * 2) + (permute<F>(piece, t) << 5) + (lane & 3) * 8;
   using L = __attribute__((address_space(3))) v4s;
   const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L *)at);
-  const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L *)(at + 16 * W * 2));
+  const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L *)(at + (F == 16 ? 16 : 8) * W * 2));
   return __builtin_bit_cast(v8b, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
@@ -80,7 +86,7 @@ template <typename T> __device__ __forceinline__ T from_global(const uint8_t *p)
   return *reinterpret_cast<const __attribute__((address_space(1))) T *>((uintptr_t)p);
 }
 
-// A workgroup of WI x WO wavefronts computes 16 FI WI (i) by 16 FO WO (o) elements of dW
+// A workgroup of WI x WO wavefronts computes F FI WI (i) by F FO WO (o) elements of dW
 // over the tokens [z * t_each, (z + 1) * t_each), z = blockIdx.y % splits, of part
 // blockIdx.y / splits of dY, into dst + blockIdx.y * N * K.
 //
@@ -90,15 +96,19 @@ template <typename T> __device__ __forceinline__ T from_global(const uint8_t *p)
 // 4-bit product, half of the eight wavefronts of a large tile read a stage while the other
 // half multiplies (16384 x 4096 x 8192: 890 us, 1.23 PFLOP/s, against 1090 with all in
 // step and two stages of 64 tokens).  Bound by the phases (the matrix units are busy 57% of the
-// time, LDS 28%) and by power: the clock falls to 1.9 to 2.1 GHz.  The 32 x 32 x 16 matrix
-// instruction takes 8% fewer cycles at a clock 11% lower: 894 us against 862.
-template <int WI, int WO, int FI, int FO, bool DIRECT, int DY, int DO>
+// time, LDS 28%) and by power: the clock falls to 1.9 to 2.1 GHz.
+//
+// F = 32 takes the 32 x 32 x 16 matrix instruction: a third more from registers alone, at more
+// power.  The large tile is 11% slower in clock for 8% fewer cycles with it (894 us against
+// 862) and takes F = 16; the small one, bound by latency, is faster (999 x 504 x 1000 14.5 us
+// against 15.3, 16384 x 256 x 256 23.5 against 25.5).
+template <int F, int WI, int WO, int FI, int FO, bool DIRECT, int DY, int DO>
 __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *dst, uint64_t t_each, uint32_t tiles_o,
                                                            uint32_t tiles_i, uint32_t splits) {
   using TY = typename Num<DY>::T;
   static_assert(!DIRECT || DY == IBP_BF16, "");
   using TO = typename Num<DO>::T;
-  constexpr uint32_t kWaves = WI * WO, kThreads = kWaves * 64, kWideI = 16 * FI * WI, kWideO = 16 * FO * WO;
+  constexpr uint32_t kWaves = WI * WO, kThreads = kWaves * 64, kWideI = F * FI * WI, kWideO = F * FO * WO;
   constexpr uint32_t kPiecesY = kT * kWideO / 8 / kThreads, kPiecesX = kT * kWideI / 8 / kThreads;
   constexpr uint32_t kBytesY = kT * kWideO * 2, kStage = kBytesY + kT * kWideI * 2, kRing = 4;
   constexpr uint32_t kStepY = kThreads / (kWideO / 8), kStepX = kThreads / (kWideI / 8);  // tokens between a thread's pieces
@@ -107,7 +117,7 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
   const uint32_t lane = lane_id(), wave = uniform(threadIdx.x / kWave);
   const TileId tile = tile_of(blockIdx.x, tiles_o, tiles_i);
   const uint32_t o0 = tile.row * kWideO, i0 = tile.col * kWideI;
-  const uint32_t wi = (wave % WI) * FI, wo = (wave / WI) * FO;  // in blocks of 16
+  const uint32_t wi = (wave % WI) * FI, wo = (wave / WI) * FO;  // in blocks of F
   const uint32_t part = blockIdx.y / splits;
   const uint64_t t0 = (blockIdx.y - part * splits) * t_each, t1 = t0 + t_each < a.T ? t0 + t_each : a.T;
   const uint32_t cp = (uint32_t)mx_code_pitch(a.K, true), sp = (uint32_t)mx_scale_pitch(a.K);
@@ -118,7 +128,7 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
   const uint32_t ty = threadIdx.x / (kWideO / 8), sy = threadIdx.x % (kWideO / 8);
   const uint32_t tx = threadIdx.x / (kWideI / 8), sx = threadIdx.x % (kWideI / 8), cx = i0 + sx * 8;
   // LDS takes dY's pieces in lane order; the permutation is made by their sources
-  const uint32_t cy = o0 + ((((sy >> 1) ^ (ty & 7)) << 1) | (sy & 1)) * 8;
+  const uint32_t cy = o0 + (permute<F>(sy >> 1, ty) << 1 | (sy & 1)) * 8;
   const bool in_y = !DIRECT || cy < a.N, in_x = cx < cp;
   // without DIRECT a piece past the row's end is the row's last eight elements (load8)
   const bool wide = a.N >= 8;
@@ -129,13 +139,14 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
   const uint32_t scale_shift = cx / kMxBlock % 4 * 8;
   const uint64_t go_y = in_y ? (uint64_t)kStepY * a.N * sizeof(TY) : 0, go_x = in_x ? (uint64_t)kStepX * cp : 0;
   const uint64_t go_s = in_x ? (uint64_t)kStepX * sp : 0;
-  const uint32_t at_x = kBytesY + tile_at<kWideI>(tx, sx);
+  const uint32_t at_x = kBytesY + tile_at<kWideI, F>(tx, sx);
 
-  v4f acc[FI][FO];
+  using Acc = typename std::conditional<F == 16, v4f, v16f>::type;
+  Acc acc[FI][FO];
 #pragma unroll
   for (int x = 0; x < FI; ++x)
 #pragma unroll
-    for (int y = 0; y < FO; ++y) acc[x][y] = v4f{0, 0, 0, 0};
+    for (int y = 0; y < FO; ++y) acc[x][y] = Acc{};
 
   // An even number of stages, the last perhaps of zeros: the loop takes two at a time, so
   // that the two sets of registers of loads in flight are known to the compiler.
@@ -200,15 +211,19 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
   const bool behind = kPingPong && wave >= kWaves / 2;
   constexpr uint32_t kLoads = 2 * kPiecesX + kPiecesY;  // a wavefront's per turn
   static_assert(kLoads < 16, "");
-  v8b fx[FI], fy[FO];
+  constexpr uint32_t kDeep = F == 16 ? 1 : 2;  // matrix instructions that a stage is deep
+  v8b fx[kDeep][FI], fy[kDeep][FO];
   // What the loads in flight fill is not what is read; __restrict__ says so to the compiler,
   // which otherwise would wait for all of them before an LDS read.
   auto read = [&](uint8_t *__restrict__ filled, const uint8_t *__restrict__ now) {
     (void)filled;
 #pragma unroll
-    for (int y = 0; y < FO; ++y) fy[y] = fragment<kWideO>(now, wo + y, lane);
+    for (uint32_t s = 0; s < kDeep; ++s) {
 #pragma unroll
-    for (int x = 0; x < FI; ++x) fx[x] = fragment<kWideI>(now + kBytesY, wi + x, lane);
+      for (int y = 0; y < FO; ++y) fy[s][y] = fragment<kWideO, F>(now, wo + y, s, lane);
+#pragma unroll
+      for (int x = 0; x < FI; ++x) fx[s][x] = fragment<kWideI, F>(now + kBytesY, wi + x, s, lane);
+    }
   };
   auto write = [&](uint8_t *__restrict__ filled, uint8_t *__restrict__ settled, Set &f, uint32_t k) {
     settle(settled, f);
@@ -224,12 +239,18 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
     barrier();
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int x = 0; x < FI; ++x) {
+    for (uint32_t s = 0; s < kDeep; ++s) {
 #pragma unroll
-      for (int y = 0; y < FO; ++y) acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[x], fy[y], acc[x][y], 0, 0, 0);
-      if (x == 0) {
-        __builtin_amdgcn_sched_barrier(0);  // the compiler would put this before the matrix instructions
-        write(ring + ((k + 3) % kRing) * kStage, ring + ((k + 2) % kRing) * kStage, f, k);
+      for (int x = 0; x < FI; ++x) {
+#pragma unroll
+        for (int y = 0; y < FO; ++y) {
+          if constexpr (F == 16) acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[s][x], fy[s][y], acc[x][y], 0, 0, 0);
+          else acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fx[s][x], fy[s][y], acc[x][y], 0, 0, 0);
+        }
+        if (s == 0 && x == 0) {
+          __builtin_amdgcn_sched_barrier(0);  // the compiler would put this before the matrix instructions
+          write(ring + ((k + 3) % kRing) * kStage, ring + ((k + 2) % kRing) * kStage, f, k);
+        }
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -256,14 +277,19 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
   }
   if (kPingPong && !behind) barrier();
   __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);  // no load into LDS outlives the workgroup
-  // a lane has four consecutive i of one o
+  // a lane has once or four times four consecutive i of one o
   TO *dw = static_cast<TO *>(dst) + (uint64_t)blockIdx.y * a.N * a.K;
 #pragma unroll
   for (int y = 0; y < FO; ++y) {
-    const uint32_t o = o0 + (wo + y) * 16 + (lane & 15);
+    const uint32_t o = o0 + (wo + y) * F + lane % F;
     if (o >= a.N) continue;
 #pragma unroll
-    for (int x = 0; x < FI; ++x) store4<TO>(dw + (uint64_t)o * a.K, i0 + (wi + x) * 16 + 4 * (lane >> 4), a.K, acc[x][y]);
+    for (int x = 0; x < FI; ++x) {
+#pragma unroll
+      for (int q = 0; q < F * F / 256; ++q)
+        store4<TO>(dw + (uint64_t)o * a.K, i0 + (wi + x) * F + 8 * q + 4 * (lane / F), a.K,
+                   v4f{acc[x][y][4 * q], acc[x][y][4 * q + 1], acc[x][y][4 * q + 2], acc[x][y][4 * q + 3]});
+    }
   }
 }
 
@@ -319,14 +345,14 @@ template <int DO> hipError_t go(const MxWgradArgs &a, const Plan &p, void *dst, 
     return hipGetLastError();
   };
   if constexpr (DO == IBP_F32) {  // parts are always joined
-    if (a.dy_dtype == IBP_F16) return launch(wgrad_kernel<2, 2, 4, 4, false, IBP_F16, DO>, 256);
-    if (a.dy_dtype == IBP_F32) return launch(wgrad_kernel<2, 2, 4, 4, false, IBP_F32, DO>, 256);
+    if (a.dy_dtype == IBP_F16) return launch(wgrad_kernel<32, 2, 2, 2, 2, false, IBP_F16, DO>, 256);
+    if (a.dy_dtype == IBP_F32) return launch(wgrad_kernel<32, 2, 2, 2, 2, false, IBP_F32, DO>, 256);
   }
   if (p.big)
-    return direct ? launch(wgrad_kernel<2, 4, 8, 4, true, IBP_BF16, DO>, 512)
-                  : launch(wgrad_kernel<2, 4, 8, 4, false, IBP_BF16, DO>, 512);
-  return direct ? launch(wgrad_kernel<2, 2, 4, 4, true, IBP_BF16, DO>, 256)
-                : launch(wgrad_kernel<2, 2, 4, 4, false, IBP_BF16, DO>, 256);
+    return direct ? launch(wgrad_kernel<16, 2, 4, 8, 4, true, IBP_BF16, DO>, 512)
+                  : launch(wgrad_kernel<16, 2, 4, 8, 4, false, IBP_BF16, DO>, 512);
+  return direct ? launch(wgrad_kernel<32, 2, 2, 2, 2, true, IBP_BF16, DO>, 256)
+                : launch(wgrad_kernel<32, 2, 2, 2, 2, false, IBP_BF16, DO>, 256);
 }
 
 }  // namespace
