@@ -91,7 +91,8 @@ template <typename T> __device__ __forceinline__ T from_global(const uint8_t *p)
 // blockIdx.y / splits of dY, into dst + blockIdx.y * N * K.
 //
 // Stages of 32 tokens lie in a ring of four.  dY comes by direct global-to-LDS loads three
-// stages ahead where its rows are aligned to 16 bytes (DIRECT), else through registers like
+// stages ahead where its rows are aligned to 16 bytes (DIRECT: they are, or wgrad_parts_kernel
+// has laid them out so; part p is then T rows further on), else through registers like
 // X, which is loaded four stages ahead and decoded into LDS two stages ahead.  As in the
 // 4-bit product, half of the eight wavefronts of a large tile read a stage while the other
 // half multiplies (16384 x 4096 x 8192: 890 us, 1.23 PFLOP/s, against 1090 with all in
@@ -129,15 +130,16 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
   const uint32_t tx = threadIdx.x / (kWideI / 8), sx = threadIdx.x % (kWideI / 8), cx = i0 + sx * 8;
   // LDS takes dY's pieces in lane order; the permutation is made by their sources
   const uint32_t cy = o0 + (permute<F>(sy >> 1, ty) << 1 | (sy & 1)) * 8;
-  const bool in_y = !DIRECT || cy < a.N, in_x = cx < cp;
+  const bool in_y = !DIRECT || cy < a.dy_pitch, in_x = cx < cp;
   // without DIRECT a piece past the row's end is the row's last eight elements (load8)
   const bool wide = a.N >= 8;
   const uint64_t at_y = DIRECT ? cy : (wide ? (cy + 8 <= a.N ? cy : a.N - 8) : 0);
-  const uint8_t *py = in_y ? reinterpret_cast<const uint8_t *>(dy + (t0 + ty) * a.N + at_y) : kZeros;
+  const uint64_t row_y = t0 + ty + (DIRECT ? part * a.T : 0);
+  const uint8_t *py = in_y ? reinterpret_cast<const uint8_t *>(dy + row_y * a.dy_pitch + at_y) : kZeros;
   const uint8_t *px = in_x ? a.x_codes + (t0 + tx) * cp + cx : kZeros;
   const uint8_t *ps = in_x ? a.x_scales + (t0 + tx) * sp + cx / (4 * kMxBlock) * 4 : kZeros;  // its dword
   const uint32_t scale_shift = cx / kMxBlock % 4 * 8;
-  const uint64_t go_y = in_y ? (uint64_t)kStepY * a.N * sizeof(TY) : 0, go_x = in_x ? (uint64_t)kStepX * cp : 0;
+  const uint64_t go_y = in_y ? (uint64_t)kStepY * a.dy_pitch * sizeof(TY) : 0, go_x = in_x ? (uint64_t)kStepX * cp : 0;
   const uint64_t go_s = in_x ? (uint64_t)kStepX * sp : 0;
   const uint32_t at_x = kBytesY + tile_at<kWideI, F>(tx, sx);
 
@@ -293,6 +295,27 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
   }
 }
 
+// Lays dY out as the large tile's direct loads want it: its parts in BF16, T rows each, rows
+// filled up with zeros to a multiple of eight elements.  One pass; 16001 tokens of 1153, 4097
+// inputs: 198 us with it, against 300 through registers; 8192 x 4096 x 4096 in single
+// precision 778 against 2027, 4096 x 2048 x 2048 in half precision 105 against 188.  The small
+// tile takes such a dY through registers, without a launch more (999 x 500 x 1000 18.6 us,
+// 14.6 with 504).
+template <int DY> __global__ __launch_bounds__(kBlock) void wgrad_parts_kernel(MxWgradArgs a, __bf16 *out, uint32_t parts) {
+  using TY = typename Num<DY>::T;
+  const TY *dy = static_cast<const TY *>(a.dy);
+  const uint32_t pieces = a.dy_pitch / 8;
+  const uint64_t n = a.T * pieces, step = (uint64_t)gridDim.x * kBlock;
+  by_width(a.N, [&](auto wide) {
+    for (uint64_t e = (uint64_t)blockIdx.x * kBlock + threadIdx.x; e < n; e += step) {
+      const uint64_t t = e / pieces;
+      const uint32_t c = (uint32_t)(e - t * pieces) * 8;
+      const Vec8<TY> y = settle8<wide.value, TY>(load8<wide.value, TY>(dy + t * a.N, c, a.N), c, a.N);
+      for (uint32_t p = 0; p < parts; ++p) *reinterpret_cast<v8b *>(out + ((p * a.T + t) * pieces * 8 + c)) = part_of<TY>(y, p);
+    }
+  });
+}
+
 // Adds the ranges' sums in order.
 template <int DO> __global__ __launch_bounds__(kBlock) void wgrad_join_kernel(MxWgradArgs a, uint32_t splits) {
   using TO = typename Num<DO>::T;
@@ -312,18 +335,25 @@ template <int DO> __global__ __launch_bounds__(kBlock) void wgrad_join_kernel(Mx
 // tokens at least: a range's sums are written and read once in 32 bits.
 struct Plan {
   bool big;
+  bool copied;  // dY laid out anew, as the large tile takes it
   uint32_t tiles_o, tiles_i;
   uint32_t splits;
   uint32_t parts;  // of dY
   uint64_t t_each;
+
+  uint64_t pieces() const { return (uint64_t)splits * parts; }
+  uint64_t sums_bytes(uint32_t N, uint32_t K) const { return pieces() > 1 ? (pieces() * N * K * 4 + 15) & ~15ull : 0; }
 };
 
-Plan plan_of(uint64_t T, uint32_t N, uint32_t K, int dy_dtype) {
+Plan plan_of(uint64_t T, uint32_t N, uint32_t K, int dy_dtype, bool aligned) {
   Plan p;
   p.parts = dy_dtype == IBP_BF16 ? 1 : dy_dtype == IBP_F16 ? 2 : 3;
   const uint64_t big = (((uint64_t)N + 255) / 256) * (((uint64_t)K + 255) / 256);
-  // other types' pieces in flight leave no registers for the large tile
-  p.big = p.parts == 1 && T >= 1024 && big * ((T + 511) / 512) >= 256;
+  p.copied = p.parts > 1 || N % 8 != 0;
+  // BF16 rows of whole pieces that begin off 16 bytes take the small tile, through registers:
+  // its ranges are as many or fewer, so the workspace is large enough for both
+  p.big = T >= 1024 && big * ((T + 511) / 512) >= 256 && (aligned || p.copied);
+  p.copied = p.copied && p.big;
   const uint32_t wide = p.big ? 256 : 128;
   p.tiles_o = (uint32_t)(((uint64_t)N + wide - 1) / wide);
   p.tiles_i = (uint32_t)(((uint64_t)K + wide - 1) / wide);
@@ -337,44 +367,54 @@ Plan plan_of(uint64_t T, uint32_t N, uint32_t K, int dy_dtype) {
   return p;
 }
 
+uint32_t padded(uint32_t N) { return (N + 7) / 8 * 8; }
+
 template <int DO> hipError_t go(const MxWgradArgs &a, const Plan &p, void *dst, hipStream_t s) {
-  const bool direct = a.N % 8 == 0 && (uintptr_t)a.dy % 16 == 0;
   const dim3 grid(p.tiles_o * p.tiles_i, p.splits * p.parts);
   auto launch = [&](auto kernel, uint32_t threads) {
     kernel<<<grid, threads, 0, s>>>(a, dst, p.t_each, p.tiles_o, p.tiles_i, p.splits);
     return hipGetLastError();
   };
+  if (p.big) return launch(wgrad_kernel<16, 2, 4, 8, 4, true, IBP_BF16, DO>, 512);
   if constexpr (DO == IBP_F32) {  // parts are always joined
     if (a.dy_dtype == IBP_F16) return launch(wgrad_kernel<32, 2, 2, 2, 2, false, IBP_F16, DO>, 256);
     if (a.dy_dtype == IBP_F32) return launch(wgrad_kernel<32, 2, 2, 2, 2, false, IBP_F32, DO>, 256);
   }
-  if (p.big)
-    return direct ? launch(wgrad_kernel<16, 2, 4, 8, 4, true, IBP_BF16, DO>, 512)
-                  : launch(wgrad_kernel<16, 2, 4, 8, 4, false, IBP_BF16, DO>, 512);
-  return direct ? launch(wgrad_kernel<32, 2, 2, 2, 2, true, IBP_BF16, DO>, 256)
-                : launch(wgrad_kernel<32, 2, 2, 2, 2, false, IBP_BF16, DO>, 256);
+  return a.N % 8 == 0 && (uintptr_t)a.dy % 16 == 0 ? launch(wgrad_kernel<32, 2, 2, 2, 2, true, IBP_BF16, DO>, 256)
+                                                   : launch(wgrad_kernel<32, 2, 2, 2, 2, false, IBP_BF16, DO>, 256);
 }
 
 }  // namespace
 
 uint64_t mx_wgrad_workspace(uint64_t T, uint32_t N, uint32_t K, int dy_dtype) {
-  const Plan p = plan_of(T, N, K, dy_dtype);
-  const uint64_t n = (uint64_t)p.splits * p.parts;
-  return n > 1 ? n * N * K * 4 : 0;
+  const Plan p = plan_of(T, N, K, dy_dtype, true);
+  return p.sums_bytes(N, K) + (p.copied ? p.parts * T * padded(N) * 2 : 0);
 }
 
-hipError_t launch_mx_wgrad(const MxWgradArgs &a, hipStream_t s) {
-  const Plan p = plan_of(a.T, a.N, a.K, a.dy_dtype);
+hipError_t launch_mx_wgrad(const MxWgradArgs &args, hipStream_t s) {
+  MxWgradArgs a = args;
+  const Plan p = plan_of(a.T, a.N, a.K, a.dy_dtype, (uintptr_t)a.dy % 16 == 0);
   if (p.t_each > 0x7FFFFFFFull) return hipErrorInvalidValue;
-  const uint32_t pieces = p.splits * p.parts;
-  if (pieces > 1) {
+  a.dy_pitch = a.N;
+  if (p.copied) {
+    a.dy_pitch = padded(a.N);
+    __bf16 *copy = reinterpret_cast<__bf16 *>(reinterpret_cast<uint8_t *>(a.ws) + p.sums_bytes(a.N, a.K));
+    const uint64_t n = (a.T * (a.dy_pitch / 8) + kBlock - 1) / kBlock;
+    const hipError_t e = with_dtype(a.dy_dtype, [&](auto d) {
+      wgrad_parts_kernel<d.value><<<(uint32_t)(n < (1u << 20) ? n : (1u << 20)), kBlock, 0, s>>>(a, copy, p.parts);
+      return hipGetLastError();
+    });
+    if (e != hipSuccess) return e;
+    a.dy = copy;
+  }
+  if (p.pieces() > 1) {
     const hipError_t e = go<IBP_F32>(a, p, a.ws, s);
     if (e != hipSuccess) return e;
   }
   return with_dtype(a.dtype, [&](auto d) {
-    if (pieces == 1) return go<d.value>(a, p, a.dw, s);
+    if (p.pieces() == 1) return go<d.value>(a, p, a.dw, s);
     const uint64_t n = ((uint64_t)a.N * a.K + kBlock * 4 - 1) / (kBlock * 4);
-    wgrad_join_kernel<d.value><<<(uint32_t)(n < 4096 ? n : 4096), kBlock, 0, s>>>(a, pieces);
+    wgrad_join_kernel<d.value><<<(uint32_t)(n < 4096 ? n : 4096), kBlock, 0, s>>>(a, (uint32_t)p.pieces());
     return hipGetLastError();
   });
 }

@@ -78,6 +78,7 @@ struct MxWgradArgs {
   uint32_t N, K;
   int dy_dtype;
   int dtype;
+  uint32_t dy_pitch;  // set by the launch: elements from one row of dy to the next
 };
 uint64_t mx_wgrad_workspace(uint64_t T, uint32_t N, uint32_t K, int dy_dtype);
 

@@ -393,6 +393,24 @@ def test_wgrad(ibp, ty, to, t, n, k):
     within(host(got), want, np.abs(want) * half(to) + mag * t * U + TINY[to])
 
 
+@pytest.mark.parametrize("ty,n,first", [("bf16", 3000, 0), ("bf16", 3000, 3), ("bf16", 3001, 0), ("bf16", 2999, 1), ("f16", 3000, 0),
+                                        ("f32", 2999, 1)])
+def test_wgrad_of_many_tokens_and_columns(ibp, ty, n, first):
+    """The large tile: rows of whole pieces, rows that are laid out anew, tensors that begin
+    anywhere.  Whole values, sums of 1100 terms up to 4 * 7.5 in steps of 1/8: exact."""
+    t, k = 1100, 3300
+    rng = np.random.default_rng(n + first)
+    dy = rng.integers(-4, 5, (t, n)).astype(np.float32)
+    x = codes_of(rng, t, k, mx_ref.E4M3, -1, 1)
+    want = dy.T @ mx_ref.unpack(*x, k, mx_ref.E4M3).astype(np.float32)  # exact in 32 bits too
+    print(f"weight gradient: ty={ty} n={n} first={first}", flush=True)
+    flat = torch.zeros(first + t * n, dtype=DT[ty], device="cuda")
+    flat[first:] = gpu(dy, ty).flatten()
+    dw = torch.full((n, k), float("nan"), device="cuda")
+    ibp.ibp_mx_linear_wgrad(flat[first:].view(t, n), device(ibp, *x, k, mx_ref.E4M3), dw=dw)
+    assert np.array_equal(dw.cpu().numpy(), want)
+
+
 def test_wgrad_takes_single_precision_whole(ibp):
     """One token: each output is one product of 24 and 4 bits, rounded to 32; the largest
     values, infinities and NaNs (whatever bits they carry) stay what they are."""
