@@ -327,12 +327,15 @@ template <int DO> __global__ __launch_bounds__(kBlock) void wgrad_join_kernel(Mx
   }
 }
 
-// Tile and ranges of tokens.  256 x 256 tiles read each operand half as often as 128 x
-// 128 ones, so they are taken where tiles and tokens give every CU 512 tokens of one
-// (16384 tokens: 2048 x 2048 140 us against 179, 512 x 512 38 against 31; 256 tokens of
-// 4096 x 4096 26 against 24).  The tokens are cut into ranges until there is a workgroup
-// per CU (16384 tokens of 1024 x 1024: 366 us in one range, 55 in sixteen), each of 256
-// tokens at least: a range's sums are written and read once in 32 bits.
+// Tile and ranges of tokens.  256 x 256 tiles read each operand half as often as 128 x 128
+// ones, but half as many fit: two small workgroups share a CU.  The large ones are taken where
+// the small ones would not fit at once (256 large tiles: 128 tokens 23 us against 25, 500 32
+// against 38; 160: 1000 tokens 37 against 43), and where the tokens make up for the CUs left
+// empty (128: 2000 tokens 55 against 47, 4000 81 against 83, 8000 132 against 154; 16: 8000
+// 42 against 41, 16000 56 against 66; 4: 16000 38 against 29).
+// The tokens are cut into ranges until there is a workgroup per CU (16384 tokens of 1024 x
+// 1024: 366 us in one range, 55 in sixteen), each of 256 tokens at least: a range's sums are
+// written and read once in 32 bits.
 struct Plan {
   bool big;
   bool copied;  // dY laid out anew, as the large tile takes it
@@ -354,7 +357,7 @@ Plan plan_of(uint64_t T, uint32_t N, uint32_t K, int dy_dtype, bool aligned) {
   p.copied = p.parts > 1 || (N % 8 != 0 && K > 256);
   // BF16 rows of whole pieces that begin off 16 bytes take the small tile, through registers:
   // its ranges are as many or fewer, so the workspace is large enough for both
-  p.big = T >= 1024 && big * ((T + 511) / 512) >= 256 && (p.copied || (aligned && N % 8 == 0));
+  p.big = (big > 128 || (T >= 3500 && big * T >= 140000)) && (p.copied || (aligned && N % 8 == 0));
   p.copied = p.copied && p.big;
   const uint32_t wide = p.big ? 256 : 128;
   p.tiles_o = (uint32_t)(((uint64_t)N + wide - 1) / wide);
