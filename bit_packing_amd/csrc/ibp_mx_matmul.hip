@@ -25,13 +25,16 @@ constexpr uint32_t kStep = 16;  // blocks per step of the direct kernel: 512 ele
 // Scales are the low bytes of ws and xs; format codes: 0 e4m3, 4 e2m1.
 //
 // Within a block the instruction adds products aligned to the largest and drops what lies
-// more than 13 binary places below it (measured: 256 * 1 + 2^-5 * 1 is kept, + 2^-6 is
-// not).  Products of e2m1 fit (36 down to 1/4), sums over blocks are 32-bit; products of
-// e4m3 span 22 places, and what is dropped comes to 4.5e-6 of the result (2-norm), far
-// below the rounding of a 16-bit one.  For 32-bit results (FINE) the elements of magnitude
-// 2 and more, whose codes have bit 6, and the rest go through an instruction each.
-template <bool A8, bool FINE> __device__ __forceinline__ v4f mfma_mx(v8i w, v8i x, v4f acc, int ws, int xs) {
-  if constexpr (A8 && FINE) {
+// more than 13 binary places below it, counted by the factors' exponents (measured:
+// 256 * 1 + 2^-5 * 1 is kept, + 2^-6 is not; 448 * 6 + 2.25 * 0.5, whose last bit is 2^-3, is
+// kept whole).  Products of e2m1 fit (4 * 4 down to 1/4), sums over blocks are 32-bit.
+// Products of e4m3 span 20 places (256 * 4 down to 2^-10), so its elements of magnitude 2 and
+// more, whose codes have bit 6, go through one instruction (2^10 down to 2^-3) and the rest
+// through another (4 down to 2^-10): nothing is dropped.  In one instruction a block whose
+// large products cancel, as those of an outlier column may, would lose its result: 8192 x
+// 8192 x 8192 would take 370 us so, against 757 (614 without the work of splitting).
+template <bool A8> __device__ __forceinline__ v4f mfma_mx(v8i w, v8i x, v4f acc, int ws, int xs) {
+  if constexpr (A8) {
     v8i high;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -67,8 +70,8 @@ __device__ __forceinline__ uint4 scales16(const uint8_t *row, uint32_t b, uint32
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// Few rows of A: bound by the weights' bytes (1 x 8192 outputs, 8192 deep: 10 us, 3.6 TB/s of
-// weights).  A workgroup computes 16 x 16 outputs, its wavefronts take the steps of k in
+// Few rows of A: bound by the weights' bytes (1 x 8192 outputs, 8192 deep: 8.3 us from e2m1,
+// 4.3 TB/s of weights, 10.2 from e4m3, 3.5 TB/s).  A workgroup computes 16 x 16 outputs, its wavefronts take the steps of k in
 // turn and their sums are added in order through LDS.  A step is 16 blocks, four matrix
 // instructions; each load takes 64 consecutive bytes of 16 rows.
 template <bool A8, int DO> __global__ void mx_direct_kernel(MxMatmulArgs a) {
@@ -97,8 +100,8 @@ template <bool A8, int DO> __global__ void mx_direct_kernel(MxMatmulArgs a) {
     const uint32_t wd[4] = {ws4.x, ws4.y, ws4.z, ws4.w}, xd[4] = {xs4.x, xs4.y, xs4.z, xs4.w};
 #pragma unroll
     for (int s = 0; s < 4; ++s)
-      acc = mfma_mx<A8, DO == IBP_F32>(operand(w[s], make_uint4(0u, 0u, 0u, 0u)), operand(lo[s], hi[s]), acc,
-                                       (int)(wd[s] >> (8 * g)), (int)(xd[s] >> (8 * g)));
+      acc = mfma_mx<A8>(operand(w[s], make_uint4(0u, 0u, 0u, 0u)), operand(lo[s], hi[s]), acc, (int)(wd[s] >> (8 * g)),
+                         (int)(xd[s] >> (8 * g)));
   }
   if (waves > 1) {
     if (wave) *reinterpret_cast<v4f *>(red + (wave - 1) * 256 + lane * 4) = acc;
@@ -167,7 +170,7 @@ template <uint32_t ROWS, uint32_t PITCH, uint32_t WAVES> struct Tile {
   }
 };
 
-template <bool A8, bool FINE, int WM, int WN, int FM, int FN, int DO>
+template <bool A8, int WM, int WN, int FM, int FN, int DO>
 __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, void *dst, uint32_t tiles_m,
                                                              uint32_t tiles_n, uint32_t stages_each) {
   using TO = typename Num<DO>::T;
@@ -297,7 +300,7 @@ __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, voi
 #pragma unroll
     for (int m = 0; m < FM; ++m) {
 #pragma unroll
-      for (int n = 0; n < FN; ++n) acc[n][m] = mfma_mx<A8, FINE>(w[n], v[m], acc[n][m], ws[n], xs[m]);
+      for (int n = 0; n < FN; ++n) acc[n][m] = mfma_mx<A8>(w[n], v[m], acc[n][m], ws[n], xs[m]);
       if (kLateFill && m == 0) {
         __builtin_amdgcn_sched_barrier(0);  // the compiler would issue the loads first
         fill(free_stage, k + kStages - 1);
@@ -368,11 +371,13 @@ struct Plan {
 Plan plan_of(uint64_t M, uint64_t N, uint32_t K) {
   Plan p{Plan::kDirect, 0, 0, 1, 1};
   // Few rows, or so few outputs that one round of the direct kernel's workgroups covers
-  // them (8192 x 8192 weights: 16 rows 13 us against 15 for the tiles, 32 rows 21 against 15).
+  // them (8192 x 8192 weights: 16 rows of e2m1 11.5 us against 15.2 for the tiles, 32 rows 20.1
+  // against 15.3; of e4m3 15.8 against 25.9, 28.2 against 25.6).
   const uint64_t blocks = ((M + 15) / 16) * ((N + 15) / 16);
   if (blocks <= 512 || (M <= 16 && blocks <= 1u << 22)) return p;
-  // Many rows: the larger tiles from 192 of them on (1536 x 8192 outputs, 4096 deep: 37 us
-  // against 47; 1024 x 8192, 8192 deep, 128 large tiles: 62 against 56).
+  // Many rows: the larger tiles from 192 of them on (e2m1: 1536 x 8192 outputs, 4096 deep 34
+  // us against 45, 8192 deep 60 against 83; 1024 x 8192, 8192 deep, 128 large tiles: 54 each;
+  // e4m3: 98 against 95, 185 against 178; 185 against 106).
   const bool big = ((M + 255) / 256) * ((N + 255) / 256) >= 192;
   const uint32_t wide = big ? 256 : 128;
   p.kind = big ? Plan::kBig : Plan::kMiddle;
@@ -382,7 +387,7 @@ Plan plan_of(uint64_t M, uint64_t N, uint32_t K) {
   const uint32_t stages = (uint32_t)((mx_blocks(K) + 3) / 4);
   // One workgroup takes half a microsecond a stage however few there are: k is cut into
   // ranges of whole scale groups (4 stages), at least 8 stages each, until there is one per
-  // CU (128 x 8192 outputs, 8192 deep: 31.5 us in one range, 19.8 in four).
+  // CU (128 x 8192 outputs, 8192 deep: e2m1 31 us in one range, 19.3 in four; e4m3 73, 29.7).
   const uint64_t want = big ? 1 : 256 / tiles, most = stages / 8;
   uint32_t n = (uint32_t)(want < most ? want : most);
   n = n < 1 ? 1 : (n > 8 ? 8 : n);
@@ -392,12 +397,12 @@ Plan plan_of(uint64_t M, uint64_t N, uint32_t K) {
   return p;
 }
 
-template <bool A8, bool FINE, int DO> hipError_t go_tile(const MxMatmulArgs &a, const Plan &p, void *dst, hipStream_t s) {
+template <bool A8, int DO> hipError_t go_tile(const MxMatmulArgs &a, const Plan &p, void *dst, hipStream_t s) {
   const dim3 grid(p.tiles_m * p.tiles_n, p.splits);
   if (p.kind == Plan::kBig)
-    mx_tile_kernel<A8, FINE, 2, 4, 8, 4, DO><<<grid, 512, 0, s>>>(a, dst, p.tiles_m, p.tiles_n, p.stages_each);
+    mx_tile_kernel<A8, 2, 4, 8, 4, DO><<<grid, 512, 0, s>>>(a, dst, p.tiles_m, p.tiles_n, p.stages_each);
   else
-    mx_tile_kernel<A8, FINE, 2, 2, 4, 4, DO><<<grid, 256, 0, s>>>(a, dst, p.tiles_m, p.tiles_n, p.stages_each);
+    mx_tile_kernel<A8, 2, 2, 4, 4, DO><<<grid, 256, 0, s>>>(a, dst, p.tiles_m, p.tiles_n, p.stages_each);
   return hipGetLastError();
 }
 
@@ -406,12 +411,11 @@ template <bool A8> hipError_t go(const MxMatmulArgs &a, hipStream_t s) {
   if (p.kind == Plan::kDirect) return go_direct<A8>(a, s);
   if ((uint64_t)p.tiles_m * p.tiles_n > 0x7FFFFF) return hipErrorInvalidValue;
   if (p.splits > 1) {
-    const bool fine = A8 && a.dtype == IBP_F32;
-    const hipError_t e = fine ? go_tile<A8, A8, IBP_F32>(a, p, a.ws, s) : go_tile<A8, false, IBP_F32>(a, p, a.ws, s);
+    const hipError_t e = go_tile<A8, IBP_F32>(a, p, a.ws, s);
     if (e != hipSuccess) return e;
   }
   return with_dtype(a.dtype, [&](auto d) {
-    if (p.splits == 1) return go_tile<A8, A8 && d.value == IBP_F32, d.value>(a, p, a.y, s);
+    if (p.splits == 1) return go_tile<A8, d.value>(a, p, a.y, s);
     const uint64_t n = (a.M * a.N + kBlock * 4 - 1) / (kBlock * 4);
     mx_join_kernel<d.value><<<(uint32_t)(n < 4096 ? n : 4096), kBlock, 0, s>>>(a, p.splits);
     return hipGetLastError();

@@ -435,9 +435,7 @@ IBP_API uint64_t ibp_mx_linear_wgrad_workspace_bytes(uint64_t tokens, uint64_t o
 
 /*
  * Product with packed weights: d_y[i][j] = sum over k of a[i][k] * b[j][k], a of M rows
- * (e4m3 or e2m1), b of N rows (e2m1), a->cols == b->cols, d_y M x N of dtype.  Sums
- * are held in 32 bits; for a 16-bit d_y the products of an e4m3 block are added with
- * what lies 14 binary places below the block's largest cut off (4.5e-6 of the result).
+ * (e4m3 or e2m1), b of N rows (e2m1), a->cols == b->cols, d_y M x N of dtype.
  * d_workspace may be NULL when the query says 0; aligned to 16.  Asynchronous.
  */
 IBP_API int ibp_mx_matmul(const ibp_mx_t *a, const ibp_mx_t *b, void *d_y, int dtype, void *d_workspace,

@@ -1,0 +1,92 @@
+"""The language-model operators on the GPU at the ends of their ranges: what
+test_gpu_operators.py does not reach."""
+import numpy as np
+import pytest
+import torch
+
+import mx_ref
+
+pytestmark = pytest.mark.gpu
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module")
+def ibp():
+    import bit_packing_amd
+
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    bit_packing_amd.load_library()
+    return bit_packing_amd
+
+
+def device(ibp, codes, scales, cols, fmt):
+    return ibp.MxTensor(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), codes.shape[0], cols, fmt)
+
+
+def rounded(want, t):
+    """A float64 matrix whose values 32 bits hold, rounded once to a type."""
+    assert np.array_equal(want, want.astype(np.float32))
+    return torch.from_numpy(want.astype(np.float32)).to(DT[t]).cuda()
+
+
+# ---------------------------------------------------------------- products of far apart sizes
+
+def nibbles(k):
+    return k[:, 0::2] | (k[:, 1::2] << 4)
+
+
+def limit_product(fmt, how, seed):
+    """Every code v of A (rows) with every code w of B next to the largest product of the
+    types, 448 * 6 or 6 * 6: in one block, cancelled in that block, in another block of the
+    same 128 columns or behind them, or with v w in all other places of the block.  Sums of
+    up to 33 terms are whole multiples of the step of v w, below 2^24 of them: any order of
+    adding in 32 bits is exact."""
+    rng = np.random.default_rng(seed)
+    nv, cols = (126, 160) if fmt == mx_ref.E4M3 else (7, 160)
+    a, b = np.zeros((nv, cols), np.uint8), np.zeros((7, cols), np.uint8)
+    sign = 128 if fmt == mx_ref.E4M3 else 8
+    v = np.arange(1, nv + 1) + sign * rng.integers(0, 2, nv)
+    w = np.arange(1, 8)
+    p = 32 + rng.permutation(32)
+    a[:, p[0]], b[:, p[0]] = nv, 7
+    places = p[1:] if how == "many" else p[1:2]
+    a[:, places], b[:, places] = v[:, None], w[:, None]
+    other = {"block": p[2], "instruction": 64 + 5, "later": 128 + 9}.get(how)
+    if other:
+        a[:, other], b[:, other] = nv, 7 + 8
+    scales = lambda rows: np.where(np.arange(8) < 5, 127, 0).astype(np.uint8)[None].repeat(rows, 0)  # noqa: E731
+    return (a if fmt == mx_ref.E4M3 else nibbles(a), scales(nv)), (nibbles(b), scales(7)), cols
+
+
+@pytest.mark.parametrize("m,n", [(126, 7), (130, 1100), (3500, 3600)])  # one form of the product each
+@pytest.mark.parametrize("how", ["beside", "block", "instruction", "later", "many"])
+@pytest.mark.parametrize("t", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("fmt", [mx_ref.E4M3, mx_ref.E2M1])
+def test_matmul_keeps_every_product(ibp, fmt, t, how, m, n):
+    a, b, cols = limit_product(fmt, how, 1)
+    want = mx_ref.unpack(*a, cols, fmt) @ mx_ref.unpack(*b, cols, mx_ref.E2M1).T
+    ra, rb = np.arange(m) % len(want), np.arange(n) % 7
+    print(f"product: m={m} n={n} format={fmt} {t} {how}", flush=True)
+    y = ibp.ibp_mx_matmul(device(ibp, a[0][ra], a[1][ra], cols, fmt), device(ibp, b[0][rb], b[1][rb], cols, mx_ref.E2M1),
+                          dtype=DT[t])
+    want = rounded(want, t)[torch.from_numpy(ra).cuda()][:, torch.from_numpy(rb).cuda()]
+    off = (y != want).nonzero()
+    assert len(off) == 0, (len(off), off[0].tolist(), y[tuple(off[0])].item(), want[tuple(off[0])].item())
+
+
+@pytest.mark.parametrize("m,n", [(24, 7), (130, 1100), (3500, 3600)])
+@pytest.mark.parametrize("fmt", [mx_ref.E4M3, mx_ref.E2M1])
+def test_matmul_blocks_of_far_apart_scales(ibp, fmt, m, n):
+    """One block of 2^j, j up to 23, and one of 1 in the same 128 columns, another behind them."""
+    cols, one = 160, {mx_ref.E4M3: 56, mx_ref.E2M1: 2}
+    j = np.arange(m) % 24
+    a, b = np.zeros((m, cols), np.uint8), np.zeros((n, cols), np.uint8)
+    for c in (3, 70, 140):
+        a[:, c], b[:, c] = one[fmt], one[mx_ref.E2M1]
+    sa = np.where(np.arange(8) < 5, 127, 0).astype(np.uint8)[None].repeat(m, 0)
+    sb = np.where(np.arange(8) < 5, 127, 0).astype(np.uint8)[None].repeat(n, 0)
+    sa[:, 0] = 127 + j
+    y = ibp.ibp_mx_matmul(device(ibp, a if fmt == mx_ref.E4M3 else nibbles(a), sa, cols, fmt),
+                          device(ibp, nibbles(b), sb, cols, mx_ref.E2M1), dtype=torch.float32)
+    want = torch.from_numpy((2.0 ** j + 2).astype(np.float32)).cuda()[:, None].expand(m, n)
+    assert torch.equal(y, want)
