@@ -356,8 +356,9 @@ Plan plan_of(uint64_t T, uint32_t N, uint32_t K, int dy_dtype, bool aligned) {
   // 75, 299 inputs 93 against 87, 2400 inputs 557 against 291)
   p.copied = p.parts > 1 || (N % 8 != 0 && K > 256);
   // BF16 rows of whole pieces that begin off 16 bytes take the small tile, through registers:
-  // its ranges are as many or fewer, so the workspace is large enough for both
-  p.big = (big > 128 || (T >= 3500 && big * T >= 140000)) && (p.copied || (aligned && N % 8 == 0));
+  // its ranges are as many or fewer, so the workspace is large enough for both.  Without tokens
+  // there is nothing to lay out, and the small tile writes the zeros.
+  p.big = T > 0 && (big > 128 || (T >= 3500 && big * T >= 140000)) && (p.copied || (aligned && N % 8 == 0));
   p.copied = p.copied && p.big;
   const uint32_t wide = p.big ? 256 : 128;
   p.tiles_o = (uint32_t)(((uint64_t)N + wide - 1) / wide);

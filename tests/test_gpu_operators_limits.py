@@ -90,3 +90,16 @@ def test_matmul_blocks_of_far_apart_scales(ibp, fmt, m, n):
                           device(ibp, nibbles(b), sb, cols, mx_ref.E2M1), dtype=torch.float32)
     want = torch.from_numpy((2.0 ** j + 2).astype(np.float32)).cuda()[:, None].expand(m, n)
     assert torch.equal(y, want)
+
+
+# ---------------------------------------------------------------- sizes of zero
+
+@pytest.mark.parametrize("ty,n,k", [("f32", 4096, 4096), ("f16", 4096, 4096), ("bf16", 4097, 4096), ("bf16", 4096, 4096),
+                                    ("f32", 130, 70), ("bf16", 130, 70)])
+@pytest.mark.parametrize("to", ["f32", "bf16"])
+def test_wgrad_of_no_tokens(ibp, ty, to, n, k):
+    """A layer without tokens, large or small, has the gradient 0."""
+    x8 = ibp.make_mx(0, k, ibp.IBP_MX_E4M3, "cuda")
+    dw = torch.full((n, k), float("nan"), dtype=DT[to], device="cuda")
+    ibp.ibp_mx_linear_wgrad(torch.zeros(0, n, dtype=DT[ty], device="cuda"), x8, dw=dw)
+    assert dw.eq(0).all()
