@@ -30,6 +30,7 @@ raise.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from dataclasses import dataclass
 
@@ -587,8 +588,7 @@ def _matrix(x: torch.Tensor) -> tuple[int, int]:
     """(rows, cols) of a tensor read as rows of its last dimension."""
     if x.dim() == 0:
         raise ValueError("a tensor of rows is needed")
-    cols = x.shape[-1]
-    return (x.numel() // cols if cols else 0), cols
+    return math.prod(x.shape[:-1]), x.shape[-1]
 
 
 def _out(out: torch.Tensor | None, shape, dtype, device) -> torch.Tensor:
@@ -730,7 +730,7 @@ def ibp_mx_swiglu_backward(dh: torch.Tensor, gate8: MxTensor, up8: MxTensor, dga
     if stream is not None:
         with _stream_context(stream):
             return ibp_mx_swiglu_backward(dh, gate8, up8, dgate, dup)
-    if _matrix(dh) != (gate8.rows, gate8.cols) and dh.numel():
+    if _matrix(dh) != (gate8.rows, gate8.cols):
         raise ValueError("dh and the checkpoints differ in shape")
     dev = _device(dh)
     dgate = torch.empty_like(dh) if dgate is None else _out(dgate, dh.shape, dh.dtype, dev)

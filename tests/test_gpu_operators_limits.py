@@ -103,3 +103,22 @@ def test_wgrad_of_no_tokens(ibp, ty, to, n, k):
     dw = torch.full((n, k), float("nan"), dtype=DT[to], device="cuda")
     ibp.ibp_mx_linear_wgrad(torch.zeros(0, n, dtype=DT[ty], device="cuda"), x8, dw=dw)
     assert dw.eq(0).all()
+
+
+def test_rows_of_no_columns_stay_rows(ibp):
+    """Packing keeps the rows of a tensor without columns, and its product has them, as zeros."""
+    for shape, rows in (((5, 0), 5), ((2, 3, 0), 6), ((0, 7), 0)):
+        x = torch.zeros(shape, device="cuda")
+        a = ibp.ibp_mx_pack(x, ibp.IBP_MX_E4M3)
+        assert (a.rows, a.cols) == (rows, shape[-1])
+        assert ibp.ibp_mx_unpack(a).shape == (rows, shape[-1])
+        b = ibp.ibp_mx_pack(torch.zeros(9, shape[-1], device="cuda"), ibp.IBP_MX_E2M1)
+        y = torch.full((rows, 9), float("nan"), device="cuda")
+        ibp.ibp_mx_matmul(a, b, dtype=torch.float32, out=y)
+        assert y.eq(0).all()
+        h, gate8, up8 = ibp.ibp_mx_swiglu(x, x)
+        assert h.shape == shape and gate8.rows == up8.rows == rows
+        dgate, dup = ibp.ibp_mx_swiglu_backward(x, gate8, up8)
+        assert dgate.shape == dup.shape == shape
+        dw = ibp.ibp_mx_linear_wgrad(torch.ones(rows, 4, device="cuda"), a)
+        assert dw.shape == (4, shape[-1]) and dw.eq(0).all()
