@@ -62,22 +62,50 @@ template <bool E4M3> __device__ __forceinline__ uint2 load_codes(const uint8_t *
   return make_uint2(*reinterpret_cast<const uint32_t *>(codes + c / 2), 0u);
 }
 
-// 1 / (1 + exp(-g)).  The 16-bit types take it from the hardware's exp2 and reciprocal
-// (1 unit of the last place each), the argument's rounding made good by a factor: 6 half
-// units in all, far below the result's own rounding, for a third of the instructions
+// 1 / (1 + exp(-g)) of eight gates.  The 16-bit types take it from the hardware's exp2 and
+// reciprocal (1 unit of the last place each), the argument's rounding made good by a factor: 6
+// half units in all, far below the result's own rounding, for a third of the instructions
 // (forward of 16384 x 8192 in bf16 204 us against 245 with the library's exp and a true
 // quotient, which 32-bit results take).
-template <int D> __device__ __forceinline__ float sigmoid(float g) {
+//
+// Where a wavefront has a gate below -80, whose exp(-g) may overflow and whose reciprocal is
+// flushed to zero from -87.3 on, all its gates go by e = exp(-|g|), which fades out through the
+// subnormal numbers: 1 / (1 + e), times e for negative g (7 half units).  For every gate that
+// takes 213 us.
+template <int D> __device__ __forceinline__ F8 sigmoid8(const F8 &g) {
+  F8 s;
   if constexpr (D == IBP_F32) {
-    return 1.0f / (1.0f + expf(-g));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float e = expf(-fabsf(g.v[i]));
+      s.v[i] = (g.v[i] < 0.0f ? e : 1.0f) / (1.0f + e);
+    }
   } else {
     constexpr float kLog2e = 1.44269502162933349609375f, kLog2eRest = 1.925963033500011e-8f, kLn2 = 0.693147182f;
-    const float x = fminf(fmaxf(-g, -200.0f), 200.0f);  // exp2 is 0 or infinite beyond
-    const float t = x * kLog2e;
-    const float rest = fmaf(x, kLog2eRest, fmaf(x, kLog2e, -t));
-    const float e = __builtin_amdgcn_exp2f(t) * fmaf(rest, kLn2, 1.0f);
-    return __builtin_amdgcn_rcpf(1.0f + e);
+    float least = g.v[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) least = fminf(least, g.v[i]);
+    if (ballot(least < -80.0f) == 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float x = fmaxf(-g.v[i], -200.0f);  // exp2 is 0 beyond
+        const float t = x * kLog2e;
+        const float rest = fmaf(x, kLog2eRest, fmaf(x, kLog2e, -t));
+        const float e = __builtin_amdgcn_exp2f(t) * fmaf(rest, kLn2, 1.0f);
+        s.v[i] = __builtin_amdgcn_rcpf(1.0f + e);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float x = -fminf(fabsf(g.v[i]), 200.0f);
+        const float n = __builtin_rintf(x * kLog2e);
+        const float f = fmaf(x, kLog2eRest, fmaf(x, kLog2e, -n));
+        const float e = __builtin_ldexpf(__builtin_amdgcn_exp2f(f), (int)n), r = __builtin_amdgcn_rcpf(1.0f + e);
+        s.v[i] = g.v[i] < 0.0f ? e * r : r;
+      }
+    }
   }
+  return s;
 }
 
 struct Walk {
@@ -162,9 +190,9 @@ template <int D, uint32_t R> __global__ __launch_bounds__(kBlock) void mx_swiglu
         const F8 g = widen<wide.value, T>(vg[k], p.c, a.cols), u = widen<wide.value, T>(vu[k], p.c, a.cols);
         encode_lane<true>(g, a.codes + p.row[k] * cp, a.scales + p.row[k] * sp, p.c, nblk, p.ok[k]);
         encode_lane<true>(u, a.codes2 + p.row[k] * cp, a.scales2 + p.row[k] * sp, p.c, nblk, p.ok[k]);
-        F8 o;
+        F8 o = sigmoid8<D>(g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o.v[i] = g.v[i] * sigmoid<D>(g.v[i]) * u.v[i];
+        for (int i = 0; i < 8; ++i) o.v[i] = g.v[i] * o.v[i] * u.v[i];
         if (p.ok[k] && p.c < a.cols) store8<T>(h + p.row[k] * a.cols, p.c, a.cols, o);
       }
     }
@@ -197,11 +225,12 @@ template <int D, uint32_t R> __global__ __launch_bounds__(kBlock) void mx_swiglu
       for (uint32_t k = 0; k < R; ++k) {
         if (!p.ok[k]) continue;
         const F8 g = mx_decode<true>(qg[k], sg[k]), u = mx_decode<true>(qu[k], su[k]), d = widen<wide.value, T>(vd[k], p.c, a.cols);
+        const F8 s = sigmoid8<D>(g);
         F8 og, ou;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float s = sigmoid<D>(g.v[i]), ds = d.v[i] * s;
-          og.v[i] = ds * u.v[i] * (1.0f + g.v[i] * (1.0f - s));
+          const float ds = d.v[i] * s.v[i];
+          og.v[i] = ds * u.v[i] * (1.0f + g.v[i] * (1.0f - s.v[i]));
           ou.v[i] = ds * g.v[i];
         }
         store8<T>(dgate + p.row[k] * a.cols, p.c, a.cols, og);

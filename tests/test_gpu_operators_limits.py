@@ -122,3 +122,46 @@ def test_rows_of_no_columns_stay_rows(ibp):
         assert dgate.shape == dup.shape == shape
         dw = ibp.ibp_mx_linear_wgrad(torch.ones(rows, 4, device="cuda"), a)
         assert dw.shape == (4, shape[-1]) and dw.eq(0).all()
+
+
+# ---------------------------------------------------------------- the gated activation far from zero
+
+@pytest.mark.parametrize("t", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("least", [-80, -1000])
+def test_swiglu_of_far_gates(ibp, t, least):
+    """Gates whose sigmoid is a subnormal number, or exp(-g) above the largest: the results are
+    not (|u| up to 2^100, dh powers of two from 1 on).  The sigmoid is held in 32 bits: 6 units of
+    2^-24, or four steps of the subnormal numbers (exp, its sum and quotient or product); two
+    products and the last rounding as everywhere."""
+    U, tiny = 2.0 ** -24, {"f32": 2.0 ** -150, "f16": 2.0 ** -25, "bf16": 2.0 ** -134}[t]
+    half = torch.finfo(DT[t]).eps / 2
+    rng = np.random.default_rng(31)
+    gates = -np.concatenate([np.arange(80, 112, 0.5), [64, 72, 120, 192, 200, 208, 1000]])
+    gates = np.concatenate([gates[gates >= least], -gates, np.arange(-80, 0, 1.5), [0.0, -0.0, 1.0, -1.0]])
+    rows, cols = 40, len(gates)
+    power = (0, 15) if t == "f16" else (0, 100)
+    g = torch.from_numpy(np.tile(gates, (rows, 1))).to(DT[t]).cuda()
+    u = torch.from_numpy(rng.choice([-1.0, 1], (rows, cols)) * 2.0 ** rng.integers(*power, (rows, 1))).to(DT[t]).cuda()
+    dh = torch.from_numpy(2.0 ** rng.integers(0, 10, (rows, cols))).to(DT[t]).cuda()
+    h, g8, u8 = ibp.ibp_mx_swiglu(g, u)
+    dg, du = ibp.ibp_mx_swiglu_backward(dh, g8, u8)
+    host = lambda x: x.double().cpu().numpy()  # noqa: E731
+    xg, xu, xd = host(g), host(u), host(dh)
+    top = torch.finfo(DT[t]).max
+
+    def near(got, want, bound, what):
+        got, fine = host(got), np.abs(want) <= top
+        assert np.array_equal(got[~fine], np.sign(want[~fine]) * np.inf)
+        over = (np.abs(got - want) - bound)[fine]
+        at = np.argmax(over)
+        assert over[at] <= 0, (what, np.broadcast_to(xg, want.shape)[fine][at], got[fine][at], want[fine][at])
+
+    sig = lambda x: np.exp(np.minimum(x, 0)) / (1 + np.exp(-np.abs(x)))  # noqa: E731
+    want = xg * sig(xg) * xu
+    near(h, want, np.abs(want) * (half + 8 * U) + np.abs(xg * xu) * 2.0 ** -147 + tiny, "h")
+    kg, ku = (host(ibp.ibp_mx_unpack(m, torch.float32)) for m in (g8, u8))
+    s = sig(kg)
+    want = xd * ku * s * (1 + kg * sig(-kg))
+    near(dg, want, np.abs(want) * half + np.abs(xd * ku) * (1 + np.abs(kg)) * (12 * U * s + 2.0 ** -147) + tiny, "dgate")
+    want = xd * kg * s
+    near(du, want, np.abs(want) * (half + 8 * U) + np.abs(xd * kg) * 2.0 ** -147 + tiny, "dup")
