@@ -879,11 +879,42 @@ static int gated_check(const void *x, const void *y, const void *z, int dtype, c
   return IBP_OK;
 }
 
+struct Range { const void *p; uint64_t bytes; };
+
+static bool overlap(const Range &x, const Range &y) {
+  return (uintptr_t)x.p < (uintptr_t)y.p + y.bytes && (uintptr_t)y.p < (uintptr_t)x.p + x.bytes;
+}
+
+// Whether outputs lie apart from each other and from the inputs.  The first plain_outs and
+// plain_ins of them are plain tensors: such an output may be such an input itself where what
+// a lane writes is read by that lane alone, or before by its own wavefront: the last lane of a
+// row reads the row's last eight elements, some of them its neighbour's, and a row of up to
+// 512 elements belongs to one wavefront.
+static bool apart(std::initializer_list<Range> outs, uint32_t plain_outs, std::initializer_list<Range> ins,
+                  uint32_t plain_ins, uint64_t cols) {
+  const bool in_place = cols % 8 == 0 || cols <= 512;
+  for (const Range *o = outs.begin(); o != outs.end(); ++o) {
+    for (const Range *q = o + 1; q != outs.end(); ++q)
+      if (overlap(*o, *q)) return false;
+    for (const Range *i = ins.begin(); i != ins.end(); ++i) {
+      const bool itself = o->p == i->p && o < outs.begin() + plain_outs && i < ins.begin() + plain_ins;
+      if (overlap(*o, *i) && !(itself && in_place)) return false;
+    }
+  }
+  return true;
+}
+
+static Range codes_range(const ibp_mx_t *t) { return {t->codes, t->rows * mx_code_pitch(t->cols, t->format == IBP_MX_E4M3)}; }
+static Range scales_range(const ibp_mx_t *t) { return {t->scales, t->rows * mx_scale_pitch(t->cols)}; }
+
 IBP_API int ibp_mx_swiglu(const void *d_gate, const void *d_up, int dtype, void *d_h, const ibp_mx_t *gate8,
                           const ibp_mx_t *up8, void *hip_stream) {
   uint64_t b = 0;
   if (const int rc = gated_check(d_gate, d_up, d_h, dtype, gate8, up8, &b)) return rc;
   if (b == 0) return IBP_OK;
+  if (!apart({{d_h, b}, codes_range(gate8), scales_range(gate8), codes_range(up8), scales_range(up8)}, 1,
+             {{d_gate, b}, {d_up, b}}, 2, gate8->cols))
+    return IBP_ERR_INVALID_ARG;
   MxArgs a;
   mx_fill(&a, gate8, dtype);
   if (!view(d_gate, b) || !view(d_up, b) || !view(d_h, b) || !mx_view(gate8, &a.codes, &a.scales) ||
@@ -900,6 +931,9 @@ IBP_API int ibp_mx_swiglu_backward(const void *d_dh, int dtype, const ibp_mx_t *
   uint64_t b = 0;
   if (const int rc = gated_check(d_dh, d_dgate, d_dup, dtype, gate8, up8, &b)) return rc;
   if (b == 0) return IBP_OK;
+  if (!apart({{d_dgate, b}, {d_dup, b}}, 2,
+             {{d_dh, b}, codes_range(gate8), scales_range(gate8), codes_range(up8), scales_range(up8)}, 1, gate8->cols))
+    return IBP_ERR_INVALID_ARG;
   MxArgs a;
   mx_fill(&a, gate8, dtype);
   if (!view(d_dh, b) || !view(d_dgate, b) || !view(d_dup, b) || !mx_view(gate8, &a.codes, &a.scales) ||

@@ -421,8 +421,10 @@ IBP_API int ibp_mx_unpack(const ibp_mx_t *in, void *d_out, int dtype, void *hip_
  * silu(g) = g / (1 + exp(-g)), from the inputs as they come, and gate8 / up8 = their
  * e4m3 packings, in one pass.  All are gate8->rows x gate8->cols; gate8 and up8 have
  * one shape.  The backward pass takes g and u from the checkpoints: with
- * s = 1 / (1 + exp(-g)), d_dgate = dh u s (1 + g (1 - s)) and d_dup = dh g s.
- * Asynchronous.
+ * s = 1 / (1 + exp(-g)), d_dgate = dh u s (1 + g (1 - s)) and d_dup = dh g s.  d_h may be
+ * d_gate or d_up itself, and d_dgate or d_dup may be d_dh, where cols is a multiple of 8
+ * or at most 512; any other overlap of an output with an input or another output is
+ * IBP_ERR_INVALID_ARG.  Asynchronous.
  */
 IBP_API int ibp_mx_swiglu(const void *d_gate, const void *d_up, int dtype, void *d_h, const ibp_mx_t *gate8,
                           const ibp_mx_t *up8, void *hip_stream);

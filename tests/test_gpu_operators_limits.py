@@ -165,3 +165,48 @@ def test_swiglu_of_far_gates(ibp, t, least):
     near(dg, want, np.abs(want) * half + np.abs(xd * ku) * (1 + np.abs(kg)) * (12 * U * s + 2.0 ** -147) + tiny, "dgate")
     want = xd * kg * s
     near(du, want, np.abs(want) * (half + 8 * U) + np.abs(xd * kg) * 2.0 ** -147 + tiny, "dup")
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(70, 1000), (300, 512), (41, 333), (9, 4096), (2000, 2048)])
+def test_swiglu_in_place(ibp, t, rows, cols):
+    """Outputs in the place of an input equal those of their own."""
+    rng = np.random.default_rng(cols)
+    g, u, d = (torch.from_numpy(rng.standard_normal((rows, cols))).to(DT[t]).cuda() for _ in range(3))
+    h, g8, u8 = ibp.ibp_mx_swiglu(g, u)
+    dg, du = ibp.ibp_mx_swiglu_backward(d, g8, u8)
+    for first in (True, False):
+        x, y, e = g.clone(), u.clone(), d.clone()
+        got, p8, q8 = ibp.ibp_mx_swiglu(x, y, h=x if first else y)
+        assert torch.equal(got, h) and got.data_ptr() == (x if first else y).data_ptr()
+        assert torch.equal(p8.codes, g8.codes) and torch.equal(q8.codes, u8.codes)
+        assert torch.equal(p8.scales, g8.scales) and torch.equal(q8.scales, u8.scales)
+        a, b = ibp.ibp_mx_swiglu_backward(e, g8, u8, dgate=e if first else None, dup=None if first else e)
+        assert torch.equal(a, dg) and torch.equal(b, du)
+
+
+@pytest.mark.parametrize("cols,in_place", [(513, False), (1000, True), (509, True), (4097, False), (3, True)])
+def test_gated_overlaps_are_refused(ibp, cols, in_place):
+    """Outputs that overlap, and inputs in whose place another wavefront may still read."""
+    import ctypes
+
+    rows, step, ref = 4, 1 << 18, ctypes.byref  # each tensor somewhere in a quarter of a megabyte of its own
+    flat = torch.zeros(8 * step, dtype=torch.uint8, device="cuda")
+    at = lambda i, off=0: flat.data_ptr() + i * step + off  # noqa: E731
+    mx = lambda i: ibp.ibp_mx_t(0, 0, rows, cols, at(i), at(i, step // 2))  # noqa: E731
+    lib, end = ibp.load_library(), rows * cols * 4
+
+    def forward(gate=at(0), up=at(1), h=at(2), g8=mx(4), u8=mx(5)):
+        return lib.ibp_mx_swiglu(gate, up, ibp.IBP_F32, h, ref(g8), ref(u8), None)
+
+    def back(dh=at(0), dg=at(1), du=at(2), g8=mx(4), u8=mx(5)):
+        return lib.ibp_mx_swiglu_backward(dh, ibp.IBP_F32, ref(g8), ref(u8), dg, du, None)
+
+    assert forward() == back() == ibp.IBP_OK
+    some = [forward(h=at(0)), forward(h=at(1)), back(dg=at(0)), back(du=at(0))]
+    assert some == [ibp.IBP_OK if in_place else ibp.IBP_ERR_INVALID_ARG] * 4
+    bad = [forward(h=at(0, 4)), forward(h=at(0, end - 4)), forward(h=at(1, -4)), forward(h=at(4)), forward(h=at(4, step // 2)),
+           forward(g8=mx(5)), forward(gate=at(4)), forward(up=at(5, step // 2)), back(dg=at(2)), back(dg=at(0, 4)),
+           back(du=at(0, 4)), back(dg=at(4)), back(du=at(5, step // 2)), back(dg=at(2, -4))]
+    assert bad == [ibp.IBP_ERR_INVALID_ARG] * len(bad)
+    torch.cuda.synchronize()
