@@ -210,3 +210,99 @@ def test_gated_overlaps_are_refused(ibp, cols, in_place):
            back(du=at(0, 4)), back(dg=at(4)), back(du=at(5, step // 2)), back(dg=at(2, -4))]
     assert bad == [ibp.IBP_ERR_INVALID_ARG] * len(bad)
     torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------- long products, cut products
+
+def codes_of(rng, rows, cols, fmt):
+    """Whole multiples of 1/4 below 4 (e4m3) or all codes (e2m1) times scales of 1/2 to 2."""
+    v = mx_ref.TABLE[fmt]
+    pick = np.flatnonzero((v * 4 == np.floor(v * 4)) & (v < 4)) if fmt == mx_ref.E4M3 else np.arange(8)
+    w = mx_ref.blocks(cols) * 32
+    k = (rng.choice(pick, (rows, w)) + rng.integers(0, 2, (rows, w)) * (128 if fmt == mx_ref.E4M3 else 8)).astype(np.uint8)
+    k[:, cols:] = 0
+    s = np.zeros((rows, mx_ref.scale_pitch(cols)), np.uint8)
+    s[:, : mx_ref.blocks(cols)] = rng.integers(126, 129, (rows, mx_ref.blocks(cols)))
+    return k if fmt == mx_ref.E4M3 else nibbles(k), s
+
+
+def exact_product(va, vb, step):
+    """va vb^T in 64 bits on the GPU; every partial sum is a whole number of steps below 2^24."""
+    a, b = (torch.from_numpy(x).cuda() for x in (va, vb))
+    assert (a.abs() @ b.abs().t().contiguous()).max().item() < 2.0 ** 24 * step
+    return a @ b.t().contiguous()
+
+
+# k of several scale groups, without cuts and with two and eight ranges; both tiles
+LONG = [(300, 600, 2080, 2), (257, 1000, 8190, 8), (520, 700, 1500, 1), (3500, 3601, 2100, 1), (1100, 1100, 4100, 3)]
+
+
+@pytest.mark.parametrize("fmt", [mx_ref.E4M3, mx_ref.E2M1])
+@pytest.mark.parametrize("m,n,k,cuts", LONG)
+def test_long_products_are_exact(ibp, fmt, m, n, k, cuts):
+    """Products below 90 in steps of 2^-5."""
+    rng = np.random.default_rng(m + n + k)
+    a, b = codes_of(rng, m, k, fmt), codes_of(rng, n, k, mx_ref.E2M1)
+    want = exact_product(mx_ref.unpack(*a, k, fmt), mx_ref.unpack(*b, k, mx_ref.E2M1), 2.0 ** -5).float()
+    assert ibp.ibp_mx_matmul_workspace_bytes(m, n, k, fmt) == (cuts * m * n * 4 if cuts > 1 else 0)
+    da, db = device(ibp, *a, k, fmt), device(ibp, *b, k, mx_ref.E2M1)
+    for t in DT:
+        print(f"product: m={m} n={n} k={k} format={fmt} {t}", flush=True)
+        y = torch.full((m, n), float("nan"), dtype=DT[t], device="cuda")
+        assert torch.equal(ibp.ibp_mx_matmul(da, db, dtype=DT[t], out=y), want.to(DT[t])), t
+
+
+@pytest.mark.parametrize("fmt", [mx_ref.E4M3, mx_ref.E2M1])
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("m,n,k", [(300, 600, 2080), (520, 700, 1500), (3500, 3601, 700)])
+def test_long_products_keep_nan_blocks_in_their_rows(ibp, fmt, t, m, n, k):
+    rng = np.random.default_rng(k)
+    a, b = codes_of(rng, m, k, fmt), codes_of(rng, n, k, mx_ref.E2M1)
+    want = exact_product(mx_ref.unpack(*a, k, fmt), mx_ref.unpack(*b, k, mx_ref.E2M1), 2.0 ** -5).to(DT[t])
+    last = mx_ref.blocks(k) - 1
+    a[1][2, last], a[1][m - 1, 17], b[1][n - 1, last - 1], b[1][130, 0] = 255, 255, 255, 255
+    y = ibp.ibp_mx_matmul(device(ibp, *a, k, fmt), device(ibp, *b, k, mx_ref.E2M1), dtype=DT[t])
+    bad = torch.zeros(m, n, dtype=torch.bool, device="cuda")
+    bad[[2, m - 1]] = True
+    bad[:, [130, n - 1]] = True
+    assert torch.equal(torch.isnan(y), bad) and torch.equal(y[~bad], want[~bad])
+
+
+# the large tile with 16, 5 and 8 ranges (of each part), and the small one with 7
+CUT_WGRADS = [("bf16", 9000, 1000, 1000, 16), ("bf16", 9000, 1001, 1000, 16), ("f32", 9000, 1001, 1000, 5),
+              ("f16", 9001, 1000, 1003, 8), ("bf16", 1700, 130, 260, 7)]
+
+
+@pytest.mark.parametrize("ty,t,n,k,cuts", CUT_WGRADS)
+def test_cut_wgrads_are_exact(ibp, ty, t, n, k, cuts):
+    """dy whole from -4 to 4, x below 7.5 in steps of 1/8."""
+    rng = np.random.default_rng(t + n + k)
+    dy = rng.integers(-4, 5, (t, n)).astype(float)
+    x = codes_of(rng, t, k, mx_ref.E4M3)
+    v = mx_ref.unpack(*x, k, mx_ref.E4M3)
+    want = exact_product(np.ascontiguousarray(dy.T), np.ascontiguousarray(v.T), 2.0 ** -3).float()
+    parts = {"bf16": 1, "f16": 2, "f32": 3}[ty]
+    sums = -(-cuts * parts * n * k * 4 // 16) * 16
+    copy = parts * t * -(-n // 8) * 16 if t >= 9000 and (parts > 1 or n % 8) else 0  # the large tile's
+    assert ibp.ibp_mx_linear_wgrad_workspace_bytes(t, n, k, DT[ty]) == sums + copy
+    x8 = device(ibp, *x, k, mx_ref.E4M3)
+    print(f"weight gradient: t={t} n={n} k={k} {ty}", flush=True)
+    for to in ("f32", "bf16"):
+        dw = torch.full((n, k), float("nan"), dtype=DT[to], device="cuda")
+        got = ibp.ibp_mx_linear_wgrad(torch.from_numpy(dy).to(DT[ty]).cuda(), x8, dw=dw)
+        assert torch.equal(got, want.to(DT[to])), to
+
+
+@pytest.mark.parametrize("ty", ["f32", "f16"])
+def test_cut_wgrads_add_their_parts(ibp, ty):
+    """dY whose bits fill all its parts: within the 32-bit sums' own bound."""
+    t, n, k = 9000, 1000, 1000
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    dy = (torch.randn(t, n, generator=gen, device="cuda") * 0.1).to(DT[ty])
+    x8 = ibp.ibp_mx_pack(torch.randn(t, k, generator=gen, device="cuda"), ibp.IBP_MX_E4M3)
+    v, d = ibp.ibp_mx_unpack(x8, torch.float32).double(), dy.double().t().contiguous()
+    want, mag = d @ v, d.abs() @ v.abs()
+    got = ibp.ibp_mx_linear_wgrad(dy, x8, dw_dtype=torch.float32).double()
+    assert ((got - want).abs() <= mag * t * 2.0 ** -24).all()
+    # and far closer than without the last part, whose share is 2^-8 (half precision) or 2^-16
+    assert (got - want).norm() < want.norm() * (2.0 ** -19 if ty == "f32" else 2.0 ** -12)
