@@ -306,3 +306,35 @@ def test_cut_wgrads_add_their_parts(ibp, ty):
     assert ((got - want).abs() <= mag * t * 2.0 ** -24).all()
     # and far closer than without the last part, whose share is 2^-8 (half precision) or 2^-16
     assert (got - want).norm() < want.norm() * (2.0 ** -19 if ty == "f32" else 2.0 ** -12)
+
+
+# ---------------------------------------------------------------- the training example
+
+def test_gradients_of_the_example_have_the_right_size():
+    """The factor that fits a gradient of the example best to the one that torch computes from
+    the same packed values is 1 up to 4%: rounding to e2m1 (a quarter at most, a tenth in the
+    mean square) and e4m3 adds errors that are as good as independent of the gradient, so it
+    moves the factor by its square, 1% for each of the two 4-bit packings of a weight."""
+    import os
+    import sys
+
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import bit_packing_amd as ibp
+    import packed_training
+
+    torch.manual_seed(3)
+    model = packed_training.Model(500, 192, 384, 9)
+    model.scale = 1.25
+    ids = torch.randint(500, (1000,), device="cuda")
+    y, kept = model.forward(ids)
+    dy = (torch.randn_like(y.float()) * 0.01).to(torch.bfloat16)
+    grads = model.backward(dy, kept)
+    wg, wu, wd = (ibp.ibp_mx_unpack(layer.w4, dtype=torch.float32).requires_grad_() for layer in (model.gate, model.up, model.down))
+    table = model.table.float().requires_grad_()
+    x = table[ids] * model.scale
+    h = torch.nn.functional.silu(x @ wg.t()) * (x @ wu.t())
+    (h @ wd.t()).backward(dy.float())
+    for name, want in (("down", wd.grad), ("gate", wg.grad), ("up", wu.grad), ("table", table.grad)):
+        factor = ((grads[name].double() * want.double()).sum() / want.double().square().sum()).item()
+        print(name, factor)
+        assert abs(factor - 1) < 0.04, (name, factor)
