@@ -178,7 +178,7 @@ __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, voi
   constexpr uint32_t kPitchA = A8 ? 128 : 64, kPitchB = 64, kBlocks = 4;
   using TileA = Tile<kRowsA, kPitchA, kWaves>;
   using TileB = Tile<kRowsB, kPitchB, kWaves>;
-  static_assert(kRowsA + kRowsB == 64 * kWaves, "a wavefront loads the scale dwords of 64 rows");
+  static_assert(kRowsA + kRowsB == 64 * kWaves, "a wavefront loads the scales of 64 rows");
   constexpr uint32_t kStage = TileA::kBytes + TileB::kBytes, kStages = A8 ? 3 : 4;
   constexpr uint32_t kLoads = TileA::kLoads + TileB::kLoads;  // a wavefront's loads per stage
   // Scales come for kGroup stages at a time, 16 bytes of each row of A, then of B: a dword

@@ -25,7 +25,7 @@ struct EmbedGradArgs {
   const int64_t *ids;
   void *grad;          // n_rows x dim
   uint32_t *err;       // optional
-  uint8_t *ws;         // embed_grad_layout(...).bytes bytes, aligned to 16
+  uint8_t *ws;         // embed_grad_workspace(...) bytes, aligned to 16
   uint64_t n_rows;
   uint64_t n_ids;      // < 2^31
   int64_t padding_id;  // this id takes no part; -1 for none

@@ -14,12 +14,9 @@ static __device__ __align__(32) const uint8_t kZeros[32] = {};
 typedef __attribute__((address_space(3))) void lds_void;
 typedef const __attribute__((address_space(1))) void global_void;
 
-// Lane l's 16 (or 4) bytes at `from` go to byte 16 l (4 l) of the wavefront's `to`.
+// Lane l's 16 bytes at `from` go to byte 16 l of the wavefront's `to`.
 __device__ __forceinline__ void to_lds16(const uint8_t *from, uint8_t *to) {
   __builtin_amdgcn_global_load_lds((global_void *)from, (lds_void *)to, 16, 0, 0);
-}
-__device__ __forceinline__ void to_lds4(const uint8_t *from, uint8_t *to) {
-  __builtin_amdgcn_global_load_lds((global_void *)from, (lds_void *)to, 4, 0, 0);
 }
 
 // Tile of a workgroup among rows x cols of them.  Workgroups go to the eight XCDs in
