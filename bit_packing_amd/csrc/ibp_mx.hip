@@ -4,12 +4,13 @@
 //
 // All four are one pass over the data, bound by HBM: 16384 x 8192 in bf16 is packed to e2m1
 // and read back in 137 us (5.0 TB/s; a copy of 1 GiB reaches 5.2), packed to e4m3 in 73; the
-// gated activation takes 204 us forward (5.4 TB/s) and 191 back (5.7).  A lane takes eight
+// gated activation takes 185 us forward (5.8 TB/s) and 183 back (5.9).  A lane takes eight
 // consecutive elements (16 bytes of a 16-bit type), so four lanes hold a block and share its
 // largest magnitude by two lane exchanges, and 16 lanes hold the four blocks whose scale
 // bytes make one dword.  A row is cut into strips of 8 times the smallest power of two of
 // lanes, from 16 to the workgroup, that covers it; a workgroup step is one strip of R * 256
-// / lanes rows, R of them per lane, loaded before any is worked on.
+// / lanes rows, R of them per lane (one or four, where it packs or reads back), loaded before
+// any is worked on.
 #include "ibp_device.h"
 #include "ibp_num.h"
 
@@ -65,8 +66,8 @@ template <bool E4M3> __device__ __forceinline__ uint2 load_codes(const uint8_t *
 // 1 / (1 + exp(-g)) of eight gates.  The 16-bit types take it from the hardware's exp2 and
 // reciprocal (1 unit of the last place each), the argument's rounding made good by a factor: 6
 // half units in all, far below the result's own rounding, for a third of the instructions
-// (forward of 16384 x 8192 in bf16 204 us against 245 with the library's exp and a true
-// quotient, which 32-bit results take).
+// (forward of 16384 x 8192 in bf16, four rows a lane, 204 us against 245 with the library's exp
+// and a true quotient, which 32-bit results take).
 //
 // Where a wavefront has a gate below -80, whose exp(-g) may overflow and whose reciprocal is
 // flushed to zero from -87.3 on, all its gates go by e = exp(-|g|), which fades out through the
@@ -170,7 +171,7 @@ template <int D, bool E4M3, uint32_t R> __global__ __launch_bounds__(kBlock) voi
 }
 
 // h = g * sigmoid(g) * u in 32 bits from the inputs as they came; g and u packed.
-template <int D, uint32_t R> __global__ __launch_bounds__(kBlock) void mx_swiglu_kernel(MxArgs a, Walk w) {
+template <int D> __global__ __launch_bounds__(kBlock) void mx_swiglu_kernel(MxArgs a, Walk w) {
   using T = typename Num<D>::T;
   const uint32_t nblk = (uint32_t)mx_blocks(a.cols);
   const uint64_t cp = mx_code_pitch(a.cols, true), sp = mx_scale_pitch(a.cols);
@@ -178,72 +179,53 @@ template <int D, uint32_t R> __global__ __launch_bounds__(kBlock) void mx_swiglu
   T *h = static_cast<T *>(a.out);
   by_width(a.cols, [&](auto wide) {
     for (uint32_t unit = blockIdx.x; unit < w.units; unit += gridDim.x) {
-      const Place<R> p(w, unit, a.rows);
-      Vec8<T> vg[R], vu[R];
+      const Place<1> p(w, unit, a.rows);
+      const uint64_t row = p.row[0];
+      const Vec8<T> vg = load8<wide.value, T>(gate + row * a.cols, p.c, a.cols);
+      const Vec8<T> vu = load8<wide.value, T>(up + row * a.cols, p.c, a.cols);
+      const F8 g = widen<wide.value, T>(vg, p.c, a.cols), u = widen<wide.value, T>(vu, p.c, a.cols);
+      encode_lane<true>(g, a.codes + row * cp, a.scales + row * sp, p.c, nblk, p.ok[0]);
+      encode_lane<true>(u, a.codes2 + row * cp, a.scales2 + row * sp, p.c, nblk, p.ok[0]);
+      F8 o = sigmoid8<D>(g);
 #pragma unroll
-      for (uint32_t k = 0; k < R; ++k) {
-        vg[k] = load8<wide.value, T>(gate + p.row[k] * a.cols, p.c, a.cols);
-        vu[k] = load8<wide.value, T>(up + p.row[k] * a.cols, p.c, a.cols);
-      }
-#pragma unroll
-      for (uint32_t k = 0; k < R; ++k) {
-        const F8 g = widen<wide.value, T>(vg[k], p.c, a.cols), u = widen<wide.value, T>(vu[k], p.c, a.cols);
-        encode_lane<true>(g, a.codes + p.row[k] * cp, a.scales + p.row[k] * sp, p.c, nblk, p.ok[k]);
-        encode_lane<true>(u, a.codes2 + p.row[k] * cp, a.scales2 + p.row[k] * sp, p.c, nblk, p.ok[k]);
-        F8 o = sigmoid8<D>(g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o.v[i] = g.v[i] * o.v[i] * u.v[i];
-        if (p.ok[k] && p.c < a.cols) store8<T>(h + p.row[k] * a.cols, p.c, a.cols, o);
-      }
+      for (int i = 0; i < 8; ++i) o.v[i] = g.v[i] * o.v[i] * u.v[i];
+      if (p.ok[0] && p.c < a.cols) store8<T>(h + row * a.cols, p.c, a.cols, o);
     }
   });
 }
 
 // With s = sigmoid(g): dgate = dh u s (1 + g (1 - s)), dup = dh g s, g and u read back
 // from the checkpoints.
-template <int D, uint32_t R> __global__ __launch_bounds__(kBlock) void mx_swiglu_backward_kernel(MxArgs a, Walk w) {
+template <int D> __global__ __launch_bounds__(kBlock) void mx_swiglu_backward_kernel(MxArgs a, Walk w) {
   using T = typename Num<D>::T;
   const uint64_t cp = mx_code_pitch(a.cols, true), sp = mx_scale_pitch(a.cols);
   const T *dh = static_cast<const T *>(a.in2);
   T *dgate = static_cast<T *>(a.out), *dup = static_cast<T *>(a.out2);
   by_width(a.cols, [&](auto wide) {
     for (uint32_t unit = blockIdx.x; unit < w.units; unit += gridDim.x) {
-      const Place<R> p(w, unit, a.rows);
-      if (p.c >= a.cols) continue;
-      uint2 qg[R], qu[R];
-      uint32_t sg[R], su[R];
-      Vec8<T> vd[R];
+      const Place<1> p(w, unit, a.rows);
+      if (p.c >= a.cols || !p.ok[0]) continue;
+      const uint64_t row = p.row[0];
+      const uint2 qg = load_codes<true>(a.codes + row * cp, p.c), qu = load_codes<true>(a.codes2 + row * cp, p.c);
+      const uint32_t sg = a.scales[row * sp + p.c / kMxBlock], su = a.scales2[row * sp + p.c / kMxBlock];
+      const Vec8<T> vd = load8<wide.value, T>(dh + row * a.cols, p.c, a.cols);
+      const F8 g = mx_decode<true>(qg, sg), u = mx_decode<true>(qu, su), d = widen<wide.value, T>(vd, p.c, a.cols);
+      const F8 s = sigmoid8<D>(g);
+      F8 og, ou;
 #pragma unroll
-      for (uint32_t k = 0; k < R; ++k) {
-        qg[k] = load_codes<true>(a.codes + p.row[k] * cp, p.c);
-        qu[k] = load_codes<true>(a.codes2 + p.row[k] * cp, p.c);
-        sg[k] = a.scales[p.row[k] * sp + p.c / kMxBlock];
-        su[k] = a.scales2[p.row[k] * sp + p.c / kMxBlock];
-        vd[k] = load8<wide.value, T>(dh + p.row[k] * a.cols, p.c, a.cols);
+      for (int i = 0; i < 8; ++i) {
+        const float ds = d.v[i] * s.v[i];
+        og.v[i] = ds * u.v[i] * (1.0f + g.v[i] * (1.0f - s.v[i]));
+        ou.v[i] = ds * g.v[i];
       }
-#pragma unroll
-      for (uint32_t k = 0; k < R; ++k) {
-        if (!p.ok[k]) continue;
-        const F8 g = mx_decode<true>(qg[k], sg[k]), u = mx_decode<true>(qu[k], su[k]), d = widen<wide.value, T>(vd[k], p.c, a.cols);
-        const F8 s = sigmoid8<D>(g);
-        F8 og, ou;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float ds = d.v[i] * s.v[i];
-          og.v[i] = ds * u.v[i] * (1.0f + g.v[i] * (1.0f - s.v[i]));
-          ou.v[i] = ds * g.v[i];
-        }
-        store8<T>(dgate + p.row[k] * a.cols, p.c, a.cols, og);
-        store8<T>(dup + p.row[k] * a.cols, p.c, a.cols, ou);
-      }
+      store8<T>(dgate + row * a.cols, p.c, a.cols, og);
+      store8<T>(dup + row * a.cols, p.c, a.cols, ou);
     }
   });
 }
 
 constexpr uint32_t kMaxGrid = 1u << 22;
 
-// Rows per lane: four where that leaves the GPU full (1024 workgroups), else one, so
-// that small calls spread over the CUs.
 bool walk_of(const MxArgs &a, uint32_t each, Walk *w) {
   const uint32_t need = (a.cols + 7) / 8;  // lanes that a row has work for
   w->lanes = 16;
@@ -256,16 +238,24 @@ bool walk_of(const MxArgs &a, uint32_t each, Walk *w) {
   return true;
 }
 
-template <typename F> hipError_t with_walk(const MxArgs &a, F &&f) {
+uint32_t grid_of(const Walk &w) { return w.units < kMaxGrid ? w.units : kMaxGrid; }
+
+// Packing and reading back.  Rows per lane: four of a 16-bit type where that leaves the GPU
+// full, so that small calls spread over the CUs; bf16 of 4096 columns, four rows against one:
+// 512 units of four rows pack in 3.8 and 3.8 us, 256 in 3.4 and 3.0, 1024 in 4.9 and 5.4, 2048 in
+// 7.8 and 9.2; 16384 x 8192 is packed to e2m1 in 61 and 65 and read back in 59 and 72.  One of
+// fp32, whose rows are twice the registers (113 and 105, 150 and 119).
+template <int D, typename F> hipError_t with_walk(const MxArgs &a, F &&f) {
   Walk w;
-  if (!walk_of(a, 4, &w)) return hipErrorInvalidValue;
-  auto grid = [&] { return w.units < kMaxGrid ? w.units : kMaxGrid; };
-  if (w.units >= 1024) {
-    f(std::integral_constant<uint32_t, 4>{}, w, grid());
-  } else {
-    if (!walk_of(a, 1, &w)) return hipErrorInvalidValue;
-    f(std::integral_constant<uint32_t, 1>{}, w, grid());
+  if constexpr (D != IBP_F32) {
+    if (!walk_of(a, 4, &w)) return hipErrorInvalidValue;
+    if (w.units >= 1024) {
+      f(std::integral_constant<uint32_t, 4>{}, w, grid_of(w));
+      return hipGetLastError();
+    }
   }
+  if (!walk_of(a, 1, &w)) return hipErrorInvalidValue;
+  f(std::integral_constant<uint32_t, 1>{}, w, grid_of(w));
   return hipGetLastError();
 }
 
@@ -273,7 +263,7 @@ template <typename F> hipError_t with_walk(const MxArgs &a, F &&f) {
 
 hipError_t launch_mx_pack(const MxArgs &a, hipStream_t s) {
   return with_dtype(a.dtype, [&](auto d) {
-    return with_walk(a, [&](auto r, const Walk &w, uint32_t grid) {
+    return with_walk<d.value>(a, [&](auto r, const Walk &w, uint32_t grid) {
       if (a.e4m3) mx_pack_kernel<d.value, true, r.value><<<grid, kBlock, 0, s>>>(a, w);
       else mx_pack_kernel<d.value, false, r.value><<<grid, kBlock, 0, s>>>(a, w);
     });
@@ -282,26 +272,31 @@ hipError_t launch_mx_pack(const MxArgs &a, hipStream_t s) {
 
 hipError_t launch_mx_unpack(const MxArgs &a, hipStream_t s) {
   return with_dtype(a.dtype, [&](auto d) {
-    return with_walk(a, [&](auto r, const Walk &w, uint32_t grid) {
+    return with_walk<d.value>(a, [&](auto r, const Walk &w, uint32_t grid) {
       if (a.e4m3) mx_unpack_kernel<d.value, true, r.value><<<grid, kBlock, 0, s>>>(a, w);
       else mx_unpack_kernel<d.value, false, r.value><<<grid, kBlock, 0, s>>>(a, w);
     });
   });
 }
 
+// The gated activation has more to do an element, and takes a row a lane (16384 x 8192 in
+// bf16: 185 us forward against 191 with four rows, 183 backward against 194; 4000 x 4097 25
+// against 28, 24 against 26; 8000 x 2048 22.0 against 24.4, 22.4 against 22.1).
 hipError_t launch_mx_swiglu(const MxArgs &a, hipStream_t s) {
+  Walk w;
+  if (!walk_of(a, 1, &w)) return hipErrorInvalidValue;
   return with_dtype(a.dtype, [&](auto d) {
-    return with_walk(a, [&](auto r, const Walk &w, uint32_t grid) {
-      mx_swiglu_kernel<d.value, r.value><<<grid, kBlock, 0, s>>>(a, w);
-    });
+    mx_swiglu_kernel<d.value><<<grid_of(w), kBlock, 0, s>>>(a, w);
+    return hipGetLastError();
   });
 }
 
 hipError_t launch_mx_swiglu_backward(const MxArgs &a, hipStream_t s) {
+  Walk w;
+  if (!walk_of(a, 1, &w)) return hipErrorInvalidValue;
   return with_dtype(a.dtype, [&](auto d) {
-    return with_walk(a, [&](auto r, const Walk &w, uint32_t grid) {
-      mx_swiglu_backward_kernel<d.value, r.value><<<grid, kBlock, 0, s>>>(a, w);
-    });
+    mx_swiglu_backward_kernel<d.value><<<grid_of(w), kBlock, 0, s>>>(a, w);
+    return hipGetLastError();
   });
 }
 
