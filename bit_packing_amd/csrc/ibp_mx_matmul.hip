@@ -115,7 +115,10 @@ template <bool A8, int DO> __global__ void mx_direct_kernel(MxMatmulArgs a) {
 template <bool A8> hipError_t go_direct(const MxMatmulArgs &a, hipStream_t s) {
   const uint64_t gx = (a.N + 15) / 16, gy = (a.M + 15) / 16;
   const uint32_t steps = (uint32_t)((mx_blocks(a.K) + kStep - 1) / kStep);
-  uint32_t waves = gx * gy < 512 ? 16 : 4;
+  // Up to one workgroup a CU sixteen wavefronts, which share a long k; beyond, four (8192 deep,
+  // one row of e4m3: 4096 outputs 6.6 us against 8.1, 4624 outputs 10.9 against 9.5, 8176 11.2
+  // against 9.7; of e2m1 5.8 against 6.4, 8.7 against 8.2, 8.8 against 8.3).
+  uint32_t waves = gx * gy <= 256 ? 16 : 4;
   while (waves > 1 && waves > steps) waves /= 2;
   return with_dtype(a.dtype, [&](auto d) {
     mx_direct_kernel<A8, d.value><<<dim3((uint32_t)gx, (uint32_t)gy), waves * kWave, (waves - 1) * 1024, s>>>(a);
@@ -387,7 +390,9 @@ Plan plan_of(uint64_t M, uint64_t N, uint32_t K) {
   const uint32_t stages = (uint32_t)((mx_blocks(K) + 3) / 4);
   // One workgroup takes half a microsecond a stage however few there are: k is cut into
   // ranges of whole scale groups (4 stages), at least 8 stages each, until there is one per
-  // CU (128 x 8192 outputs, 8192 deep: e2m1 31 us in one range, 19.3 in four; e4m3 73, 29.7).
+  // CU (128 x 8192 outputs, 8192 deep: e2m1 31 us in one range, 19.3 in four; e4m3 73, 29.7),
+  // eight at most, for as much workspace each as 32-bit results take (384 x 384 outputs, 8192
+  // deep, e2m1: 13.4 in eight, 16.4 in sixteen; 256 x 1024, 65536 deep: 38, 29).
   const uint64_t want = big ? 1 : 256 / tiles, most = stages / 8;
   uint32_t n = (uint32_t)(want < most ? want : most);
   n = n < 1 ? 1 : (n > 8 ? 8 : n);
