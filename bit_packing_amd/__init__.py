@@ -24,6 +24,9 @@ have the names of the C entry points:
   activation checkpoints and the backward pass from them;
 * ``ibp_mx_matmul`` -- product of packed activations with packed 4-bit weights.
 
+The operators take part in no autograd graph: a tensor that requires a gradient gets none
+from them, and the backward ones are called by name.
+
 There is no fallback: if ``libibp.so`` is missing or no GPU is present the calls
 raise.
 """

@@ -32,7 +32,7 @@ constexpr uint32_t kStep = 16;  // blocks per step of the direct kernel: 512 ele
 // more, whose codes have bit 6, go through one instruction (2^10 down to 2^-3) and the rest
 // through another (4 down to 2^-10): nothing is dropped.  In one instruction a block whose
 // large products cancel, as those of an outlier column may, would lose its result: 8192 x
-// 8192 x 8192 would take 370 us so, against 757 (614 without the work of splitting).
+// 8192 x 8192 would take 370 us so, against 742 (614 without the work of splitting).
 template <bool A8> __device__ __forceinline__ v4f mfma_mx(v8i w, v8i x, v4f acc, int ws, int xs) {
   if constexpr (A8) {
     v8i high;
@@ -70,8 +70,9 @@ __device__ __forceinline__ uint4 scales16(const uint8_t *row, uint32_t b, uint32
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// Few rows of A: bound by the weights' bytes (1 x 8192 outputs, 8192 deep: 8.3 us from e2m1,
-// 4.3 TB/s of weights, 10.2 from e4m3, 3.5 TB/s).  A workgroup computes 16 x 16 outputs, its wavefronts take the steps of k in
+// Few rows of A: bound by the latency of a step's loads, of which the next step's are not in
+// flight (1 x 8192 outputs, 8192 deep: 8.3 us from e2m1, 4.3 TB/s of weights, 10.2 from e4m3, 3.5
+// TB/s; half of the wavefronts' time is waiting).  A workgroup computes 16 x 16 outputs, its wavefronts take the steps of k in
 // turn and their sums are added in order through LDS.  A step is 16 blocks, four matrix
 // instructions; each load takes 64 consecutive bytes of 16 rows.
 template <bool A8, int DO> __global__ void mx_direct_kernel(MxMatmulArgs a) {
@@ -133,7 +134,7 @@ template <bool A8> hipError_t go_direct(const MxMatmulArgs &a, hipStream_t s) {
 // Operands go through LDS by the direct global-to-LDS loads, in stages of 128 elements
 // of every row, one matrix instruction deep, in a ring of kStages: while one is
 // multiplied the loads of the next ones are in flight.  8192 x 8192 x 8192 in e2m1 takes
-// 279 us, 3.9 PFLOP/s (310 us with two stages of 256 elements and all wavefronts in step);
+// 272 us, 4.0 PFLOP/s (310 us with two stages of 256 elements and all wavefronts in step);
 // with the loads left out 80% of that, with the matrix instructions left out as long: it
 // is bound by a turn's two phases, reading LDS and issuing loads in one, multiplying in
 // the other, and by power: the clock falls to 2.0 GHz.  The 32 x 32 x 64 matrix instruction

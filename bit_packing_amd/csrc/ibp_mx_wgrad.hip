@@ -95,7 +95,7 @@ template <typename T> __device__ __forceinline__ T from_global(const uint8_t *p)
 // has laid them out so; part p is then T rows further on), else through registers like
 // X, which is loaded four stages ahead and decoded into LDS two stages ahead.  As in the
 // 4-bit product, half of the eight wavefronts of a large tile read a stage while the other
-// half multiplies (16384 x 4096 x 8192: 890 us, 1.23 PFLOP/s, against 1090 with all in
+// half multiplies (16384 x 4096 x 8192: 859 us, 1.28 PFLOP/s, against 1090 with all in
 // step and two stages of 64 tokens).  Bound by the phases (the matrix units are busy 57% of the
 // time, LDS 28%) and by power: the clock falls to 1.9 to 2.1 GHz.
 //
