@@ -22,7 +22,12 @@ have the names of the C entry points:
   power-of-two scale per 32);
 * ``ibp_mx_swiglu`` / ``ibp_mx_swiglu_backward`` / ``ibp_mx_linear_wgrad`` -- 8-bit
   activation checkpoints and the backward pass from them;
-* ``ibp_mx_matmul`` -- product of packed activations with packed 4-bit weights.
+* ``ibp_mx_matmul`` -- product of packed activations with packed 4-bit weights;
+* ``ibp_i8_pack`` / ``ibp_i8_unpack`` / ``ibp_i8_matmul`` -- 8-bit integer rows with a scale
+  each, and their product;
+* ``ibp_expert_order`` / ``ibp_mx_grouped_matmul`` / ``ibp_mx_grouped_wgrad`` -- a layer of
+  experts: tokens sorted by expert, the product of packed rows with their expert's 4-bit
+  weights, and those weights' gradients.
 
 The operators take part in no autograd graph: a tensor that requires a gradient gets none
 from them, and the backward ones are called by name.
@@ -52,6 +57,8 @@ IBP_NOALLOC_SCRATCH_BYTES = 8 << 20  # device array behind ibp_compress_noalloc,
 IBP_F32, IBP_F16, IBP_BF16 = 0, 1, 2
 IBP_MAX_COLS, IBP_MAX_TOKENS = 1 << 30, 1 << 31
 IBP_MX_E4M3, IBP_MX_E2M1 = 0, 1
+IBP_I8_MAX_DEPTH = 131071  # products of 8-bit codes that a 32-bit sum holds
+IBP_MAX_EXPERTS = 1024
 
 EXPORTS = (
     "ibp_status_str", "ibp_num_segments", "ibp_max_stream_bytes", "ibp_stream_bytes",
@@ -66,6 +73,9 @@ EXPORTS = (
     "ibp_mx_codes_pitch", "ibp_mx_scales_pitch", "ibp_mx_pack", "ibp_mx_unpack", "ibp_mx_swiglu",
     "ibp_mx_swiglu_backward", "ibp_mx_matmul", "ibp_mx_matmul_workspace_bytes", "ibp_mx_linear_wgrad",
     "ibp_mx_linear_wgrad_workspace_bytes",
+    "ibp_i8_codes_pitch", "ibp_i8_pack", "ibp_i8_unpack", "ibp_i8_matmul", "ibp_i8_matmul_workspace_bytes",
+    "ibp_expert_order", "ibp_expert_order_workspace_bytes", "ibp_mx_grouped_matmul",
+    "ibp_mx_grouped_matmul_workspace_bytes", "ibp_mx_grouped_wgrad", "ibp_mx_grouped_wgrad_workspace_bytes",
 )
 
 
@@ -89,6 +99,12 @@ class ibp_mx_t(ctypes.Structure):
     """A packed microscaled tensor: element format, shape, device pointers."""
     _fields_ = [("format", ctypes.c_uint32), ("reserved", ctypes.c_uint32), ("rows", ctypes.c_uint64),
                 ("cols", ctypes.c_uint64), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class ibp_i8_t(ctypes.Structure):
+    """A tensor of 8-bit integer rows: shape, device pointers."""
+    _fields_ = [("rows", ctypes.c_uint64), ("cols", ctypes.c_uint64), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p)]
 
 
 class MxTensor:
@@ -134,6 +150,35 @@ class MxTensor:
         if _nbytes(self._codes) < rows * codes or _nbytes(self._scales) < rows * scales:
             raise ValueError("codes or scales are smaller than their shape needs")
         return ibp_mx_t(self.format, 0, rows, cols, _ptr(self._codes), _ptr(self._scales))
+
+
+class I8Tensor:
+    """A tensor of rows x cols elements in 8-bit integers: int8 codes [rows,
+    ibp_i8_codes_pitch] and float32 scales [rows] on the device."""
+    __slots__ = ("rows", "cols", "codes", "scales")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int):
+        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
+
+    def __repr__(self):
+        return f"I8Tensor({self.rows} x {self.cols})"
+
+    @property
+    def device(self) -> torch.device:
+        return _device(self.codes)
+
+    def struct(self) -> ibp_i8_t:
+        # the C side sees pointers only: the tensors must hold what the shape says
+        if self.codes.dtype != torch.int8 or self.scales.dtype != torch.float32:
+            raise ValueError("codes are int8, scales float32")
+        if self.codes.numel() < self.rows * _i8_pitch(self.cols) or self.scales.numel() < self.rows:
+            raise ValueError("codes or scales are smaller than their shape needs")
+        return ibp_i8_t(self.rows, self.cols, _ptr(self.codes), _ptr(self.scales))
+
+
+def _i8_pitch(cols: int) -> int:
+    """Bytes from one row of 8-bit codes to the next."""
+    return (cols + 15) // 16 * 16
 
 
 def _mx_pitches(cols: int, format: int) -> tuple[int, int]:
@@ -229,10 +274,25 @@ def load_library() -> ctypes.CDLL:
         lib.ibp_mx_matmul_workspace_bytes.argtypes = [_u64, _u64, _u64, _u32]
         lib.ibp_mx_linear_wgrad.argtypes = [_vp, _int, _u64, _mxp, _vp, _int, _vp, _u64, _vp]
         lib.ibp_mx_linear_wgrad_workspace_bytes.argtypes = [_u64, _u64, _u64, _int]
-        for f in ("ibp_embedding_grad_workspace_bytes", "ibp_mx_codes_pitch", "ibp_mx_scales_pitch",
+        _i8p = ctypes.POINTER(ibp_i8_t)
+        lib.ibp_i8_codes_pitch.argtypes = [_u64]
+        lib.ibp_i8_pack.argtypes = [_vp, _int, _i8p, _vp]
+        lib.ibp_i8_unpack.argtypes = [_i8p, _vp, _int, _vp]
+        lib.ibp_i8_matmul.argtypes = [_i8p, _i8p, _vp, _int, _vp, _u64, _vp]
+        lib.ibp_i8_matmul_workspace_bytes.argtypes = [_u64, _u64, _u64]
+        lib.ibp_expert_order.argtypes = [_vp, _u64, _u64, _vp, _vp, _vp, _u64, _vp, _vp]
+        lib.ibp_expert_order_workspace_bytes.argtypes = [_u64, _u64]
+        lib.ibp_mx_grouped_matmul.argtypes = [_mxp, _mxp, _vp, _u64, _vp, _int, _vp, _u64, _vp, _vp]
+        lib.ibp_mx_grouped_matmul_workspace_bytes.argtypes = [_u64, _u64, _u64, _u64, _u32]
+        lib.ibp_mx_grouped_wgrad.argtypes = [_vp, _int, _u64, _mxp, _vp, _u64, _vp, _int, _vp, _u64, _vp, _vp]
+        lib.ibp_mx_grouped_wgrad_workspace_bytes.argtypes = [_u64, _u64, _u64, _u64, _int]
+        for f in ("ibp_i8_codes_pitch", "ibp_i8_matmul_workspace_bytes", "ibp_expert_order_workspace_bytes",
+                  "ibp_mx_grouped_matmul_workspace_bytes", "ibp_mx_grouped_wgrad_workspace_bytes",
+                  "ibp_embedding_grad_workspace_bytes", "ibp_mx_codes_pitch", "ibp_mx_scales_pitch",
                   "ibp_mx_matmul_workspace_bytes", "ibp_mx_linear_wgrad_workspace_bytes"):
             getattr(lib, f).restype = _u64
-        for f in ("ibp_embedding_lookup", "ibp_embedding_grad", "ibp_mx_pack", "ibp_mx_unpack", "ibp_mx_swiglu",
+        for f in ("ibp_i8_pack", "ibp_i8_unpack", "ibp_i8_matmul", "ibp_expert_order", "ibp_mx_grouped_matmul",
+                  "ibp_mx_grouped_wgrad", "ibp_embedding_lookup", "ibp_embedding_grad", "ibp_mx_pack", "ibp_mx_unpack", "ibp_mx_swiglu",
                   "ibp_mx_swiglu_backward", "ibp_mx_matmul", "ibp_mx_linear_wgrad",
                   "ibp_build_metadata", "ibp_compress", "ibp_decompress", "ibp_decompress_gather",
                   "ibp_gather_raw", "ibp_compress_slots", "ibp_decompress_gather_slots",
@@ -783,4 +843,169 @@ def ibp_mx_linear_wgrad(dy: torch.Tensor, x8: MxTensor, dw_dtype=None, dw: torch
                                  _dtype(dw.dtype), _ptr(workspace), 0 if workspace is None else _nbytes(workspace),
                                  _stream(None))
     _check(rc, "ibp_mx_linear_wgrad")
+    return dw
+
+
+# ------------------------------------------------------------------ 8-bit integer rows and experts
+
+
+def _here(*tensors) -> torch.device:
+    """The device of the tensors that are on one, which has to be the current one: a call
+    runs on the current device's stream."""
+    dev = None
+    for t in tensors:
+        if t is not None and t.is_cuda:
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError("the tensors are on different devices")
+    if dev is None:
+        return _device()
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, not on the current device")
+    return dev
+
+
+def _mx_tensors(m: MxTensor):
+    return (m._both,) if m._both is not None else (m._codes, m._scales)
+
+
+def ibp_i8_codes_pitch(cols: int) -> int:
+    return int(load_library().ibp_i8_codes_pitch(cols))
+
+
+def ibp_i8_matmul_workspace_bytes(m: int, n: int, k: int) -> int:
+    return int(load_library().ibp_i8_matmul_workspace_bytes(m, n, k))
+
+
+def ibp_expert_order_workspace_bytes(n_ids: int, n_experts: int) -> int:
+    return int(load_library().ibp_expert_order_workspace_bytes(n_ids, n_experts))
+
+
+def ibp_mx_grouped_matmul_workspace_bytes(m: int, n_experts: int, n: int, k: int, a_format: int) -> int:
+    return int(load_library().ibp_mx_grouped_matmul_workspace_bytes(m, n_experts, n, k, a_format))
+
+
+def ibp_mx_grouped_wgrad_workspace_bytes(tokens: int, n_experts: int, outs: int, ins: int, dy_dtype=torch.bfloat16) -> int:
+    return int(load_library().ibp_mx_grouped_wgrad_workspace_bytes(tokens, n_experts, outs, ins, _dtype(dy_dtype)))
+
+
+def make_i8(rows: int, cols: int, device) -> I8Tensor:
+    """An I8Tensor of unwritten codes and scales."""
+    return I8Tensor(torch.empty(rows, _i8_pitch(cols), dtype=torch.int8, device=device),
+                    torch.empty(rows, dtype=torch.float32, device=device), rows, cols)
+
+
+def ibp_i8_pack(x: torch.Tensor, out: I8Tensor | None = None, stream=None) -> I8Tensor:
+    """The rows (last dimension) of x in 8-bit integers, with a scale each."""
+    if stream is not None:
+        with _stream_context(stream):
+            return ibp_i8_pack(x, out)
+    rows, cols = _matrix(x)
+    dtype = _dtype(x.dtype)
+    if out is None:
+        out = make_i8(rows, cols, _here(x))
+    elif (out.rows, out.cols) != (rows, cols):
+        raise ValueError("the packed output has another shape")
+    else:
+        _here(x, out.codes, out.scales)
+    _check(load_library().ibp_i8_pack(_ptr(x), dtype, ctypes.byref(out.struct()), _stream(None)), "ibp_i8_pack")
+    return out
+
+
+def ibp_i8_unpack(t: I8Tensor, dtype=torch.bfloat16, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The values [rows, cols] of 8-bit integer rows."""
+    if stream is not None:
+        with _stream_context(stream):
+            return ibp_i8_unpack(t, dtype, out)
+    out = _out(out, (t.rows, t.cols), dtype, _here(t.codes, t.scales, out))
+    _check(load_library().ibp_i8_unpack(ctypes.byref(t.struct()), _ptr(out), _dtype(out.dtype), _stream(None)),
+           "ibp_i8_unpack")
+    return out
+
+
+def ibp_i8_matmul(a: I8Tensor, b: I8Tensor, dtype=torch.bfloat16, out: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """[a.rows, b.rows] product of 8-bit integer rows along their columns, each output times
+    its row's scale of a and of b; at most IBP_I8_MAX_DEPTH columns."""
+    if stream is not None:
+        with _stream_context(stream):
+            return ibp_i8_matmul(a, b, dtype, out, workspace)
+    lib, dev = load_library(), _here(a.codes, a.scales, b.codes, b.scales, out, workspace)
+    out = _out(out, (a.rows, b.rows), dtype, dev)
+    workspace = _workspace(workspace, int(lib.ibp_i8_matmul_workspace_bytes(a.rows, b.rows, a.cols)), dev)
+    rc = lib.ibp_i8_matmul(ctypes.byref(a.struct()), ctypes.byref(b.struct()), _ptr(out), _dtype(out.dtype),
+                           _ptr(workspace), 0 if workspace is None else _nbytes(workspace), _stream(None))
+    _check(rc, "ibp_i8_matmul")
+    return out
+
+
+def ibp_expert_order(ids: torch.Tensor, n_experts: int, order: torch.Tensor | None = None,
+                     offsets: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                     err: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """(order, offsets): the positions of ids (any shape, read flat) sorted by expert, equal
+    ones in their order, and the n_experts + 1 places where the experts' positions begin.
+    Ids out of range come behind the last expert's and set IBP_DEVERR_BAD_ID."""
+    if stream is not None:
+        with _stream_context(stream):
+            return ibp_expert_order(ids, n_experts, order, offsets, workspace, err)
+    lib, dev, n = load_library(), _here(_ids(ids), order, offsets, workspace, err), ids.numel()
+    order = _out(order, (n,), torch.int64, dev)
+    offsets = _out(offsets, (n_experts + 1,), torch.int64, dev)
+    workspace = _workspace(workspace, int(lib.ibp_expert_order_workspace_bytes(n, n_experts)), dev)
+    rc = lib.ibp_expert_order(_ptr(ids), n, n_experts, _ptr(order), _ptr(offsets), _ptr(workspace),
+                              0 if workspace is None else _nbytes(workspace), _ptr(err), _stream(None))
+    _check(rc, "ibp_expert_order")
+    return order, offsets
+
+
+def _experts(offsets: torch.Tensor) -> int:
+    if offsets.dtype != torch.int64 or offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets are int64 [experts + 1]")
+    return offsets.numel() - 1
+
+
+def ibp_mx_grouped_matmul(a: MxTensor, b: MxTensor, offsets: torch.Tensor, dtype=torch.bfloat16,
+                          out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                          err: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """[a.rows, b.rows / experts] product of packed rows, sorted by expert, with their expert's
+    packed 4-bit weights: rows offsets[e] to offsets[e + 1] of a take the e-th part of b's
+    rows.  Rows that belong to no expert are left as they were."""
+    if stream is not None:
+        with _stream_context(stream):
+            return ibp_mx_grouped_matmul(a, b, offsets, dtype, out, workspace, err)
+    n = _experts(offsets)
+    if b.rows % n:
+        raise ValueError("b's rows are not a multiple of the experts")
+    lib, dev = load_library(), _here(*_mx_tensors(a), *_mx_tensors(b), offsets, out, workspace, err)
+    out = _out(out, (a.rows, b.rows // n), dtype, dev)
+    workspace = _workspace(workspace, int(lib.ibp_mx_grouped_matmul_workspace_bytes(a.rows, n, b.rows // n, a.cols,
+                                                                                    a.format)), dev)
+    rc = lib.ibp_mx_grouped_matmul(ctypes.byref(a.struct()), ctypes.byref(b.struct()), _ptr(offsets), n, _ptr(out),
+                                   _dtype(out.dtype), _ptr(workspace), 0 if workspace is None else _nbytes(workspace),
+                                   _ptr(err), _stream(None))
+    _check(rc, "ibp_mx_grouped_matmul")
+    return out
+
+
+def ibp_mx_grouped_wgrad(dy: torch.Tensor, x8: MxTensor, offsets: torch.Tensor, dw_dtype=None,
+                         dw: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                         err: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """[experts, outs, x8.cols] weight gradients: for each expert the sum over its rows,
+    offsets[e] to offsets[e + 1], of dy's row times x8's row; zeros for an expert without
+    rows.  dy [x8.rows, outs], x8 in e4m3.  dw is of dw_dtype, dy's by default."""
+    if stream is not None:
+        with _stream_context(stream):
+            return ibp_mx_grouped_wgrad(dy, x8, offsets, dw_dtype, dw, workspace, err)
+    if dy.dim() != 2 or dy.shape[0] != x8.rows:
+        raise ValueError("dy is [x8.rows, outs]")
+    n, outs = _experts(offsets), dy.shape[1]
+    lib, dev = load_library(), _here(dy, *_mx_tensors(x8), offsets, dw, workspace, err)
+    dw = _out(dw, (n, outs, x8.cols), dw_dtype or (dy.dtype if dw is None else dw.dtype), dev)
+    need = int(lib.ibp_mx_grouped_wgrad_workspace_bytes(x8.rows, n, outs, x8.cols, _dtype(dy.dtype)))
+    workspace = _workspace(workspace, need, dev)
+    rc = lib.ibp_mx_grouped_wgrad(_ptr(dy), _dtype(dy.dtype), outs, ctypes.byref(x8.struct()), _ptr(offsets), n,
+                                  _ptr(dw), _dtype(dw.dtype), _ptr(workspace),
+                                  0 if workspace is None else _nbytes(workspace), _ptr(err), _stream(None))
+    _check(rc, "ibp_mx_grouped_wgrad")
     return dw

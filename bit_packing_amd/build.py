@@ -9,7 +9,7 @@ import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCES = [os.path.join(HERE, "csrc", f) for f in ("ibp_meta.hip", "ibp_encode.hip", "ibp_decode.hip", "ibp_decode_pos.hip", "ibp_slots.hip", "ibp_zip.hip", "ibp_embed.hip", "ibp_mx.hip", "ibp_mx_matmul.hip", "ibp_mx_wgrad.hip", "ibp_api.hip")]
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("ibp_meta.hip", "ibp_encode.hip", "ibp_decode.hip", "ibp_decode_pos.hip", "ibp_slots.hip", "ibp_zip.hip", "ibp_embed.hip", "ibp_mx.hip", "ibp_mx_matmul.hip", "ibp_mx_wgrad.hip", "ibp_i8.hip", "ibp_i8_matmul.hip", "ibp_expert.hip", "ibp_api.hip")]
 LIB = os.path.join(HERE, "libibp.so")
 LIB_SANITIZED = os.path.join(HERE, "libibp_san.so")
 # host code only: each -fsanitize= after -Xarch_host, so no GPU code is instrumented

@@ -882,7 +882,7 @@ static int gated_check(const void *x, const void *y, const void *z, int dtype, c
 struct Range { const void *p; uint64_t bytes; };
 
 static bool overlap(const Range &x, const Range &y) {
-  return (uintptr_t)x.p < (uintptr_t)y.p + y.bytes && (uintptr_t)y.p < (uintptr_t)x.p + x.bytes;
+  return x.bytes && y.bytes && (uintptr_t)x.p < (uintptr_t)y.p + y.bytes && (uintptr_t)y.p < (uintptr_t)x.p + x.bytes;
 }
 
 // Whether outputs lie apart from each other and from the inputs.  The first plain_outs and
@@ -988,6 +988,9 @@ IBP_API int ibp_mx_matmul(const ibp_mx_t *a, const ibp_mx_t *b, void *d_y, int d
   p.K = (uint32_t)a->cols;
   p.a_e4m3 = a->format == IBP_MX_E4M3;
   p.dtype = dtype;
+  p.offsets = nullptr;
+  p.experts = 0;
+  p.err = nullptr;
   return status_of(launch_mx_matmul(p, static_cast<hipStream_t>(hip_stream)));
 }
 
@@ -1020,7 +1023,239 @@ IBP_API int ibp_mx_linear_wgrad(const void *d_dy, int dy_dtype, uint64_t outs, c
   p.K = (uint32_t)x8->cols;
   p.dy_dtype = dy_dtype;
   p.dtype = dw_dtype;
+  p.offsets = nullptr;
+  p.experts = 0;
+  p.err = nullptr;
   return status_of(launch_mx_wgrad(p, static_cast<hipStream_t>(hip_stream)));
+}
+
+// ------------------------------------------------------------------ 8-bit integer rows
+
+IBP_API uint64_t ibp_i8_codes_pitch(uint64_t cols) { return cols > IBP_MAX_COLS ? 0 : i8_pitch(cols); }
+
+// Field checks of a tensor of 8-bit integer rows, before any HIP call.
+static int i8_check(const ibp_i8_t *t) {
+  if (!t) return IBP_ERR_INVALID_ARG;
+  uint64_t b;
+  if (t->cols > IBP_MAX_COLS || !matrix_bytes(t->rows, i8_pitch(t->cols), 1, &b) || !mul_ok(t->rows, 4, &b)) return IBP_ERR_SIZE;
+  if (!aligned(t->codes, 16) || !aligned(t->scales, 4)) return IBP_ERR_INVALID_ARG;
+  if (t->rows && (!t->scales || (t->cols && !t->codes))) return IBP_ERR_INVALID_ARG;
+  return IBP_OK;
+}
+
+static Range codes_range(const ibp_i8_t *t) { return {t->codes, t->rows * i8_pitch(t->cols)}; }
+static Range scales_range(const ibp_i8_t *t) { return {t->scales, t->rows * 4}; }
+
+static bool i8_view(const ibp_i8_t *t, int8_t **codes, float **scales) {
+  *codes = t->codes;
+  *scales = t->scales;
+  return view(*codes, codes_range(t).bytes) && view(*scales, scales_range(t).bytes);
+}
+
+IBP_API int ibp_i8_pack(const void *d_in, int dtype, const ibp_i8_t *out, void *hip_stream) {
+  if (!dtype_ok(dtype)) return IBP_ERR_INVALID_ARG;
+  if (const int rc = i8_check(out)) return rc;
+  uint64_t b;
+  if (!matrix_bytes(out->rows, out->cols, dtype_size(dtype), &b)) return IBP_ERR_SIZE;
+  if (out->rows == 0) return IBP_OK;
+  if ((b && !d_in) || !aligned(d_in, dtype_size(dtype))) return IBP_ERR_INVALID_ARG;
+  if (!apart({codes_range(out), scales_range(out)}, 0, {{d_in, b}}, 0, 0)) return IBP_ERR_INVALID_ARG;
+  I8Args a;
+  if (!view(d_in, b) || !i8_view(out, &a.codes, &a.scales)) return IBP_ERR_INVALID_ARG;
+  a.in = d_in;
+  a.out = nullptr;
+  a.rows = out->rows;
+  a.cols = (uint32_t)out->cols;
+  a.dtype = dtype;
+  return status_of(launch_i8_pack(a, static_cast<hipStream_t>(hip_stream)));
+}
+
+IBP_API int ibp_i8_unpack(const ibp_i8_t *in, void *d_out, int dtype, void *hip_stream) {
+  if (!dtype_ok(dtype)) return IBP_ERR_INVALID_ARG;
+  if (const int rc = i8_check(in)) return rc;
+  uint64_t b;
+  if (!matrix_bytes(in->rows, in->cols, dtype_size(dtype), &b)) return IBP_ERR_SIZE;
+  if (b == 0) return IBP_OK;
+  if (!d_out || !aligned(d_out, dtype_size(dtype))) return IBP_ERR_INVALID_ARG;
+  if (!apart({{d_out, b}}, 0, {codes_range(in), scales_range(in)}, 0, 0)) return IBP_ERR_INVALID_ARG;
+  I8Args a;
+  if (!view(d_out, b) || !i8_view(in, &a.codes, &a.scales)) return IBP_ERR_INVALID_ARG;
+  a.in = nullptr;
+  a.out = d_out;
+  a.rows = in->rows;
+  a.cols = (uint32_t)in->cols;
+  a.dtype = dtype;
+  return status_of(launch_i8_unpack(a, static_cast<hipStream_t>(hip_stream)));
+}
+
+IBP_API uint64_t ibp_i8_matmul_workspace_bytes(uint64_t m, uint64_t n, uint64_t k) {
+  if (!product_rows_ok(m) || !product_rows_ok(n) || k > IBP_I8_MAX_DEPTH) return 0;
+  return m && n ? i8_matmul_workspace(m, n, (uint32_t)k) : 0;
+}
+
+IBP_API int ibp_i8_matmul(const ibp_i8_t *a, const ibp_i8_t *b, void *d_y, int dtype, void *d_workspace,
+                          uint64_t workspace_bytes, void *hip_stream) {
+  if (!dtype_ok(dtype)) return IBP_ERR_INVALID_ARG;
+  if (const int rc = i8_check(a)) return rc;
+  if (const int rc = i8_check(b)) return rc;
+  uint64_t yb;
+  if (a->cols != b->cols || a->cols > IBP_I8_MAX_DEPTH || !product_rows_ok(a->rows) || !product_rows_ok(b->rows) ||
+      !matrix_bytes(a->rows, b->rows, dtype_size(dtype), &yb))
+    return IBP_ERR_SIZE;
+  if (yb == 0) return IBP_OK;
+  const uint64_t wb = i8_matmul_workspace(a->rows, b->rows, (uint32_t)a->cols);
+  if (workspace_bytes < wb) return IBP_ERR_CAPACITY;
+  if (!d_y || !aligned(d_y, dtype_size(dtype)) || (wb && !d_workspace) || !aligned(d_workspace, 16))
+    return IBP_ERR_INVALID_ARG;
+  if (!apart({{d_y, yb}, {d_workspace, wb}}, 0, {codes_range(a), scales_range(a), codes_range(b), scales_range(b)}, 0, 0))
+    return IBP_ERR_INVALID_ARG;
+  int8_t *ac, *bc;
+  float *as, *bs;
+  if (!view(d_y, yb) || !i8_view(a, &ac, &as) || !i8_view(b, &bc, &bs) || !view(d_workspace, wb)) return IBP_ERR_INVALID_ARG;
+  I8MatmulArgs p;
+  p.a_codes = reinterpret_cast<const uint8_t *>(ac);
+  p.b_codes = reinterpret_cast<const uint8_t *>(bc);
+  p.a_scales = as;
+  p.b_scales = bs;
+  p.y = d_y;
+  p.ws = static_cast<int32_t *>(d_workspace);
+  p.M = a->rows;
+  p.N = b->rows;
+  p.K = (uint32_t)a->cols;
+  p.dtype = dtype;
+  return status_of(launch_i8_matmul(p, static_cast<hipStream_t>(hip_stream)));
+}
+
+// ------------------------------------------------------------------ experts
+
+static bool experts_ok(uint64_t n) { return n >= 1 && n <= IBP_MAX_EXPERTS; }
+
+IBP_API uint64_t ibp_expert_order_workspace_bytes(uint64_t n_ids, uint64_t n_experts) {
+  return n_ids < IBP_MAX_TOKENS && experts_ok(n_experts) ? expert_order_workspace(n_ids, (uint32_t)n_experts) : 0;
+}
+
+IBP_API int ibp_expert_order(const int64_t *d_ids, uint64_t n_ids, uint64_t n_experts, int64_t *d_order,
+                             int64_t *d_offsets, void *d_workspace, uint64_t workspace_bytes, uint32_t *d_err_word,
+                             void *hip_stream) {
+  if (n_ids >= IBP_MAX_TOKENS || !experts_ok(n_experts)) return IBP_ERR_SIZE;
+  const uint64_t wb = expert_order_workspace(n_ids, (uint32_t)n_experts), ib = n_ids * 8, ob = (n_experts + 1) * 8;
+  if (workspace_bytes < wb) return IBP_ERR_CAPACITY;
+  if (!d_offsets || (n_ids && (!d_ids || !d_order)) || (wb && !d_workspace)) return IBP_ERR_INVALID_ARG;
+  if (!aligned(d_ids, 8) || !aligned(d_order, 8) || !aligned(d_offsets, 8) || !aligned(d_workspace, 16) || !aligned(d_err_word, 4))
+    return IBP_ERR_INVALID_ARG;
+  if (!apart({{d_order, ib}, {d_offsets, ob}, {d_workspace, wb}}, 0, {{d_ids, ib}}, 0, 0)) return IBP_ERR_INVALID_ARG;
+  if (!view(d_ids, ib) || !view(d_order, ib) || !view(d_offsets, ob) || !view(d_workspace, wb) || !view(d_err_word, d_err_word ? 4 : 0))
+    return IBP_ERR_INVALID_ARG;
+  ExpertOrderArgs a;
+  a.ids = d_ids;
+  a.order = d_order;
+  a.offsets = d_offsets;
+  a.counts = static_cast<uint32_t *>(d_workspace);
+  a.err = d_err_word;
+  a.n = n_ids;
+  a.experts = (uint32_t)n_experts;
+  return status_of(launch_expert_order(a, static_cast<hipStream_t>(hip_stream)));
+}
+
+IBP_API uint64_t ibp_mx_grouped_matmul_workspace_bytes(uint64_t m, uint64_t n_experts, uint64_t n, uint64_t k,
+                                                       uint32_t a_format) {
+  if (!product_rows_ok(m) || !product_rows_ok(n) || k > IBP_MAX_COLS || a_format > IBP_MX_E2M1 || !experts_ok(n_experts)) return 0;
+  return m && n ? mx_grouped_matmul_workspace(m, (uint32_t)n_experts, n, (uint32_t)k) : 0;
+}
+
+IBP_API int ibp_mx_grouped_matmul(const ibp_mx_t *a, const ibp_mx_t *b, const int64_t *d_offsets, uint64_t n_experts,
+                                  void *d_y, int dtype, void *d_workspace, uint64_t workspace_bytes,
+                                  uint32_t *d_err_word, void *hip_stream) {
+  if (!dtype_ok(dtype)) return IBP_ERR_INVALID_ARG;
+  if (const int rc = mx_check(a)) return rc;
+  if (const int rc = mx_check(b)) return rc;
+  if (b->format != IBP_MX_E2M1) return IBP_ERR_INVALID_ARG;
+  if (!experts_ok(n_experts) || b->rows % n_experts) return IBP_ERR_SIZE;
+  const uint64_t N = b->rows / n_experts;
+  uint64_t yb;
+  if (a->cols != b->cols || !product_rows_ok(a->rows) || !product_rows_ok(N) ||
+      !matrix_bytes(a->rows, N, dtype_size(dtype), &yb))
+    return IBP_ERR_SIZE;
+  if (yb == 0) return IBP_OK;
+  const uint64_t wb = mx_grouped_matmul_workspace(a->rows, (uint32_t)n_experts, N, (uint32_t)a->cols);
+  const uint64_t ob = (n_experts + 1) * 8;
+  if (workspace_bytes < wb) return IBP_ERR_CAPACITY;
+  if (!d_y || !aligned(d_y, dtype_size(dtype)) || !d_offsets || !aligned(d_offsets, 8) || (wb && !d_workspace) ||
+      !aligned(d_workspace, 16) || !aligned(d_err_word, 4))
+    return IBP_ERR_INVALID_ARG;
+  if (!apart({{d_y, yb}, {d_workspace, wb}}, 0,
+             {codes_range(a), scales_range(a), codes_range(b), scales_range(b), {d_offsets, ob}}, 0, 0))
+    return IBP_ERR_INVALID_ARG;
+  uint8_t *ac, *as, *bc, *bs;
+  if (!view(d_y, yb) || !mx_view(a, &ac, &as) || !mx_view(b, &bc, &bs) || !view(d_offsets, ob) || !view(d_workspace, wb) ||
+      !view(d_err_word, d_err_word ? 4 : 0))
+    return IBP_ERR_INVALID_ARG;
+  MxMatmulArgs p;
+  p.a_codes = ac;
+  p.a_scales = as;
+  p.b_codes = bc;
+  p.b_scales = bs;
+  p.y = d_y;
+  p.ws = static_cast<float *>(d_workspace);
+  p.M = a->rows;
+  p.N = N;
+  p.K = (uint32_t)a->cols;
+  p.a_e4m3 = a->format == IBP_MX_E4M3;
+  p.dtype = dtype;
+  p.offsets = d_offsets;
+  p.experts = (uint32_t)n_experts;
+  p.err = d_err_word;
+  return status_of(launch_mx_grouped_matmul(p, static_cast<hipStream_t>(hip_stream)));
+}
+
+static bool grouped_sizes_ok(uint64_t tokens, uint64_t n_experts, uint64_t outs, uint64_t ins) {
+  return tokens < IBP_MAX_TOKENS && experts_ok(n_experts) && product_rows_ok(outs) && ins <= IBP_MAX_COLS;
+}
+
+IBP_API uint64_t ibp_mx_grouped_wgrad_workspace_bytes(uint64_t tokens, uint64_t n_experts, uint64_t outs, uint64_t ins,
+                                                      int dy_dtype) {
+  if (!grouped_sizes_ok(tokens, n_experts, outs, ins) || !dtype_ok(dy_dtype)) return 0;
+  return outs && ins ? mx_grouped_wgrad_workspace(tokens, (uint32_t)n_experts, (uint32_t)outs, (uint32_t)ins, dy_dtype) : 0;
+}
+
+IBP_API int ibp_mx_grouped_wgrad(const void *d_dy, int dy_dtype, uint64_t outs, const ibp_mx_t *x8,
+                                 const int64_t *d_offsets, uint64_t n_experts, void *d_dw, int dw_dtype,
+                                 void *d_workspace, uint64_t workspace_bytes, uint32_t *d_err_word, void *hip_stream) {
+  if (!dtype_ok(dy_dtype) || !dtype_ok(dw_dtype)) return IBP_ERR_INVALID_ARG;
+  if (const int rc = mx_check(x8)) return rc;
+  if (x8->format != IBP_MX_E4M3) return IBP_ERR_INVALID_ARG;
+  uint64_t yb, wgb;
+  if (!grouped_sizes_ok(x8->rows, n_experts, outs, x8->cols) || !matrix_bytes(x8->rows, outs, dtype_size(dy_dtype), &yb) ||
+      !matrix_bytes(n_experts * outs, x8->cols, dtype_size(dw_dtype), &wgb))
+    return IBP_ERR_SIZE;
+  if (wgb == 0) return IBP_OK;
+  const uint64_t wb = mx_grouped_wgrad_workspace(x8->rows, (uint32_t)n_experts, (uint32_t)outs, (uint32_t)x8->cols, dy_dtype);
+  const uint64_t ob = (n_experts + 1) * 8;
+  if (workspace_bytes < wb) return IBP_ERR_CAPACITY;
+  if (!d_dw || !aligned(d_dw, dtype_size(dw_dtype)) || (yb && !d_dy) || !aligned(d_dy, dtype_size(dy_dtype)) ||
+      !d_offsets || !aligned(d_offsets, 8) || (wb && !d_workspace) || !aligned(d_workspace, 16) || !aligned(d_err_word, 4))
+    return IBP_ERR_INVALID_ARG;
+  if (!apart({{d_dw, wgb}, {d_workspace, wb}}, 0, {{d_dy, yb}, codes_range(x8), scales_range(x8), {d_offsets, ob}}, 0, 0))
+    return IBP_ERR_INVALID_ARG;
+  uint8_t *xc, *xs;
+  if (!view(d_dy, yb) || !mx_view(x8, &xc, &xs) || !view(d_dw, wgb) || !view(d_offsets, ob) || !view(d_workspace, wb) ||
+      !view(d_err_word, d_err_word ? 4 : 0))
+    return IBP_ERR_INVALID_ARG;
+  MxWgradArgs p;
+  p.dy = d_dy;
+  p.x_codes = xc;
+  p.x_scales = xs;
+  p.dw = d_dw;
+  p.ws = static_cast<float *>(d_workspace);
+  p.T = x8->rows;
+  p.N = (uint32_t)outs;
+  p.K = (uint32_t)x8->cols;
+  p.dy_dtype = dy_dtype;
+  p.dtype = dw_dtype;
+  p.offsets = d_offsets;
+  p.experts = (uint32_t)n_experts;
+  p.err = d_err_word;
+  return status_of(launch_mx_grouped_wgrad(p, static_cast<hipStream_t>(hip_stream)));
 }
 
 }  // extern "C"

@@ -60,6 +60,16 @@ __device__ __forceinline__ uint32_t wave_incl_scan(uint32_t x) {
   return x;
 }
 
+// Lanes of the wavefront whose digit equals this lane's, among the lanes of `live`.
+__device__ __forceinline__ uint64_t same_digit(uint32_t d, uint32_t bits, uint64_t live) {
+  uint64_t m = live;
+  for (uint32_t b = 0; b < bits; ++b) {
+    const uint64_t v = ballot((d >> b) & 1u);
+    m &= (d >> b) & 1u ? v : ~v;
+  }
+  return m;
+}
+
 __device__ __forceinline__ uint64_t wave_sum64(uint64_t v) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);

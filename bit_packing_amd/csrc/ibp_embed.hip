@@ -120,16 +120,6 @@ __device__ __forceinline__ uint32_t key_of(const SortArgs &a, uint32_t j) {
   return (uint32_t)v;
 }
 
-// Lanes of the wavefront whose digit equals this lane's, among the lanes of `live`.
-__device__ __forceinline__ uint64_t same_digit(uint32_t d, uint32_t bits, uint64_t live) {
-  uint64_t m = live;
-  for (uint32_t b = 0; b < bits; ++b) {
-    const uint64_t v = ballot((d >> b) & 1u);
-    m &= (d >> b) & 1u ? v : ~v;
-  }
-  return m;
-}
-
 // Per workgroup, how many of its tokens have each digit.
 template <bool FIRST> __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
   __shared__ uint32_t hist[kBins];

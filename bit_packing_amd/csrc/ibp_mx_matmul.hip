@@ -47,11 +47,6 @@ template <bool A8> __device__ __forceinline__ v4f mfma_mx(v8i w, v8i x, v4f acc,
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, acc, 4, A8 ? 0 : 4, 0, ws, 0, xs);
 }
 
-// A 16-byte piece of a row, zero from byte `pitch` on.
-__device__ __forceinline__ uint4 piece(const uint8_t *row, uint32_t at, uint32_t pitch) {
-  return at < pitch ? *reinterpret_cast<const uint4 *>(row + at) : make_uint4(0u, 0u, 0u, 0u);
-}
-
 __device__ __forceinline__ v8i operand(uint4 lo, uint4 hi) {
   return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
 }
@@ -75,12 +70,28 @@ __device__ __forceinline__ uint4 scales16(const uint8_t *row, uint32_t b, uint32
 // TB/s; half of the wavefronts' time is waiting).  A workgroup computes 16 x 16 outputs, its wavefronts take the steps of k in
 // turn and their sums are added in order through LDS.  A step is 16 blocks, four matrix
 // instructions; each load takes 64 consecutive bytes of 16 rows.
-template <bool A8, int DO> __global__ void mx_direct_kernel(MxMatmulArgs a) {
+//
+// GROUPED: the rows are sorted by expert, and blockIdx.y counts units of 16 rows of one
+// expert, as many as there can be; those that there are not have nothing to do.
+template <bool GROUPED, bool A8, int DO> __global__ void mx_direct_kernel(MxMatmulArgs a) {
   using TO = typename Num<DO>::T;
   extern __shared__ float red[];
   const uint32_t lane = lane_id(), wave = uniform(threadIdx.x / kWave), waves = blockDim.x / kWave;
   const uint32_t r = lane & 15, g = lane >> 4;
-  const uint64_t n0 = (uint64_t)blockIdx.x * 16, m0 = (uint64_t)blockIdx.y * 16;
+  const uint64_t n0 = (uint64_t)blockIdx.x * 16;
+  uint64_t m0 = (uint64_t)blockIdx.y * 16;
+  if constexpr (GROUPED) {
+    const Experts x{a.offsets, a.experts, 4, a.M};
+    if (a.err && blockIdx.x == 0 && blockIdx.y == 0 && wave == 0) check_offsets(x, a.err);
+    const UnitSearch<false> search(x);
+    if (blockIdx.y >= search.total) return;
+    const Unit u = search.find(blockIdx.y);
+    if (u.row0 >= u.end) return;
+    m0 = u.row0;
+    a.M = u.end;
+    a.b_codes += u.expert * a.N * mx_code_pitch(a.K, false);
+    a.b_scales += u.expert * a.N * mx_scale_pitch(a.K);
+  }
   const uint32_t nblk = (uint32_t)mx_blocks(a.K), sp = (uint32_t)mx_scale_pitch(a.K);
   const uint32_t wp = (uint32_t)mx_code_pitch(a.K, false), xp = (uint32_t)mx_code_pitch(a.K, A8);
   // rows past the end repeat the last one; their results are not stored
@@ -122,7 +133,7 @@ template <bool A8> hipError_t go_direct(const MxMatmulArgs &a, hipStream_t s) {
   uint32_t waves = gx * gy <= 256 ? 16 : 4;
   while (waves > 1 && waves > steps) waves /= 2;
   return with_dtype(a.dtype, [&](auto d) {
-    mx_direct_kernel<A8, d.value><<<dim3((uint32_t)gx, (uint32_t)gy), waves * kWave, (waves - 1) * 1024, s>>>(a);
+    mx_direct_kernel<false, A8, d.value><<<dim3((uint32_t)gx, (uint32_t)gy), waves * kWave, (waves - 1) * 1024, s>>>(a);
     return hipGetLastError();
   });
 }
@@ -140,41 +151,11 @@ template <bool A8> hipError_t go_direct(const MxMatmulArgs &a, hipStream_t s) {
 // the other, and by power: the clock falls to 2.0 GHz.  The 32 x 32 x 64 matrix instruction
 // takes 2% fewer cycles at a clock 5% lower (with packing 330 us against 320); without
 // phases, reading each fragment's successor once it is used, 331 against 327.
+// LDS rows are 128 (e4m3) or 64 bytes (e2m1).
 //
-// LDS rows are 128 (e4m3) or 64 bytes (e2m1).  The 16-byte pieces of a row are permuted by
-// the row number, so that eight rows read at one piece lie in different banks: a read
-// takes 4 clocks then, 256 bytes a clock (measured; 8 with (row >> 2) & 3 for 64-byte
-// rows, 8 and 16 with none).  The loads write LDS in lane order, so the lanes' sources
-// make the permutation.
-template <uint32_t PITCH> __device__ __forceinline__ uint32_t swizzle(uint32_t row, uint32_t piece) {
-  return piece ^ (PITCH == 128 ? row & 7 : (row >> 1) & 3);
-}
-
-// One operand's codes of a stage: ROWS rows of PITCH bytes, the loads shared by WAVES wavefronts.
-template <uint32_t ROWS, uint32_t PITCH, uint32_t WAVES> struct Tile {
-  static constexpr uint32_t kBytes = ROWS * PITCH, kLoads = kBytes / (1024 * WAVES);
-  const uint8_t *code[kLoads];
-  uint32_t at[kLoads];
-
-  __device__ __forceinline__ void init(const uint8_t *codes, uint64_t row0, uint64_t rows, uint32_t cp, uint32_t wave,
-                                       uint32_t lane) {
-#pragma unroll
-    for (uint32_t i = 0; i < kLoads; ++i) {
-      const uint32_t slot = (i * WAVES + wave) * 64 + lane, row = slot / (PITCH / 16);
-      const uint64_t r = row0 + row < rows ? row0 + row : rows - 1;  // results of rows past the end are not stored
-      at[i] = swizzle<PITCH>(row, slot % (PITCH / 16)) * 16;
-      code[i] = codes + r * cp + at[i];
-    }
-  }
-  // The rows' bytes from k on, zeros past the rows' ends.
-  __device__ __forceinline__ void load(uint8_t *lds, uint32_t k, uint32_t cp, uint32_t wave) {
-#pragma unroll
-    for (uint32_t i = 0; i < kLoads; ++i)
-      to_lds16(k + at[i] < cp ? code[i] + k : kZeros, lds + (i * WAVES + wave) * 1024);
-  }
-};
-
-template <bool A8, int WM, int WN, int FM, int FN, int DO>
+// GROUPED: the tiles are cut from each expert's rows.  Their number is on the device, the
+// workgroups are as many as it can be; those beyond it have nothing to do.
+template <bool GROUPED, bool A8, int WM, int WN, int FM, int FN, int DO>
 __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, void *dst, uint32_t tiles_m,
                                                              uint32_t tiles_n, uint32_t stages_each) {
   using TO = typename Num<DO>::T;
@@ -191,8 +172,27 @@ __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, voi
   static_assert(kStages * kStage + 2 * kScales <= 160 * 1024 && (kStages - 2) * kLoads < 16, "");
   __shared__ __align__(1024) uint8_t ring[kStages * kStage + 2 * kScales];
   const uint32_t lane = lane_id(), wave = uniform(threadIdx.x / kWave), r = lane & 15, g = lane >> 4;
-  const TileId t = tile_of(blockIdx.x, tiles_m, tiles_n);
-  const uint64_t m0 = (uint64_t)t.row * kRowsA, n0 = (uint64_t)t.col * kRowsB;
+  const uint64_t all_m = a.M;
+  uint64_t m0, n0;
+  if constexpr (GROUPED) {
+    static_assert((kRowsA & (kRowsA - 1)) == 0, "");
+    const Experts x{a.offsets, a.experts, (uint32_t)__builtin_ctz(kRowsA), a.M};
+    if (a.err && blockIdx.x == 0 && blockIdx.y == 0 && wave == 0) check_offsets(x, a.err);
+    const UnitSearch<false> search(x);
+    if (blockIdx.x >= (uint64_t)search.total * tiles_n) return;
+    const TileId t = tile_of(blockIdx.x, search.total, tiles_n);
+    const Unit u = search.find(t.row);
+    if (u.row0 >= u.end) return;
+    m0 = u.row0;
+    n0 = (uint64_t)t.col * kRowsB;
+    a.M = u.end;
+    a.b_codes += u.expert * a.N * mx_code_pitch(a.K, false);
+    a.b_scales += u.expert * a.N * mx_scale_pitch(a.K);
+  } else {
+    const TileId t = tile_of(blockIdx.x, tiles_m, tiles_n);
+    m0 = (uint64_t)t.row * kRowsA;
+    n0 = (uint64_t)t.col * kRowsB;
+  }
 
   const uint32_t nblk = (uint32_t)mx_blocks(a.K), sp = (uint32_t)mx_scale_pitch(a.K);
   const uint32_t cpa = (uint32_t)mx_code_pitch(a.K, A8), cpb = (uint32_t)mx_code_pitch(a.K, false);
@@ -258,13 +258,6 @@ __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, voi
     }
   };
   uint8_t *const scales = ring + kStages * kStage;
-  auto barrier = [&] {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("" ::: "memory");
-  };
   // Each turn of the loop is a reading phase and a multiplying phase with a barrier after
   // each.  With two wavefronts a SIMD the second half of the wavefronts runs one phase
   // behind the first (kPingPong), so LDS serves one half while the other multiplies; in
@@ -285,8 +278,8 @@ __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, voi
   for (uint32_t k = 0; k + 1 < kStages; ++k) fill(ring + k * kStage, k);
   fill_scales(scales, 0);
   __builtin_amdgcn_s_waitcnt(kWaitVmcnt0 & ~0x0F00);  // and LDS writes
-  barrier();
-  if (behind) barrier();
+  phase_barrier();
+  if (behind) phase_barrier();
   uint32_t now = 0, next = kStages - 1;  // ring places of stage k and of stage k - 1, which is filled anew
 #pragma unroll 1
   for (uint32_t k = 0; k < steps; ++k) {
@@ -299,7 +292,7 @@ __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, voi
     // after it; loads of scales in between make the wait longer, never shorter, and are
     // kGroup stages early): after one or two barriers the first half reads it.
     __builtin_amdgcn_s_waitcnt(0x0070 | (kStages - (kLateFill ? 3 : 2)) * kLoads);
-    barrier();
+    phase_barrier();
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int m = 0; m < FM; ++m) {
@@ -312,47 +305,15 @@ __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, voi
     }
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_setprio(0);
-    barrier();
+    phase_barrier();
   }
-  if (kPingPong && wave < kWaves / 2) barrier();
+  if (kPingPong && wave < kWaves / 2) phase_barrier();
   __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);  // no load into LDS outlives the workgroup
-  // Results go through LDS, two fragments' rows at a time, so that a store covers whole
-  // lines of y (from the fragments themselves a row gets 32 bytes at a time).
   __syncthreads();
-  constexpr uint32_t kCols = 16 * FN, kPad = 16 / sizeof(TO), kEach = 16 / sizeof(TO);
-  constexpr uint32_t kOutRows = 32, kPieces = kOutRows * kCols / kEach / 64;
-  static_assert(kWaves * kOutRows * (kCols + kPad) * sizeof(TO) <= sizeof(ring), "");
-  TO *const out = reinterpret_cast<TO *>(ring) + wave * kOutRows * (kCols + kPad);
-  TO *y = static_cast<TO *>(dst) + (uint64_t)blockIdx.y * a.M * a.N;
-  typedef TO Aligned __attribute__((ext_vector_type(kEach)));
-  typedef TO Loose __attribute__((ext_vector_type(kEach), aligned(sizeof(TO))));
-  typedef TO Four __attribute__((ext_vector_type(4)));
-#pragma unroll
-  for (int m = 0; m < FM; m += 2) {
-    wave_lds_sync();
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int n = 0; n < FN; ++n) {
-        const v4f x = acc[n][m + h];
-        *reinterpret_cast<Four *>(out + (16 * h + r) * (kCols + kPad) + 16 * n + 4 * g) = Four{(TO)x[0], (TO)x[1], (TO)x[2], (TO)x[3]};
-      }
-    wave_lds_sync();
-#pragma unroll
-    for (uint32_t p = 0; p < kPieces; ++p) {
-      const uint32_t slot = p * 64 + lane, row = slot / (kCols / kEach), c = slot % (kCols / kEach) * kEach;
-      const uint64_t gm = m0 + wm + 16 * m + row, gn = n0 + wn + c;
-      if (gm >= a.M || gn >= a.N) continue;
-      const Aligned x = *reinterpret_cast<const Aligned *>(out + row * (kCols + kPad) + c);
-      if (gn + kEach <= a.N) {
-        *reinterpret_cast<Loose *>(y + gm * a.N + gn) = x;
-      } else {
-#pragma unroll
-        for (uint32_t e = 0; e < kEach; ++e)
-          if (gn + e < a.N) y[gm * a.N + gn + e] = x[e];
-      }
-    }
-  }
+  static_assert(kWaves * out_bytes<TO, FN>() <= sizeof(ring), "");
+  store_fragments<TO, FM, FN>(reinterpret_cast<TO *>(ring + wave * out_bytes<TO, FN>()),
+                              static_cast<TO *>(dst) + (uint64_t)blockIdx.y * all_m * a.N, m0 + wm, a.M, n0 + wn, a.N, lane,
+                              [&](int m, int n) { return acc[n][m]; });
 }
 
 // Adds the ranges' sums in order.
@@ -406,9 +367,9 @@ Plan plan_of(uint64_t M, uint64_t N, uint32_t K) {
 template <bool A8, int DO> hipError_t go_tile(const MxMatmulArgs &a, const Plan &p, void *dst, hipStream_t s) {
   const dim3 grid(p.tiles_m * p.tiles_n, p.splits);
   if (p.kind == Plan::kBig)
-    mx_tile_kernel<A8, 2, 4, 8, 4, DO><<<grid, 512, 0, s>>>(a, dst, p.tiles_m, p.tiles_n, p.stages_each);
+    mx_tile_kernel<false, A8, 2, 4, 8, 4, DO><<<grid, 512, 0, s>>>(a, dst, p.tiles_m, p.tiles_n, p.stages_each);
   else
-    mx_tile_kernel<A8, 2, 2, 4, 4, DO><<<grid, 256, 0, s>>>(a, dst, p.tiles_m, p.tiles_n, p.stages_each);
+    mx_tile_kernel<false, A8, 2, 2, 4, 4, DO><<<grid, 256, 0, s>>>(a, dst, p.tiles_m, p.tiles_n, p.stages_each);
   return hipGetLastError();
 }
 
@@ -428,7 +389,36 @@ template <bool A8> hipError_t go(const MxMatmulArgs &a, hipStream_t s) {
   });
 }
 
+// ------------------------------------------------------------------ rows of experts
+
+template <bool A8> hipError_t go_grouped(const MxMatmulArgs &a, hipStream_t s) {
+  const uint64_t gx = (a.N + 15) / 16, gy = most_units(a.M, a.experts, 4, false);
+  const bool big = a.M / a.experts >= 128, direct = a.M / a.experts < 24 && gy <= 65535;
+  return with_dtype(a.dtype, [&](auto d) {
+    if (direct) {
+      const uint32_t steps = (uint32_t)((mx_blocks(a.K) + kStep - 1) / kStep);
+      uint32_t waves = 4;
+      while (waves > 1 && waves > steps) waves /= 2;
+      mx_direct_kernel<true, A8, d.value><<<dim3((uint32_t)gx, (uint32_t)gy), waves * kWave, (waves - 1) * 1024, s>>>(a);
+      return hipGetLastError();
+    }
+    const uint32_t wide = big ? 256 : 128, stages = (uint32_t)((mx_blocks(a.K) + 3) / 4);
+    const uint64_t tiles_m = most_units(a.M, a.experts, big ? 8 : 7, false), tiles_n = (a.N + wide - 1) / wide;
+    if (tiles_m * tiles_n > 0x7FFFFF) return hipErrorInvalidValue;
+    const uint32_t grid = (uint32_t)(tiles_m * tiles_n), each = (stages + 3) / 4 * 4;
+    if (big) mx_tile_kernel<true, A8, 2, 4, 8, 4, d.value><<<grid, 512, 0, s>>>(a, a.y, 0, (uint32_t)tiles_n, each);
+    else mx_tile_kernel<true, A8, 2, 2, 4, 4, d.value><<<grid, 256, 0, s>>>(a, a.y, 0, (uint32_t)tiles_n, each);
+    return hipGetLastError();
+  });
+}
+
 }  // namespace
+
+uint64_t mx_grouped_matmul_workspace(uint64_t, uint32_t, uint64_t, uint32_t) { return 0; }
+
+hipError_t launch_mx_grouped_matmul(const MxMatmulArgs &a, hipStream_t s) {
+  return a.a_e4m3 ? go_grouped<true>(a, s) : go_grouped<false>(a, s);
+}
 
 uint64_t mx_matmul_workspace(uint64_t M, uint64_t N, uint32_t K) {
   const Plan p = plan_of(M, N, K);

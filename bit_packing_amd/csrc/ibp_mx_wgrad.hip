@@ -103,9 +103,14 @@ template <typename T> __device__ __forceinline__ T from_global(const uint8_t *p)
 // power.  The large tile is 11% slower in clock for 8% fewer cycles with it (894 us against
 // 862) and takes F = 16; the small one, bound by latency, is faster (999 x 504 x 1000 14.5 us
 // against 15.3, 16384 x 256 x 256 23.5 against 25.5).
-template <int F, int WI, int WO, int FI, int FO, bool DIRECT, int DY, int DO>
+//
+// GROUPED: the tokens are sorted by expert, and blockIdx.y counts units of tokens of one expert,
+// as many as there can be, of which an expert without tokens has one; dst is that expert's or,
+// where experts are cut into units, the unit's.  All parts of dY are summed by one workgroup.
+template <bool GROUPED, int F, int WI, int WO, int FI, int FO, bool DIRECT, int DY, int DO>
 __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *dst, uint64_t t_each, uint32_t tiles_o,
                                                            uint32_t tiles_i, uint32_t splits) {
+  static_assert(!GROUPED || DIRECT, "");
   using TY = typename Num<DY>::T;
   static_assert(!DIRECT || DY == IBP_BF16, "");
   using TO = typename Num<DO>::T;
@@ -116,11 +121,24 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
   static_assert(kStepY % 8 == 0 && kStepX % 8 == 0, "the permutation goes by t & 7, the same for all pieces of a thread");
   __shared__ __align__(1024) uint8_t ring[kRing * kStage];
   const uint32_t lane = lane_id(), wave = uniform(threadIdx.x / kWave);
+  uint32_t part = 0;
+  uint64_t t0, t1;
+  if constexpr (GROUPED) {
+    const Experts x{a.offsets, a.experts, (uint32_t)__builtin_ctzll(t_each), a.T};
+    if (a.err && blockIdx.x == 0 && blockIdx.y == 0 && wave == 0) check_offsets(x, a.err);
+    const UnitSearch<true> search(x);
+    if (blockIdx.y >= search.total) return;
+    const Unit u = search.find(blockIdx.y);
+    t0 = u.row0;
+    t1 = u.row0 + t_each < u.end ? u.row0 + t_each : u.end;
+  } else {
+    part = blockIdx.y / splits;
+    t0 = (blockIdx.y - part * splits) * t_each;
+    t1 = t0 + t_each < a.T ? t0 + t_each : a.T;
+  }
   const TileId tile = tile_of(blockIdx.x, tiles_o, tiles_i);
   const uint32_t o0 = tile.row * kWideO, i0 = tile.col * kWideI;
   const uint32_t wi = (wave % WI) * FI, wo = (wave / WI) * FO;  // in blocks of F
-  const uint32_t part = blockIdx.y / splits;
-  const uint64_t t0 = (blockIdx.y - part * splits) * t_each, t1 = t0 + t_each < a.T ? t0 + t_each : a.T;
   const uint32_t cp = (uint32_t)mx_code_pitch(a.K, true), sp = (uint32_t)mx_scale_pitch(a.K);
   const TY *dy = static_cast<const TY *>(a.dy);
 
@@ -134,10 +152,13 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
   // without DIRECT a piece past the row's end is the row's last eight elements (load8)
   const bool wide = a.N >= 8;
   const uint64_t at_y = DIRECT ? cy : (wide ? (cy + 8 <= a.N ? cy : a.N - 8) : 0);
-  const uint64_t row_y = t0 + ty + (DIRECT ? part * a.T : 0);
-  const uint8_t *py = in_y ? reinterpret_cast<const uint8_t *>(dy + row_y * a.dy_pitch + at_y) : kZeros;
-  const uint8_t *px = in_x ? a.x_codes + (t0 + tx) * cp + cx : kZeros;
-  const uint8_t *ps = in_x ? a.x_scales + (t0 + tx) * sp + cx / (4 * kMxBlock) * 4 : kZeros;  // its dword
+  const uint8_t *py, *px, *ps;  // ps: its scales' dword
+  auto begin = [&](uint32_t part) {
+    const uint64_t row_y = t0 + ty + (DIRECT ? part * a.T : 0);
+    py = in_y ? reinterpret_cast<const uint8_t *>(dy + row_y * a.dy_pitch + at_y) : kZeros;
+    px = in_x ? a.x_codes + (t0 + tx) * cp + cx : kZeros;
+    ps = in_x ? a.x_scales + (t0 + tx) * sp + cx / (4 * kMxBlock) * 4 : kZeros;
+  };
   const uint32_t scale_shift = cx / kMxBlock % 4 * 8;
   const uint64_t go_y = in_y ? (uint64_t)kStepY * a.dy_pitch * sizeof(TY) : 0, go_x = in_x ? (uint64_t)kStepX * cp : 0;
   const uint64_t go_s = in_x ? (uint64_t)kStepX * sp : 0;
@@ -200,13 +221,6 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
     for (uint32_t p = 0; p < kPiecesX; ++p)
       *reinterpret_cast<v8b *>(st + at_x + p * kStepX * kWideI * 2) = decode8(f.q[p], mx_factor((f.s[p] >> scale_shift) & 0xFFu));
   };
-  auto barrier = [&] {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("" ::: "memory");
-  };
   // A turn is a reading phase and a multiplying phase with a barrier after each; with two
   // wavefronts a SIMD the second half of them runs one phase behind the first.
   constexpr bool kPingPong = kWaves == 8;
@@ -238,7 +252,7 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
     // turn k - 1's are not waited for): after two barriers the first half reads it.
     __builtin_amdgcn_s_waitcnt(0xC07F);
     if constexpr (DIRECT) __builtin_amdgcn_s_waitcnt(0x0F70 | kLoads);
-    barrier();
+    phase_barrier();
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (uint32_t s = 0; s < kDeep; ++s) {
@@ -257,28 +271,34 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
     }
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_setprio(0);
-    barrier();
+    phase_barrier();
   };
-  if (steps) {
-#pragma unroll
-    for (uint32_t k = 0; k < 3; ++k) fetch_direct(ring + k * kStage, k);
-#pragma unroll
-    for (uint32_t k = 0; k < 2; ++k) fetch(set[k], k);
-#pragma unroll
-    for (uint32_t k = 0; k < 2; ++k) settle(ring + k * kStage, set[k]);
-#pragma unroll
-    for (uint32_t k = 0; k < 2; ++k) fetch(set[k], k + 2);
-    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0 & ~0x0F00);  // and LDS writes
-  }
-  barrier();
-  if (behind) barrier();
+  const uint32_t parts = GROUPED ? splits : part + 1;
 #pragma unroll 1
-  for (uint32_t k = 0; k < steps; k += 2) {
-    turn(set[0], k);
-    turn(set[1], k + 1);
+  for (uint32_t p = part; p < parts; ++p) {
+    begin(p);
+    if (steps) {
+#pragma unroll
+      for (uint32_t k = 0; k < 3; ++k) fetch_direct(ring + k * kStage, k);
+#pragma unroll
+      for (uint32_t k = 0; k < 2; ++k) fetch(set[k], k);
+#pragma unroll
+      for (uint32_t k = 0; k < 2; ++k) settle(ring + k * kStage, set[k]);
+#pragma unroll
+      for (uint32_t k = 0; k < 2; ++k) fetch(set[k], k + 2);
+      __builtin_amdgcn_s_waitcnt(kWaitVmcnt0 & ~0x0F00);  // and LDS writes
+    }
+    phase_barrier();
+    if (behind) phase_barrier();
+#pragma unroll 1
+    for (uint32_t k = 0; k < steps; k += 2) {
+      turn(set[0], k);
+      turn(set[1], k + 1);
+    }
+    if (kPingPong && !behind) phase_barrier();
+    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);  // no load into LDS outlives the workgroup, or this part
+    if (GROUPED && p + 1 < parts) phase_barrier();  // every wavefront's
   }
-  if (kPingPong && !behind) barrier();
-  __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);  // no load into LDS outlives the workgroup
   // a lane has once or four times four consecutive i of one o
   TO *dw = static_cast<TO *>(dst) + (uint64_t)blockIdx.y * a.N * a.K;
 #pragma unroll
@@ -376,22 +396,111 @@ Plan plan_of(uint64_t T, uint32_t N, uint32_t K, int dy_dtype, bool aligned) {
 
 uint32_t padded(uint32_t N) { return (N + 7) / 8 * 8; }
 
+// dY's parts into `copy`, rows of a.dy_pitch elements.
+hipError_t lay_out(const MxWgradArgs &a, __bf16 *copy, uint32_t parts, hipStream_t s) {
+  const uint64_t n = (a.T * (a.dy_pitch / 8) + kBlock - 1) / kBlock;
+  return with_dtype(a.dy_dtype, [&](auto d) {
+    wgrad_parts_kernel<d.value><<<(uint32_t)(n < (1u << 20) ? n : (1u << 20)), kBlock, 0, s>>>(a, copy, parts);
+    return hipGetLastError();
+  });
+}
+
 template <int DO> hipError_t go(const MxWgradArgs &a, const Plan &p, void *dst, hipStream_t s) {
   const dim3 grid(p.tiles_o * p.tiles_i, p.splits * p.parts);
   auto launch = [&](auto kernel, uint32_t threads) {
     kernel<<<grid, threads, 0, s>>>(a, dst, p.t_each, p.tiles_o, p.tiles_i, p.splits);
     return hipGetLastError();
   };
-  if (p.big) return launch(wgrad_kernel<16, 2, 4, 8, 4, true, IBP_BF16, DO>, 512);
+  if (p.big) return launch(wgrad_kernel<false, 16, 2, 4, 8, 4, true, IBP_BF16, DO>, 512);
   if constexpr (DO == IBP_F32) {  // parts are always joined
-    if (a.dy_dtype == IBP_F16) return launch(wgrad_kernel<32, 2, 2, 2, 2, false, IBP_F16, DO>, 256);
-    if (a.dy_dtype == IBP_F32) return launch(wgrad_kernel<32, 2, 2, 2, 2, false, IBP_F32, DO>, 256);
+    if (a.dy_dtype == IBP_F16) return launch(wgrad_kernel<false, 32, 2, 2, 2, 2, false, IBP_F16, DO>, 256);
+    if (a.dy_dtype == IBP_F32) return launch(wgrad_kernel<false, 32, 2, 2, 2, 2, false, IBP_F32, DO>, 256);
   }
-  return a.N % 8 == 0 && (uintptr_t)a.dy % 16 == 0 ? launch(wgrad_kernel<32, 2, 2, 2, 2, true, IBP_BF16, DO>, 256)
-                                                   : launch(wgrad_kernel<32, 2, 2, 2, 2, false, IBP_BF16, DO>, 256);
+  return a.N % 8 == 0 && (uintptr_t)a.dy % 16 == 0 ? launch(wgrad_kernel<false, 32, 2, 2, 2, 2, true, IBP_BF16, DO>, 256)
+                                                   : launch(wgrad_kernel<false, 32, 2, 2, 2, 2, false, IBP_BF16, DO>, 256);
+}
+
+// ------------------------------------------------------------------ tokens of experts
+
+// Adds an expert's units in order; zeros where it has none.
+template <int DO> __global__ __launch_bounds__(kBlock) void grouped_join_kernel(MxWgradArgs a, uint64_t t_each, uint32_t most) {
+  using TO = typename Num<DO>::T;
+  const uint64_t n = (uint64_t)a.N * a.K;
+  const UnitSearch<true> search(Experts{a.offsets, a.experts, (uint32_t)__builtin_ctzll(t_each), a.T});
+  const uint2 units = search.units_of(blockIdx.y);
+  const uint32_t last = units.x + units.y < most ? units.x + units.y : most;
+  TO *dw = static_cast<TO *>(a.dw) + blockIdx.y * n;
+  for (uint64_t e = ((uint64_t)blockIdx.x * kBlock + threadIdx.x) * 4; e < n; e += (uint64_t)gridDim.x * kBlock * 4) {
+    v4f s{0, 0, 0, 0};
+    for (uint32_t k = units.x; k < last; ++k) s += load4(a.ws + k * n, e, n);
+    store4<TO>(dw, e, n, s);
+  }
+}
+
+struct GroupedPlan {
+  bool big;
+  bool copied;      // dY laid out anew
+  uint32_t parts;   // of dY
+  uint32_t shift;   // log2 of a unit's tokens; 31: experts are not cut
+  uint32_t tiles_o, tiles_i;
+  uint64_t units;   // at most
+
+  bool joined() const { return shift < 31; }
+  uint64_t sums_bytes(uint32_t N, uint32_t K) const { return joined() ? (units * N * K * 4 + 15) & ~15ull : 0; }
+};
+
+GroupedPlan grouped_plan(uint64_t T, uint32_t experts, uint32_t N, uint32_t K, int dy_dtype, bool aligned) {
+  GroupedPlan p;
+  p.parts = dy_dtype == IBP_BF16 ? 1 : dy_dtype == IBP_F16 ? 2 : 3;
+  p.copied = T > 0 && (p.parts > 1 || N % 8 != 0 || !aligned);
+  const uint64_t big = (((uint64_t)N + 255) / 256) * (((uint64_t)K + 255) / 256) * experts;
+  p.big = big > 128;
+  const uint32_t wide = p.big ? 256 : 128;
+  p.tiles_o = (uint32_t)(((uint64_t)N + wide - 1) / wide);
+  p.tiles_i = (uint32_t)(((uint64_t)K + wide - 1) / wide);
+  p.shift = 31;
+  p.units = most_units(T, experts, p.shift, true);
+  return p;
+}
+
+template <int DO> hipError_t go_grouped(const MxWgradArgs &a, const GroupedPlan &p, void *dst, hipStream_t s) {
+  const dim3 grid(p.tiles_o * p.tiles_i, (uint32_t)p.units);
+  if (p.big) wgrad_kernel<true, 16, 2, 4, 8, 4, true, IBP_BF16, DO><<<grid, 512, 0, s>>>(a, dst, 1ull << p.shift, p.tiles_o, p.tiles_i, p.parts);
+  else wgrad_kernel<true, 32, 2, 2, 2, 2, true, IBP_BF16, DO><<<grid, 256, 0, s>>>(a, dst, 1ull << p.shift, p.tiles_o, p.tiles_i, p.parts);
+  return hipGetLastError();
 }
 
 }  // namespace
+
+uint64_t mx_grouped_wgrad_workspace(uint64_t T, uint32_t experts, uint32_t N, uint32_t K, int dy_dtype) {
+  // as for a dY that begins off 16 bytes, which is laid out anew whatever its rows
+  const GroupedPlan p = grouped_plan(T, experts, N, K, dy_dtype, false);
+  return p.sums_bytes(N, K) + (p.copied ? p.parts * T * padded(N) * 2 : 0);
+}
+
+hipError_t launch_mx_grouped_wgrad(const MxWgradArgs &args, hipStream_t s) {
+  MxWgradArgs a = args;
+  const GroupedPlan p = grouped_plan(a.T, a.experts, a.N, a.K, a.dy_dtype, (uintptr_t)a.dy % 16 == 0);
+  if (p.units > 65535) return hipErrorInvalidValue;
+  a.dy_pitch = a.N;
+  if (p.copied) {
+    a.dy_pitch = padded(a.N);
+    __bf16 *copy = reinterpret_cast<__bf16 *>(reinterpret_cast<uint8_t *>(a.ws) + p.sums_bytes(a.N, a.K));
+    const hipError_t e = lay_out(a, copy, p.parts, s);
+    if (e != hipSuccess) return e;
+    a.dy = copy;
+  }
+  if (p.joined()) {
+    const hipError_t e = go_grouped<IBP_F32>(a, p, a.ws, s);
+    if (e != hipSuccess) return e;
+  }
+  return with_dtype(a.dtype, [&](auto d) {
+    if (!p.joined()) return go_grouped<d.value>(a, p, a.dw, s);
+    const uint64_t n = ((uint64_t)a.N * a.K + kBlock * 4 - 1) / (kBlock * 4);
+    grouped_join_kernel<d.value><<<dim3((uint32_t)(n < 4096 ? n : 4096), a.experts), kBlock, 0, s>>>(a, 1ull << p.shift, (uint32_t)p.units);
+    return hipGetLastError();
+  });
+}
 
 uint64_t mx_wgrad_workspace(uint64_t T, uint32_t N, uint32_t K, int dy_dtype) {
   const Plan p = plan_of(T, N, K, dy_dtype, true);
@@ -406,11 +515,7 @@ hipError_t launch_mx_wgrad(const MxWgradArgs &args, hipStream_t s) {
   if (p.copied) {
     a.dy_pitch = padded(a.N);
     __bf16 *copy = reinterpret_cast<__bf16 *>(reinterpret_cast<uint8_t *>(a.ws) + p.sums_bytes(a.N, a.K));
-    const uint64_t n = (a.T * (a.dy_pitch / 8) + kBlock - 1) / kBlock;
-    const hipError_t e = with_dtype(a.dy_dtype, [&](auto d) {
-      wgrad_parts_kernel<d.value><<<(uint32_t)(n < (1u << 20) ? n : (1u << 20)), kBlock, 0, s>>>(a, copy, p.parts);
-      return hipGetLastError();
-    });
+    const hipError_t e = lay_out(a, copy, p.parts, s);
     if (e != hipSuccess) return e;
     a.dy = copy;
   }

@@ -66,8 +66,14 @@ struct MxMatmulArgs {
   uint32_t K;
   bool a_e4m3;
   int dtype;
+  // rows of A sorted by expert: expert e's are [offsets[e], offsets[e + 1]) and have rows
+  // [e N, (e + 1) N) of B; no offsets for one B that all rows share
+  const int64_t *offsets;
+  uint32_t experts;
+  uint32_t *err;                      // optional
 };
 uint64_t mx_matmul_workspace(uint64_t M, uint64_t N, uint32_t K);
+uint64_t mx_grouped_matmul_workspace(uint64_t M, uint32_t experts, uint64_t N, uint32_t K);
 
 struct MxWgradArgs {
   const void *dy;                     // T x N
@@ -79,8 +85,47 @@ struct MxWgradArgs {
   int dy_dtype;
   int dtype;
   uint32_t dy_pitch;  // set by the launch: elements from one row of dy to the next
+  const int64_t *offsets;  // tokens sorted by expert, dw of experts x N x K; or none
+  uint32_t experts;
+  uint32_t *err;           // optional
 };
 uint64_t mx_wgrad_workspace(uint64_t T, uint32_t N, uint32_t K, int dy_dtype);
+uint64_t mx_grouped_wgrad_workspace(uint64_t T, uint32_t experts, uint32_t N, uint32_t K, int dy_dtype);
+
+// 8-bit integer rows with a scale each.
+__host__ __device__ constexpr uint64_t i8_pitch(uint64_t cols) { return (cols + 15) / 16 * 16; }
+
+struct I8Args {
+  const void *in;      // pack: rows x cols
+  void *out;           // unpack: rows x cols
+  int8_t *codes;
+  float *scales;
+  uint64_t rows;
+  uint32_t cols;
+  int dtype;
+};
+
+struct I8MatmulArgs {
+  const uint8_t *a_codes, *b_codes;  // M and N rows of K
+  const float *a_scales, *b_scales;
+  void *y;                           // M x N
+  int32_t *ws;                       // split partial sums, or null
+  uint64_t M, N;
+  uint32_t K;                        // <= IBP_I8_MAX_DEPTH
+  int dtype;
+};
+uint64_t i8_matmul_workspace(uint64_t M, uint64_t N, uint32_t K);
+
+struct ExpertOrderArgs {
+  const int64_t *ids;
+  int64_t *order;
+  int64_t *offsets;    // experts + 1
+  uint32_t *counts;    // expert_order_workspace(...) bytes
+  uint32_t *err;       // optional
+  uint64_t n;          // < 2^31
+  uint32_t experts;    // <= IBP_MAX_EXPERTS
+};
+uint64_t expert_order_workspace(uint64_t n, uint32_t experts);
 
 // Launchers.  Each returns the hipError_t of its launch(es).
 hipError_t launch_lookup(const LookupArgs &a, hipStream_t s);  // ibp_embed.hip
@@ -90,6 +135,12 @@ hipError_t launch_mx_unpack(const MxArgs &a, hipStream_t s);
 hipError_t launch_mx_swiglu(const MxArgs &a, hipStream_t s);
 hipError_t launch_mx_swiglu_backward(const MxArgs &a, hipStream_t s);
 hipError_t launch_mx_matmul(const MxMatmulArgs &a, hipStream_t s);  // ibp_mx_matmul.hip
+hipError_t launch_mx_grouped_matmul(const MxMatmulArgs &a, hipStream_t s);
 hipError_t launch_mx_wgrad(const MxWgradArgs &a, hipStream_t s);    // ibp_mx_wgrad.hip
+hipError_t launch_mx_grouped_wgrad(const MxWgradArgs &a, hipStream_t s);
+hipError_t launch_i8_pack(const I8Args &a, hipStream_t s);  // ibp_i8.hip
+hipError_t launch_i8_unpack(const I8Args &a, hipStream_t s);
+hipError_t launch_i8_matmul(const I8MatmulArgs &a, hipStream_t s);  // ibp_i8_matmul.hip
+hipError_t launch_expert_order(const ExpertOrderArgs &a, hipStream_t s);  // ibp_expert.hip
 
 }  // namespace ibp

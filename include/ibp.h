@@ -454,6 +454,94 @@ IBP_API int ibp_mx_matmul(const ibp_mx_t *a, const ibp_mx_t *b, void *d_y, int d
 IBP_API int ibp_mx_linear_wgrad(const void *d_dy, int dy_dtype, uint64_t outs, const ibp_mx_t *x8, void *d_dw,
                                 int dw_dtype, void *d_workspace, uint64_t workspace_bytes, void *hip_stream);
 
+/*
+ * 8-bit integer rows.  A row of cols elements with the largest magnitude m has the scale
+ * m / 127, rounded to 32 bits, and the codes 127 x / m rounded to the nearest whole number,
+ * ties to even (the quotient itself is rounded, whatever the element type); an element
+ * reads back as its code times the scale.  A row of zeros has the scale 0; a row that holds
+ * an infinity or a NaN has codes 0 and a NaN scale, and reads back as NaN throughout.
+ *   codes:  rows x ibp_i8_codes_pitch(cols) bytes, cols filled up with zeros to a multiple
+ *           of 16; aligned to 16.
+ *   scales: rows floats.
+ * Codes (-128 too) and scales (any float) made elsewhere are taken as they are; the bytes
+ * that fill a row up have to be 0.
+ */
+typedef struct {
+  uint64_t rows;
+  uint64_t cols; /* <= IBP_MAX_COLS */
+  int8_t *codes;
+  float *scales;
+} ibp_i8_t;
+
+/* Bytes from one row of codes to the next. */
+IBP_API uint64_t ibp_i8_codes_pitch(uint64_t cols);
+
+/* Pack d_in (out->rows x out->cols of dtype) into out's codes and scales, and read a
+ * packed tensor back (values past the type's range become infinities).  Outputs and inputs
+ * may not overlap (IBP_ERR_INVALID_ARG).  Asynchronous. */
+IBP_API int ibp_i8_pack(const void *d_in, int dtype, const ibp_i8_t *out, void *hip_stream);
+IBP_API int ibp_i8_unpack(const ibp_i8_t *in, void *d_out, int dtype, void *hip_stream);
+
+/*
+ * Product of 8-bit integer rows with a scale for each token and channel:
+ * d_y[i][j] = a.scale[i] * b.scale[j] * sum over k of a.code[i][k] * b.code[j][k], a of M
+ * rows, b of N rows, a->cols == b->cols <= IBP_I8_MAX_DEPTH, d_y M x N of dtype.  The sum is
+ * exact (of whole numbers in 32 bits, which hold that many products of any codes), then
+ * rounded to a float and multiplied by the smaller scale and the larger one, so that it
+ * overflows only where the result does.  d_y may not overlap an input.  d_workspace may be
+ * NULL when the query says 0; aligned to 16.  Asynchronous.
+ */
+#define IBP_I8_MAX_DEPTH 131071u
+IBP_API uint64_t ibp_i8_matmul_workspace_bytes(uint64_t m, uint64_t n, uint64_t k);
+IBP_API int ibp_i8_matmul(const ibp_i8_t *a, const ibp_i8_t *b, void *d_y, int dtype, void *d_workspace,
+                          uint64_t workspace_bytes, void *hip_stream);
+
+/*
+ * A layer of experts: each token has rows for the experts it goes to, the rows are sorted by
+ * expert, and d_offsets (device, n_experts + 1 words) says where an expert's rows begin:
+ * expert e has rows [d_offsets[e], d_offsets[e + 1]), none where both are equal.  Offsets
+ * stay on the device; the work is laid out there.  Offsets that fall or leave the rows set
+ * IBP_DEVERR_CORRUPT: nothing outside the output is read or written then, but its rows hold
+ * anything.  n_experts from 1 to IBP_MAX_EXPERTS.
+ */
+#define IBP_MAX_EXPERTS 1024u
+
+/*
+ * Order by expert: d_order lists the positions 0..n_ids - 1 sorted by d_ids (equal ones in
+ * their order), d_offsets[e] how many ids lie below e.  Positions whose id is negative or >=
+ * n_experts come behind the last expert's, in their order, and set IBP_DEVERR_BAD_ID.
+ * n_ids < IBP_MAX_TOKENS.  d_workspace as the query says, aligned to 16 (NULL for 0).
+ * Asynchronous.
+ */
+IBP_API uint64_t ibp_expert_order_workspace_bytes(uint64_t n_ids, uint64_t n_experts);
+IBP_API int ibp_expert_order(const int64_t *d_ids, uint64_t n_ids, uint64_t n_experts, int64_t *d_order,
+                             int64_t *d_offsets, void *d_workspace, uint64_t workspace_bytes, uint32_t *d_err_word,
+                             void *hip_stream);
+
+/*
+ * Product with packed weights of experts: d_y[i][j] = sum over k of a[i][k] * b[e N + j][k],
+ * e the expert of row i, a of M rows (e4m3 or e2m1), b of n_experts * N rows (e2m1), d_y
+ * M x N of dtype.  Rows of d_y that belong to no expert (before d_offsets[0], from
+ * d_offsets[n_experts] on) are left as they were.  With weights packed along their other
+ * axis it is the gradient of the activations too.  Asynchronous.
+ */
+IBP_API uint64_t ibp_mx_grouped_matmul_workspace_bytes(uint64_t m, uint64_t n_experts, uint64_t n, uint64_t k,
+                                                       uint32_t a_format);
+IBP_API int ibp_mx_grouped_matmul(const ibp_mx_t *a, const ibp_mx_t *b, const int64_t *d_offsets, uint64_t n_experts,
+                                  void *d_y, int dtype, void *d_workspace, uint64_t workspace_bytes,
+                                  uint32_t *d_err_word, void *hip_stream);
+
+/*
+ * Weight gradients of experts from the 8-bit checkpoint of their input: d_dw[e][o][i] = sum
+ * over the rows t of expert e of d_dy[t][o] * x8[t][i], as ibp_mx_linear_wgrad; zeros for an
+ * expert without rows.  d_dw n_experts x outs x x8->cols of dw_dtype.  Asynchronous.
+ */
+IBP_API uint64_t ibp_mx_grouped_wgrad_workspace_bytes(uint64_t tokens, uint64_t n_experts, uint64_t outs, uint64_t ins,
+                                                      int dy_dtype);
+IBP_API int ibp_mx_grouped_wgrad(const void *d_dy, int dy_dtype, uint64_t outs, const ibp_mx_t *x8,
+                                 const int64_t *d_offsets, uint64_t n_experts, void *d_dw, int dw_dtype,
+                                 void *d_workspace, uint64_t workspace_bytes, uint32_t *d_err_word, void *hip_stream);
+
 #ifdef __cplusplus
 }
 #endif
