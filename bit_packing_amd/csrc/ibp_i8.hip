@@ -57,6 +57,10 @@ template <int D> __device__ __forceinline__ uint2 codes8(const F8 &x, const Code
   return make_uint2(four(q), four(q + 4));
 }
 
+// The largest float that a code of 127 times it leaves finite; the largest float over 127 is
+// rounded to the one above.
+constexpr float kMaxScale = 0x1.020406p+121f;
+
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
 // R strips a row, kept in registers; 0: any number, read twice.
@@ -117,7 +121,7 @@ __global__ __launch_bounds__(kBlock) void i8_pack_kernel(I8Args a, uint32_t lane
           put(load8<wide.value, T>(from, c, a.cols), c);
         }
       }
-      if (ok && tx == 0) a.scales[row] = fine ? amax / 127.0f : __builtin_bit_cast(float, 0x7FC00000u);
+      if (ok && tx == 0) a.scales[row] = fine ? fminf(amax / 127.0f, kMaxScale) : __builtin_bit_cast(float, 0x7FC00000u);
     }
   });
 }

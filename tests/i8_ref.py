@@ -21,7 +21,9 @@ def pack(x):
     up = (twice > m1) | ((twice == m1) & (low % 2 != 0))
     codes = np.zeros((rows, pitch(cols)), np.int8)
     codes[:, :cols] = np.where(m[:, None] > 0, low + up, 0)
-    scales = (m.astype(np.float32) / np.float32(127)).astype(np.float32)
+    scales = m.astype(np.float32) / np.float32(127)
+    with np.errstate(over="ignore"):  # the largest rows' scales are rounded down, so that 127 of them are finite
+        scales = np.where(np.isinf(scales * np.float32(127)), np.nextafter(scales, np.float32(0)), scales)
     return codes, np.where(bad, np.float32(np.nan), scales)
 
 

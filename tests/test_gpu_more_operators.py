@@ -2,7 +2,9 @@
 mx_ref).
 
 Packing, the integer product and the order are compared for equality: their definitions say
-every rounding.  The grouped products are exact where 32-bit sums are (whole multiples of a
+every rounding.  Only where a product is rounded to half precision the compiler may leave out
+the rounding to 32 bits before it (one instruction does both), so there the result is within
+half a step, and half a step of 32 bits, of the product.  The grouped products are exact where 32-bit sums are (whole multiples of a
 power of two below 2^24 steps), and otherwise off by at most half a step of the result's type
 and n 2^-24 of the terms' magnitudes for n terms.
 """
@@ -50,6 +52,19 @@ def within(got, want, bound):
     assert over.size == 0 or over.max() <= 0, f"off by {over.max()} more than allowed at {np.argmax(over)} of {over.size}"
 
 
+def check_product(y, left, right, t):
+    """y is the product of two float32 arrays, in t."""
+    with np.errstate(over="ignore", invalid="ignore"):
+        if t != "f16":
+            assert np.array_equal(host(y), rounded(left * right, t), equal_nan=True)
+            return
+        want = left.astype(np.float64) * right.astype(np.float64)
+    got, fits = host(y), np.abs(want) < 65504
+    over = np.abs(want) >= 65520
+    assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(got[over], np.sign(want[over]) * np.inf)
+    within(got[fits], want[fits], np.abs(want[fits]) * (half(t) + U) + TINY[t])
+
+
 def i8(ibp, codes, scales, cols):
     return ibp.I8Tensor(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), codes.shape[0], cols)
 
@@ -86,8 +101,7 @@ def test_i8_pack_and_unpack(ibp, t, rows, cols):
     assert np.array_equal(p.scales.cpu().numpy(), scales, equal_nan=True)
     assert np.array_equal(p.codes.cpu().numpy(), codes)
     for to in DT:
-        got = host(ibp.ibp_i8_unpack(p, dtype=DT[to]))
-        assert np.array_equal(got, rounded(i8_ref.unpack(codes, scales, cols), to), equal_nan=True), to
+        check_product(ibp.ibp_i8_unpack(p, dtype=DT[to]), codes[:, :cols].astype(np.float32), scales[:, None], to)
 
 
 @pytest.mark.parametrize("t", ["f32", "f16", "bf16"])
@@ -141,7 +155,8 @@ def test_i8_pack_takes_rows_of_any_alignment(ibp):
     assert np.array_equal(p.codes.cpu().numpy(), codes) and np.array_equal(p.scales.cpu().numpy(), scales)
     y = torch.zeros(1 + 50 * 77, dtype=torch.float16, device="cuda")
     ibp.ibp_i8_unpack(p, dtype=torch.float16, out=y[1:].view(50, 77))
-    assert y[0] == 0 and np.array_equal(host(y[1:].view(50, 77)), rounded(i8_ref.unpack(codes, scales, 77), "f16"))
+    assert y[0] == 0
+    check_product(y[1:].view(50, 77), codes[:, :77].astype(np.float32), scales[:, None], "f16")
 
 
 def test_i8_pack_past_32_bit_offsets(ibp):
@@ -177,10 +192,9 @@ def test_i8_matmul(ibp, to, m, n, k):
     # sums below 2^53 are exact in float64 products, which are quicker than integer ones
     sums = (a.astype(np.float64) @ b.T.astype(np.float64)).astype(np.int64).astype(np.float32)
     less = np.abs(sa)[:, None] < np.abs(sb)[None]
-    want = sums * np.where(less, sa[:, None], sb[None]) * np.where(less, sb[None], sa[:, None])
     y = torch.full((m, n), float("nan"), dtype=DT[to], device="cuda")
     ibp.ibp_i8_matmul(i8(ibp, a, sa, k), i8(ibp, b, sb, k), dtype=DT[to], out=y)
-    assert np.array_equal(host(y), rounded(want, to))
+    check_product(y, sums * np.where(less, sa[:, None], sb[None]), np.where(less, sb[None], sa[:, None]), to)
 
 
 @pytest.mark.parametrize("m,n", [(1, 20), (300, 200), (1100, 1100)])
