@@ -13,6 +13,9 @@ namespace dev {
 // and nothing else: vmcnt 0 (bits 3:0 and 15:14), expcnt 7 (6:4), lgkmcnt 15 (11:8).
 constexpr int kWaitVmcnt0 = 0x0F70;
 
+// The same for all but the last n vector memory loads (n < 64), and for all LDS operations.
+constexpr int wait_loads_and_lds(uint32_t n) { return (int)((n & 15) | 0x70 | (n >> 4) << 14); }
+
 // ------------------------------------------------------------------ wave helpers
 
 __device__ __forceinline__ uint32_t lane_id() { return threadIdx.x & (kWave - 1); }

@@ -80,12 +80,6 @@ template <typename TY> __device__ __forceinline__ v8b part_of(Vec8<TY> y, uint32
   }
 }
 
-// A load that the compiler knows to be of global memory: from a pointer chosen between a
-// matrix and kZeros it would make a flat load, which LDS waits count too.
-template <typename T> __device__ __forceinline__ T from_global(const uint8_t *p) {
-  return *reinterpret_cast<const __attribute__((address_space(1))) T *>((uintptr_t)p);
-}
-
 // A workgroup of WI x WO wavefronts computes F FI WI (i) by F FO WO (o) elements of dW
 // over the tokens [z * t_each, (z + 1) * t_each), z = blockIdx.y % splits, of part
 // blockIdx.y / splits of dY, into dst + blockIdx.y * N * K.

@@ -21,6 +21,12 @@ __device__ __forceinline__ void to_lds16(const uint8_t *from, uint8_t *to) {
   __builtin_amdgcn_global_load_lds((global_void *)from, (lds_void *)to, 16, 0, 0);
 }
 
+// A load that the compiler knows to be of global memory: from a pointer chosen between a
+// matrix and kZeros it would make a flat load, which LDS waits count too.
+template <typename T> __device__ __forceinline__ T from_global(const uint8_t *p) {
+  return *reinterpret_cast<const __attribute__((address_space(1))) T *>((uintptr_t)p);
+}
+
 // Tile of a workgroup among rows x cols of them.  Workgroups go to the eight XCDs in
 // turn; the tiles of one XCD lie together, in bands of kBand tile rows walked column by
 // column, so its L2 keeps the band's rows.
