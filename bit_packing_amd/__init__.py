@@ -75,7 +75,7 @@ EXPORTS = (
     "ibp_mx_linear_wgrad_workspace_bytes",
     "ibp_i8_codes_pitch", "ibp_i8_pack", "ibp_i8_unpack", "ibp_i8_matmul", "ibp_i8_matmul_workspace_bytes",
     "ibp_expert_order", "ibp_expert_order_workspace_bytes", "ibp_mx_grouped_matmul",
-    "ibp_mx_grouped_matmul_workspace_bytes", "ibp_mx_grouped_wgrad", "ibp_mx_grouped_wgrad_workspace_bytes",
+    "ibp_mx_grouped_wgrad", "ibp_mx_grouped_wgrad_workspace_bytes",
 )
 
 
@@ -282,13 +282,11 @@ def load_library() -> ctypes.CDLL:
         lib.ibp_i8_matmul_workspace_bytes.argtypes = [_u64, _u64, _u64]
         lib.ibp_expert_order.argtypes = [_vp, _u64, _u64, _vp, _vp, _vp, _u64, _vp, _vp]
         lib.ibp_expert_order_workspace_bytes.argtypes = [_u64, _u64]
-        lib.ibp_mx_grouped_matmul.argtypes = [_mxp, _mxp, _vp, _u64, _vp, _int, _vp, _u64, _vp, _vp]
-        lib.ibp_mx_grouped_matmul_workspace_bytes.argtypes = [_u64, _u64, _u64, _u64, _u32]
+        lib.ibp_mx_grouped_matmul.argtypes = [_mxp, _mxp, _vp, _u64, _vp, _int, _vp, _vp]
         lib.ibp_mx_grouped_wgrad.argtypes = [_vp, _int, _u64, _mxp, _vp, _u64, _vp, _int, _vp, _u64, _vp, _vp]
         lib.ibp_mx_grouped_wgrad_workspace_bytes.argtypes = [_u64, _u64, _u64, _u64, _int]
         for f in ("ibp_i8_codes_pitch", "ibp_i8_matmul_workspace_bytes", "ibp_expert_order_workspace_bytes",
-                  "ibp_mx_grouped_matmul_workspace_bytes", "ibp_mx_grouped_wgrad_workspace_bytes",
-                  "ibp_embedding_grad_workspace_bytes", "ibp_mx_codes_pitch", "ibp_mx_scales_pitch",
+                  "ibp_mx_grouped_wgrad_workspace_bytes", "ibp_embedding_grad_workspace_bytes", "ibp_mx_codes_pitch", "ibp_mx_scales_pitch",
                   "ibp_mx_matmul_workspace_bytes", "ibp_mx_linear_wgrad_workspace_bytes"):
             getattr(lib, f).restype = _u64
         for f in ("ibp_i8_pack", "ibp_i8_unpack", "ibp_i8_matmul", "ibp_expert_order", "ibp_mx_grouped_matmul",
@@ -882,10 +880,6 @@ def ibp_expert_order_workspace_bytes(n_ids: int, n_experts: int) -> int:
     return int(load_library().ibp_expert_order_workspace_bytes(n_ids, n_experts))
 
 
-def ibp_mx_grouped_matmul_workspace_bytes(m: int, n_experts: int, n: int, k: int, a_format: int) -> int:
-    return int(load_library().ibp_mx_grouped_matmul_workspace_bytes(m, n_experts, n, k, a_format))
-
-
 def ibp_mx_grouped_wgrad_workspace_bytes(tokens: int, n_experts: int, outs: int, ins: int, dy_dtype=torch.bfloat16) -> int:
     return int(load_library().ibp_mx_grouped_wgrad_workspace_bytes(tokens, n_experts, outs, ins, _dtype(dy_dtype)))
 
@@ -966,24 +960,21 @@ def _experts(offsets: torch.Tensor) -> int:
 
 
 def ibp_mx_grouped_matmul(a: MxTensor, b: MxTensor, offsets: torch.Tensor, dtype=torch.bfloat16,
-                          out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
-                          err: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                          out: torch.Tensor | None = None, err: torch.Tensor | None = None,
+                          stream=None) -> torch.Tensor:
     """[a.rows, b.rows / experts] product of packed rows, sorted by expert, with their expert's
     packed 4-bit weights: rows offsets[e] to offsets[e + 1] of a take the e-th part of b's
     rows.  Rows that belong to no expert are left as they were."""
     if stream is not None:
         with _stream_context(stream):
-            return ibp_mx_grouped_matmul(a, b, offsets, dtype, out, workspace, err)
+            return ibp_mx_grouped_matmul(a, b, offsets, dtype, out, err)
     n = _experts(offsets)
     if b.rows % n:
         raise ValueError("b's rows are not a multiple of the experts")
-    lib, dev = load_library(), _here(*_mx_tensors(a), *_mx_tensors(b), offsets, out, workspace, err)
+    lib, dev = load_library(), _here(*_mx_tensors(a), *_mx_tensors(b), offsets, out, err)
     out = _out(out, (a.rows, b.rows // n), dtype, dev)
-    workspace = _workspace(workspace, int(lib.ibp_mx_grouped_matmul_workspace_bytes(a.rows, n, b.rows // n, a.cols,
-                                                                                    a.format)), dev)
     rc = lib.ibp_mx_grouped_matmul(ctypes.byref(a.struct()), ctypes.byref(b.struct()), _ptr(offsets), n, _ptr(out),
-                                   _dtype(out.dtype), _ptr(workspace), 0 if workspace is None else _nbytes(workspace),
-                                   _ptr(err), _stream(None))
+                                   _dtype(out.dtype), _ptr(err), _stream(None))
     _check(rc, "ibp_mx_grouped_matmul")
     return out
 

@@ -1157,15 +1157,8 @@ IBP_API int ibp_expert_order(const int64_t *d_ids, uint64_t n_ids, uint64_t n_ex
   return status_of(launch_expert_order(a, static_cast<hipStream_t>(hip_stream)));
 }
 
-IBP_API uint64_t ibp_mx_grouped_matmul_workspace_bytes(uint64_t m, uint64_t n_experts, uint64_t n, uint64_t k,
-                                                       uint32_t a_format) {
-  if (!product_rows_ok(m) || !product_rows_ok(n) || k > IBP_MAX_COLS || a_format > IBP_MX_E2M1 || !experts_ok(n_experts)) return 0;
-  return m && n ? mx_grouped_matmul_workspace(m, (uint32_t)n_experts, n, (uint32_t)k) : 0;
-}
-
 IBP_API int ibp_mx_grouped_matmul(const ibp_mx_t *a, const ibp_mx_t *b, const int64_t *d_offsets, uint64_t n_experts,
-                                  void *d_y, int dtype, void *d_workspace, uint64_t workspace_bytes,
-                                  uint32_t *d_err_word, void *hip_stream) {
+                                  void *d_y, int dtype, uint32_t *d_err_word, void *hip_stream) {
   if (!dtype_ok(dtype)) return IBP_ERR_INVALID_ARG;
   if (const int rc = mx_check(a)) return rc;
   if (const int rc = mx_check(b)) return rc;
@@ -1177,17 +1170,14 @@ IBP_API int ibp_mx_grouped_matmul(const ibp_mx_t *a, const ibp_mx_t *b, const in
       !matrix_bytes(a->rows, N, dtype_size(dtype), &yb))
     return IBP_ERR_SIZE;
   if (yb == 0) return IBP_OK;
-  const uint64_t wb = mx_grouped_matmul_workspace(a->rows, (uint32_t)n_experts, N, (uint32_t)a->cols);
   const uint64_t ob = (n_experts + 1) * 8;
-  if (workspace_bytes < wb) return IBP_ERR_CAPACITY;
-  if (!d_y || !aligned(d_y, dtype_size(dtype)) || !d_offsets || !aligned(d_offsets, 8) || (wb && !d_workspace) ||
-      !aligned(d_workspace, 16) || !aligned(d_err_word, 4))
+  if (!d_y || !aligned(d_y, dtype_size(dtype)) || !d_offsets || !aligned(d_offsets, 8) || !aligned(d_err_word, 4))
     return IBP_ERR_INVALID_ARG;
-  if (!apart({{d_y, yb}, {d_workspace, wb}}, 0,
+  if (!apart({{d_y, yb}}, 0,
              {codes_range(a), scales_range(a), codes_range(b), scales_range(b), {d_offsets, ob}}, 0, 0))
     return IBP_ERR_INVALID_ARG;
   uint8_t *ac, *as, *bc, *bs;
-  if (!view(d_y, yb) || !mx_view(a, &ac, &as) || !mx_view(b, &bc, &bs) || !view(d_offsets, ob) || !view(d_workspace, wb) ||
+  if (!view(d_y, yb) || !mx_view(a, &ac, &as) || !mx_view(b, &bc, &bs) || !view(d_offsets, ob) ||
       !view(d_err_word, d_err_word ? 4 : 0))
     return IBP_ERR_INVALID_ARG;
   MxMatmulArgs p;
@@ -1196,7 +1186,7 @@ IBP_API int ibp_mx_grouped_matmul(const ibp_mx_t *a, const ibp_mx_t *b, const in
   p.b_codes = bc;
   p.b_scales = bs;
   p.y = d_y;
-  p.ws = static_cast<float *>(d_workspace);
+  p.ws = nullptr;
   p.M = a->rows;
   p.N = N;
   p.K = (uint32_t)a->cols;

@@ -33,18 +33,32 @@ constexpr uint32_t kStep = 16;  // blocks per step of the direct kernel: 512 ele
 // through another (4 down to 2^-10): nothing is dropped.  In one instruction a block whose
 // large products cancel, as those of an outlier column may, would lose its result: 8192 x
 // 8192 x 8192 would take 370 us so, against 742 (614 without the work of splitting).
+//
+// split takes the large elements' bytes out of four.
+__device__ __forceinline__ int split(int &x) {
+  // bytes with the bit: a selector of 12 gives 0x00, a larger one 0xFF
+  const int mask = (int)__builtin_amdgcn_perm(0u, 0u, ((uint32_t)x & 0x40404040u) | 0x0C0C0C0Cu);
+  const int high = x & mask;
+  x &= ~mask;
+  return high;
+}
+
+template <bool A8> __device__ __forceinline__ v4f mfma_one(v8i w, v8i x, v4f acc, int ws, int xs) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, acc, 4, A8 ? 0 : 4, 0, ws, 0, xs);
+}
+
 template <bool A8> __device__ __forceinline__ v4f mfma_mx(v8i w, v8i x, v4f acc, int ws, int xs) {
   if constexpr (A8) {
     v8i high;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t bit = ((uint32_t)x[i] >> 6) & 0x01010101u;
-      high[i] = x[i] & (int)((bit << 8) - bit);  // bytes with the bit
-      x[i] ^= high[i];
+      int low = x[i];
+      high[i] = split(low);
+      x[i] = low;
     }
-    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, high, acc, 4, 0, 0, ws, 0, xs);
+    acc = mfma_one<A8>(w, high, acc, ws, xs);
   }
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, acc, 4, A8 ? 0 : 4, 0, ws, 0, xs);
+  return mfma_one<A8>(w, x, acc, ws, xs);
 }
 
 __device__ __forceinline__ v8i operand(uint4 lo, uint4 hi) {
@@ -294,13 +308,41 @@ __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, voi
     __builtin_amdgcn_s_waitcnt(0x0070 | (kStages - (kLateFill ? 3 : 2)) * kLoads);
     phase_barrier();
     __builtin_amdgcn_s_setprio(1);
+    if constexpr (A8) {
+      // A fragment's successor is split between its matrix instructions, four bytes at a time,
+      // which they hide: split all at once, before them, the matrix units would wait meanwhile.
+      v8i high, next;
+      constexpr int kEach = 2 * FN / 8;  // matrix instructions for four bytes
 #pragma unroll
-    for (int m = 0; m < FM; ++m) {
+      for (int i = 0; i < 8; ++i) {
+        int low = v[0][i];
+        high[i] = split(low);
+        v[0][i] = low;
+      }
 #pragma unroll
-      for (int n = 0; n < FN; ++n) acc[n][m] = mfma_mx<A8>(w[n], v[m], acc[n][m], ws[n], xs[m]);
-      if (kLateFill && m == 0) {
-        __builtin_amdgcn_sched_barrier(0);  // the compiler would issue the loads first
-        fill(free_stage, k + kStages - 1);
+      for (int m = 0; m < FM; ++m) {
+#pragma unroll
+        for (int i = 0; i < 2 * FN; ++i) {
+          const int n = i % FN;
+          acc[n][m] = mfma_one<A8>(w[n], i < FN ? high : v[m], acc[n][m], ws[n], xs[m]);
+          if (m + 1 < FM && i % kEach == 0) {
+            int low = v[m + 1 < FM ? m + 1 : 0][i / kEach];
+            next[i / kEach] = split(low);
+            v[m + 1 < FM ? m + 1 : 0][i / kEach] = low;
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        high = next;
+      }
+    } else {
+#pragma unroll
+      for (int m = 0; m < FM; ++m) {
+#pragma unroll
+        for (int n = 0; n < FN; ++n) acc[n][m] = mfma_one<A8>(w[n], v[m], acc[n][m], ws[n], xs[m]);
+        if (kLateFill && m == 0) {
+          __builtin_amdgcn_sched_barrier(0);  // the compiler would issue the loads first
+          fill(free_stage, k + kStages - 1);
+        }
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -311,7 +353,7 @@ __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, voi
   __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);  // no load into LDS outlives the workgroup
   __syncthreads();
   static_assert(kWaves * out_bytes<TO, FN>() <= sizeof(ring), "");
-  store_fragments<TO, FM, FN>(reinterpret_cast<TO *>(ring + wave * out_bytes<TO, FN>()),
+  store_fragments<TO, FM, FN, 2, GROUPED>(reinterpret_cast<TO *>(ring + wave * out_bytes<TO, FN>()),
                               static_cast<TO *>(dst) + (uint64_t)blockIdx.y * all_m * a.N, m0 + wm, a.M, n0 + wn, a.N, lane,
                               [&](int m, int n) { return acc[n][m]; });
 }
@@ -364,10 +406,14 @@ Plan plan_of(uint64_t M, uint64_t N, uint32_t K) {
   return p;
 }
 
+// The large tile's wavefronts and fragments: few fragments of e4m3 a wavefront, as it splits each.
+struct BigTile { int wm, wn, fm, fn; };
+template <bool A8> constexpr BigTile kBigTile = A8 ? BigTile{4, 2, 4, 8} : BigTile{2, 4, 8, 4};
+
 template <bool A8, int DO> hipError_t go_tile(const MxMatmulArgs &a, const Plan &p, void *dst, hipStream_t s) {
   const dim3 grid(p.tiles_m * p.tiles_n, p.splits);
   if (p.kind == Plan::kBig)
-    mx_tile_kernel<false, A8, 2, 4, 8, 4, DO><<<grid, 512, 0, s>>>(a, dst, p.tiles_m, p.tiles_n, p.stages_each);
+    mx_tile_kernel<false, A8, kBigTile<A8>.wm, kBigTile<A8>.wn, kBigTile<A8>.fm, kBigTile<A8>.fn, DO><<<grid, 512, 0, s>>>(a, dst, p.tiles_m, p.tiles_n, p.stages_each);
   else
     mx_tile_kernel<false, A8, 2, 2, 4, 4, DO><<<grid, 256, 0, s>>>(a, dst, p.tiles_m, p.tiles_n, p.stages_each);
   return hipGetLastError();
@@ -391,30 +437,182 @@ template <bool A8> hipError_t go(const MxMatmulArgs &a, hipStream_t s) {
 
 // ------------------------------------------------------------------ rows of experts
 
-template <bool A8> hipError_t go_grouped(const MxMatmulArgs &a, hipStream_t s) {
-  const uint64_t gx = (a.N + 15) / 16, gy = most_units(a.M, a.experts, 4, false);
-  const bool big = a.M / a.experts >= 128, direct = a.M / a.experts < 24 && gy <= 65535;
-  return with_dtype(a.dtype, [&](auto d) {
-    if (direct) {
-      const uint32_t steps = (uint32_t)((mx_blocks(a.K) + kStep - 1) / kStep);
-      uint32_t waves = 4;
-      while (waves > 1 && waves > steps) waves /= 2;
-      mx_direct_kernel<true, A8, d.value><<<dim3((uint32_t)gx, (uint32_t)gy), waves * kWave, (waves - 1) * 1024, s>>>(a);
-      return hipGetLastError();
+// A few rows an expert: bound by reading the weights.  A workgroup of four wavefronts
+// computes 16 FM rows of one expert by 64 FN columns, each wavefront all rows of 16 FN columns.
+// Operands come as in the larger tiles, in a ring of STAGES stages of 128 elements; one
+// barrier a stage, at which its loads are done and all have read the stage before, whose
+// place is filled anew.  Several workgroups a CU overlap their loads and products.
+template <bool A8, int FM, int FN, int STAGES, int DO>
+__global__ __launch_bounds__(256) void mx_rows_kernel(MxMatmulArgs a, uint32_t tiles_n) {
+  using TO = typename Num<DO>::T;
+  constexpr uint32_t kWaves = 4, kPitchA = A8 ? 128 : 64, kPitchB = 64, kRowsB = 64 * FN;
+  constexpr uint32_t kLeastA = 1024 * kWaves / kPitchA;  // rows that a load of every wavefront covers
+  constexpr uint32_t kRowsA = 16 * FM < kLeastA ? kLeastA : 16 * FM;
+  using TileA = Tile<kRowsA, kPitchA, kWaves>;
+  using TileB = Tile<kRowsB, kPitchB, kWaves>;
+  constexpr uint32_t kStage = TileA::kBytes + TileB::kBytes, kLoads = TileA::kLoads + TileB::kLoads;
+  // scales of four stages, 16 bytes of each row of A, then of B
+  constexpr uint32_t kGroup = 4, kLoaders = (16 * FM + kRowsB + 63) / 64, kScales = kLoaders * 1024;
+  static_assert(STAGES - 1 <= (int)kGroup, "a stage is asked for after its scales");
+  static_assert(kLoaders <= kWaves && (STAGES - 2) * kLoads < 64, "");
+  __shared__ __align__(1024) uint8_t ring[STAGES * kStage + 2 * kScales];
+  const uint32_t lane = lane_id(), wave = uniform(threadIdx.x / kWave), r = lane & 15, g = lane >> 4;
+  const Experts x{a.offsets, a.experts, (uint32_t)__builtin_ctz(16 * FM), a.M};
+  if (a.err && blockIdx.x == 0 && wave == 0) check_offsets(x, a.err);
+  const UnitSearch<false> search(x);
+  if (blockIdx.x >= (uint64_t)search.total * tiles_n) return;
+  const TileId t = tile_of(blockIdx.x, search.total, tiles_n);
+  const Unit u = search.find(t.row);
+  if (u.row0 >= u.end) return;
+  const uint64_t m0 = u.row0, n0 = (uint64_t)t.col * kRowsB;
+  a.b_codes += u.expert * a.N * mx_code_pitch(a.K, false);
+  a.b_scales += u.expert * a.N * mx_scale_pitch(a.K);
+  const uint32_t nblk = (uint32_t)mx_blocks(a.K), sp = (uint32_t)mx_scale_pitch(a.K);
+  const uint32_t cpa = (uint32_t)mx_code_pitch(a.K, A8), cpb = (uint32_t)mx_code_pitch(a.K, false);
+  TileA ta;
+  TileB tb;
+  ta.init(a.a_codes, m0, u.end, cpa, wave, lane);
+  tb.init(a.b_codes, n0, a.N, cpb, wave, lane);
+  const uint8_t *scale;
+  {
+    const uint32_t row = wave * 64 + lane;
+    const bool of_a = row < 16 * FM;
+    const uint64_t at = of_a ? m0 + row : n0 + row - 16 * FM, rows = of_a ? u.end : a.N;
+    scale = (of_a ? a.a_scales : a.b_scales) + (at < rows ? at : rows - 1) * sp;
+  }
+  v4f acc[FN][FM];
+#pragma unroll
+  for (int n = 0; n < FN; ++n)
+#pragma unroll
+    for (int m = 0; m < FM; ++m) acc[n][m] = v4f{0, 0, 0, 0};
+  uint8_t *const scales = ring + STAGES * kStage;
+  // Always kLoads loads, of zeros past the rows' end: the waits below count on it.
+  auto fill = [&](uint8_t *st, uint32_t stage) {
+    ta.load(st, stage * kPitchA, cpa, wave);
+    tb.load(st + TileA::kBytes, stage * kPitchB, cpb, wave);
+  };
+  // as in the larger tiles
+  auto fill_scales = [&](uint8_t *sc, uint32_t q) {
+    if (wave >= kLoaders) return;
+    if ((q + 1) * 16 <= sp) {
+      to_lds16(scale + q * 16, sc + wave * 1024);
+    } else {
+      uint32_t d[kGroup];
+#pragma unroll
+      for (uint32_t j = 0; j < kGroup; ++j)
+        d[j] = q * 16 + j * 4 < sp ? *reinterpret_cast<const uint32_t *>(scale + q * 16 + j * 4) : 0u;
+      *reinterpret_cast<uint4 *>(sc + wave * 1024 + lane * 16) = make_uint4(d[0], d[1], d[2], d[3]);
     }
-    const uint32_t wide = big ? 256 : 128, stages = (uint32_t)((mx_blocks(a.K) + 3) / 4);
-    const uint64_t tiles_m = most_units(a.M, a.experts, big ? 8 : 7, false), tiles_n = (a.N + wide - 1) / wide;
-    if (tiles_m * tiles_n > 0x7FFFFF) return hipErrorInvalidValue;
-    const uint32_t grid = (uint32_t)(tiles_m * tiles_n), each = (stages + 3) / 4 * 4;
-    if (big) mx_tile_kernel<true, A8, 2, 4, 8, 4, d.value><<<grid, 512, 0, s>>>(a, a.y, 0, (uint32_t)tiles_n, each);
-    else mx_tile_kernel<true, A8, 2, 2, 4, 4, d.value><<<grid, 256, 0, s>>>(a, a.y, 0, (uint32_t)tiles_n, each);
+  };
+  const uint32_t steps = (nblk + 3) / 4, wn = wave * 16 * FN;
+  const uint32_t at_a = r * kPitchA + swizzle<kPitchA>(r, g) * 16, at_a2 = r * kPitchA + swizzle<kPitchA>(r, 4 + g) * 16;
+  const uint32_t at_b = TileA::kBytes + (wn + r) * kPitchB + swizzle<kPitchB>(r, g) * 16;
+  v8i w[FN], v[FM];
+  int ws[FN], xs[FM];
+  // What is filled is not what is read; __restrict__ says so to the compiler, which
+  // otherwise would wait for all loads in flight before an LDS read.
+  auto read = [&](uint8_t *__restrict__ filled, uint8_t *__restrict__ filled_scales, const uint8_t *__restrict__ st,
+                  const uint8_t *__restrict__ sc, uint32_t k) {
+    if (k % kGroup == 0) fill_scales(filled_scales, k / kGroup + 1);
+    fill(filled, k + STAGES - 1);
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int n = 0; n < FN; ++n) {
+      w[n] = operand(*reinterpret_cast<const uint4 *>(st + at_b + n * 16 * kPitchB), none);
+      ws[n] = sc[(16 * FM + wn + r) * 16 + g + n * 256];
+    }
+#pragma unroll
+    for (int m = 0; m < FM; ++m) {
+      v[m] = operand(*reinterpret_cast<const uint4 *>(st + at_a + m * 16 * kPitchA),
+                     A8 ? *reinterpret_cast<const uint4 *>(st + at_a2 + m * 16 * kPitchA) : none);
+      xs[m] = sc[r * 16 + g + m * 256];
+    }
+  };
+  fill_scales(scales, 0);
+#pragma unroll
+  for (uint32_t k = 0; k + 1 < STAGES; ++k) fill(ring + k * kStage, k);
+  uint32_t now = 0, next = STAGES - 1;
+#pragma unroll 1
+  for (uint32_t k = 0; k < steps; ++k) {
+    __builtin_amdgcn_s_waitcnt(wait_loads_and_lds((STAGES - 2) * kLoads));
+    phase_barrier();
+    const uint32_t odd = k / kGroup & 1;
+    read(ring + next * kStage, scales + (odd ^ 1) * kScales, ring + now * kStage, scales + odd * kScales + k % kGroup * 4, k);
+    next = now;
+    now = now + 1 == STAGES ? 0 : now + 1;
+#pragma unroll
+    for (int m = 0; m < FM; ++m)
+#pragma unroll
+      for (int n = 0; n < FN; ++n) acc[n][m] = mfma_mx<A8>(w[n], v[m], acc[n][m], ws[n], xs[m]);
+  }
+  __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);  // no load into LDS outlives the workgroup
+  TO *y = static_cast<TO *>(a.y);
+#pragma unroll
+  for (int m = 0; m < FM; ++m) {
+    const uint64_t gm = m0 + 16 * m + r;
+    if (gm >= u.end) continue;
+#pragma unroll
+    for (int n = 0; n < FN; ++n) store4<TO>(y + gm * a.N, n0 + wn + 16 * n + 4 * g, a.N, acc[n][m]);
+  }
+}
+
+template <bool A8, int FM, int STAGES> hipError_t go_rows(const MxMatmulArgs &a, hipStream_t s) {
+  constexpr uint32_t kCols = 128;
+  const uint64_t tiles_n = (a.N + kCols - 1) / kCols;
+  const uint64_t grid = most_units(a.M, a.experts, __builtin_ctz(16 * FM), false) * tiles_n;
+  if (grid > 0xFFFFFF) return hipErrorInvalidValue;
+  return with_dtype(a.dtype, [&](auto d) {
+    mx_rows_kernel<A8, FM, kCols / 64, STAGES, d.value><<<(uint32_t)grid, 256, 0, s>>>(a, (uint32_t)tiles_n);
     return hipGetLastError();
   });
 }
 
-}  // namespace
+template <bool A8> hipError_t go_grouped(const MxMatmulArgs &a, hipStream_t s) {
+  const uint64_t T = a.M, E = a.experts, units = most_units(T, E, 4, false);
+  // So little work that the direct kernel's wavefronts, which share k, are not many either (2
+  // rows of 8 experts, 4096 x 4096, e4m3 7.0 us against 14.5; 90 of 3, 2000 x 2000 6.1 and 9.1;
+  // 8 of 64, 2048 x 4096 11.1 and 15.3; 16 of 64 21.5 and 16.6; 300 of 8, 1000 x 1000 8.1 and 6.6).
+  if (units * ((a.N + 63) / 64) <= 256) {
+    const uint32_t steps = (uint32_t)((mx_blocks(a.K) + kStep - 1) / kStep);
+    uint32_t waves = 4;
+    while (waves > 1 && waves > steps) waves /= 2;
+    return with_dtype(a.dtype, [&](auto d) {
+      mx_direct_kernel<true, A8, d.value><<<dim3((uint32_t)((a.N + 15) / 16), (uint32_t)units), waves * kWave, (waves - 1) * 1024, s>>>(a);
+      return hipGetLastError();
+    });
+  }
+  // The rest goes by the rows an expert has on average, as their number is all that the host
+  // knows, and by the tiles that they make, half a tile more an expert.  256 x 256 tiles (32
+  // experts, 2048 x 4096, ragged, e4m3): 8192 rows 149 us, with 128 x 128 tiles 152, evenly
+  // spread 86 and 109; 4096 rows 146 and 101; 4096 rows of 4 experts, 4096 x 4096 (288 tiles) 147
+  // and 143.  128 x 128: 4096 rows 101, with 64 rows by 128 columns 108, of e2m1 49 and 59; 2048
+  // rows 90 and 62, 45 and 40; 800 rows of 4 experts, 4096 x 2048 (256 tiles) 24.0 and 24.0, 2000
+  // of 8, 500 x 500 (80 tiles) 10.4 and 7.7.
+  auto tiles = [&](uint64_t wide) { return (T / wide + E / 2) * ((a.N + wide - 1) / wide); };
+  const bool big = T >= 192 * E && tiles(256) >= 384, middle = T >= 112 * E && tiles(128) >= 256;
+  if (big || middle) {
+    const uint32_t wide = big ? 256 : 128, each = (uint32_t)((mx_blocks(a.K) + 15) / 16 * 4);
+    const uint64_t tiles_n = (a.N + wide - 1) / wide, grid = most_units(T, E, big ? 8 : 7, false) * tiles_n;
+    if (grid > 0x7FFFFF) return hipErrorInvalidValue;
+    return with_dtype(a.dtype, [&](auto d) {
+      if (big) mx_tile_kernel<true, A8, kBigTile<A8>.wm, kBigTile<A8>.wn, kBigTile<A8>.fm, kBigTile<A8>.fn, d.value><<<(uint32_t)grid, 512, 0, s>>>(a, a.y, 0, (uint32_t)tiles_n, each);
+      else mx_tile_kernel<true, A8, 2, 2, 4, 4, d.value><<<(uint32_t)grid, 256, 0, s>>>(a, a.y, 0, (uint32_t)tiles_n, each);
+      return hipGetLastError();
+    });
+  }
+  // Fewer rows a tile read and split fewer codes for nothing, more read the weights less often
+  // (32 ragged experts, 2048 x 4096; tiles of 16, 32 and 64 rows; e4m3: 512 rows 34, 41, 43 us,
+  // 1024 rows 55, 41, 60, 2048 rows 79, 70, 62; e2m1: 512 rows 32.5, 32.2, 31.1, 2048 rows 72, 51,
+  // 40; 64 rows of 64 experts 32.3, 32.3, 35.2).
+  if constexpr (A8) {
+    if (T <= 16 * E) return go_rows<true, 1, 5>(a, s);
+    return T <= 48 * E ? go_rows<true, 2, 5>(a, s) : go_rows<true, 4, 4>(a, s);
+  } else {
+    return T < 8 * E ? go_rows<false, 2, 5>(a, s) : go_rows<false, 4, 4>(a, s);
+  }
+}
 
-uint64_t mx_grouped_matmul_workspace(uint64_t, uint32_t, uint64_t, uint32_t) { return 0; }
+}  // namespace
 
 hipError_t launch_mx_grouped_matmul(const MxMatmulArgs &a, hipStream_t s) {
   return a.a_e4m3 ? go_grouped<true>(a, s) : go_grouped<false>(a, s);

@@ -293,18 +293,26 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
     __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);  // no load into LDS outlives the workgroup, or this part
     if (GROUPED && p + 1 < parts) phase_barrier();  // every wavefront's
   }
-  // a lane has once or four times four consecutive i of one o
   TO *dw = static_cast<TO *>(dst) + (uint64_t)blockIdx.y * a.N * a.K;
+  if constexpr (F == 16) {
+    constexpr int kAt = sizeof(TO) == 2 ? 2 : 1;
+    static_assert(kWaves * out_bytes<TO, FI, kAt>() <= sizeof(ring), "");
+    __syncthreads();  // all have read the last stage
+    store_fragments<TO, FO, FI, kAt, GROUPED>(reinterpret_cast<TO *>(ring + wave * out_bytes<TO, FI, kAt>()), dw, o0 + wo * 16, a.N,
+                                     i0 + wi * 16, a.K, lane, [&](int y, int x) { return acc[x][y]; });
+  } else {
+    // four times four consecutive i of one o
 #pragma unroll
-  for (int y = 0; y < FO; ++y) {
-    const uint32_t o = o0 + (wo + y) * F + lane % F;
-    if (o >= a.N) continue;
+    for (int y = 0; y < FO; ++y) {
+      const uint32_t o = o0 + (wo + y) * F + lane % F;
+      if (o >= a.N) continue;
 #pragma unroll
-    for (int x = 0; x < FI; ++x) {
+      for (int x = 0; x < FI; ++x) {
 #pragma unroll
-      for (int q = 0; q < F * F / 256; ++q)
-        store4<TO>(dw + (uint64_t)o * a.K, i0 + (wi + x) * F + 8 * q + 4 * (lane / F), a.K,
-                   v4f{acc[x][y][4 * q], acc[x][y][4 * q + 1], acc[x][y][4 * q + 2], acc[x][y][4 * q + 3]});
+        for (int q = 0; q < F * F / 256; ++q)
+          store4<TO>(dw + (uint64_t)o * a.K, i0 + (wi + x) * F + 8 * q + 4 * (lane / F), a.K,
+                     v4f{acc[x][y][4 * q], acc[x][y][4 * q + 1], acc[x][y][4 * q + 2], acc[x][y][4 * q + 3]});
+      }
     }
   }
 }

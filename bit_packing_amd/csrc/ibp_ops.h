@@ -73,7 +73,6 @@ struct MxMatmulArgs {
   uint32_t *err;                      // optional
 };
 uint64_t mx_matmul_workspace(uint64_t M, uint64_t N, uint32_t K);
-uint64_t mx_grouped_matmul_workspace(uint64_t M, uint32_t experts, uint64_t N, uint32_t K);
 
 struct MxWgradArgs {
   const void *dy;                     // T x N

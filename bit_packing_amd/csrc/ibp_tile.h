@@ -89,23 +89,25 @@ __device__ __forceinline__ void phase_barrier() {
 
 // A wavefront's FM x FN fragments, value(m, n) being four consecutive columns of a lane's row
 // of fragment (m, n), into y from row0 and col0 on, rows and columns below their ends.  They
-// go through LDS (`out`, the wavefront's own), two fragments' rows at a time, so that a store
-// covers whole lines of y (from the fragments themselves a row gets 32 bytes at a time).
-constexpr uint32_t kOutRows = 32;
-template <typename TO, int FN> constexpr uint32_t out_bytes() { return kOutRows * (16 * FN * sizeof(TO) + 16); }
-template <typename TO, int FM, int FN, typename F>
+// go through LDS (`out`, the wavefront's own), AT fragments' rows at a time, so that a store
+// covers whole lines of y (from the fragments themselves a row gets 32 bytes at a time).  STREAM:
+// past the caches, which large results would empty of operands (the weight gradients of 32
+// experts, 2048 x 4096, 537 MB: of 32768 tokens 642 us without, 606 with; of 8192 304 and 245;
+// the product of 32768 rows, 134 MB, 403 and 394; that of 8-bit integers, 134 MB, 235 and 239).
+template <typename TO, int FN, int AT = 2> constexpr uint32_t out_bytes() { return AT * 16 * (16 * FN * sizeof(TO) + 16); }
+template <typename TO, int FM, int FN, int AT = 2, bool STREAM = false, typename F>
 __device__ __forceinline__ void store_fragments(TO *out, TO *y, uint64_t row0, uint64_t rows, uint64_t col0,
                                                 uint64_t cols, uint32_t lane, F &&value) {
-  constexpr uint32_t kCols = 16 * FN, kPad = 16 / sizeof(TO), kEach = 16 / sizeof(TO), kPieces = kOutRows * kCols / kEach / 64;
+  constexpr uint32_t kCols = 16 * FN, kPad = 16 / sizeof(TO), kEach = 16 / sizeof(TO), kPieces = AT * 16 * kCols / kEach / 64;
   typedef TO Aligned __attribute__((ext_vector_type(kEach)));
   typedef TO Loose __attribute__((ext_vector_type(kEach), aligned(sizeof(TO))));
   typedef TO Four __attribute__((ext_vector_type(4)));
   const uint32_t r = lane & 15, g = lane >> 4;
 #pragma unroll
-  for (int m = 0; m < FM; m += 2) {
+  for (int m = 0; m < FM; m += AT) {
     wave_lds_sync();
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < AT; ++h)
 #pragma unroll
       for (int n = 0; n < FN; ++n) {
         const v4f x = value(m + h, n);
@@ -119,7 +121,8 @@ __device__ __forceinline__ void store_fragments(TO *out, TO *y, uint64_t row0, u
       if (gm >= rows || gn >= cols) continue;
       const Aligned x = *reinterpret_cast<const Aligned *>(out + row * (kCols + kPad) + c);
       if (gn + kEach <= cols) {
-        *reinterpret_cast<Loose *>(y + gm * cols + gn) = x;
+        if constexpr (STREAM) __builtin_nontemporal_store((Loose)x, reinterpret_cast<Loose *>(y + gm * cols + gn));
+        else *reinterpret_cast<Loose *>(y + gm * cols + gn) = x;
       } else {
 #pragma unroll
         for (uint32_t e = 0; e < kEach; ++e)

@@ -525,11 +525,8 @@ IBP_API int ibp_expert_order(const int64_t *d_ids, uint64_t n_ids, uint64_t n_ex
  * d_offsets[n_experts] on) are left as they were.  With weights packed along their other
  * axis it is the gradient of the activations too.  Asynchronous.
  */
-IBP_API uint64_t ibp_mx_grouped_matmul_workspace_bytes(uint64_t m, uint64_t n_experts, uint64_t n, uint64_t k,
-                                                       uint32_t a_format);
 IBP_API int ibp_mx_grouped_matmul(const ibp_mx_t *a, const ibp_mx_t *b, const int64_t *d_offsets, uint64_t n_experts,
-                                  void *d_y, int dtype, void *d_workspace, uint64_t workspace_bytes,
-                                  uint32_t *d_err_word, void *hip_stream);
+                                  void *d_y, int dtype, uint32_t *d_err_word, void *hip_stream);
 
 /*
  * Weight gradients of experts from the 8-bit checkpoint of their input: d_dw[e][o][i] = sum

@@ -288,7 +288,9 @@ def offsets_of(rng, rows, experts, how):
 GROUPED = [(1, 1, 1, 1, "even"), (1, 3, 16, 32, "one"), (5, 8, 33, 31, "ragged"), (16, 4, 17, 129, "even"), (17, 2, 100, 512, "one"),
            (64, 64, 70, 700, "ragged"), (64, 300, 40, 96, "ragged"), (100, 1024, 9, 64, "ragged"), (300, 5, 129, 640, "ragged"),
            (700, 9, 200, 333, "ragged"), (1000, 3, 300, 288, "even"), (1500, 2, 256, 1056, "one"), (3000, 4, 520, 160, "ragged"),
-           (2500, 20, 260, 545, "even"), (5000, 7, 500, 256, "ragged"), (600, 1, 257, 2080, "even")]
+           (2500, 20, 260, 545, "even"), (5000, 7, 500, 256, "ragged"), (600, 1, 257, 2080, "even"),
+           (200, 100, 201, 320, "ragged"), (300, 10, 700, 160, "ragged"), (900, 20, 333, 2080, "ragged"), (130, 17, 2000, 96, "one"),
+           (2100, 6, 1700, 160, "ragged"), (2200, 8, 2001, 545, "even"), (6500, 8, 3600, 96, "ragged"), (6600, 20, 3501, 160, "even")]
 
 
 @pytest.mark.parametrize("fmt", [mx_ref.E4M3, mx_ref.E2M1])

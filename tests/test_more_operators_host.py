@@ -48,8 +48,6 @@ def test_queries(ibp):
     assert ibp.ibp_expert_order_workspace_bytes(1 << 20, 64) > 0
     assert ibp.ibp_expert_order_workspace_bytes(ibp.IBP_MAX_TOKENS, 64) == 0
     assert ibp.ibp_expert_order_workspace_bytes(1 << 20, ibp.IBP_MAX_EXPERTS + 1) == 0
-    assert ibp.ibp_mx_grouped_matmul_workspace_bytes(10, 0, 10, 32, 0) == 0
-    assert ibp.ibp_mx_grouped_matmul_workspace_bytes(10, 2, 10, 32, 7) == 0
     assert ibp.ibp_mx_grouped_wgrad_workspace_bytes(10, 0, 8, 32) == 0
     assert ibp.ibp_mx_grouped_wgrad_workspace_bytes(10, 2, 8, 32, torch.float32) >= 3 * 10 * 8 * 2
 
@@ -123,15 +121,15 @@ def test_order_refusals(ibp):
 def test_grouped_refusals(ibp):
     lib = ibp.load_library()
     a, b, no = mx(ibp), mx(ibp, fmt=1, rows=24, codes=3 * FAKE, scales=4 * FAKE), ibp.IBP_ERR_INVALID_ARG
-    call = lambda a=a, b=b, off=5 * FAKE, n=8, y=FAR, t=F32, w=None, wb=0, err=None: lib.ibp_mx_grouped_matmul(  # noqa: E731
-        ref(a), ref(b), off, n, y, t, w, wb, err, None)
+    call = lambda a=a, b=b, off=5 * FAKE, n=8, y=FAR, t=F32, err=None: lib.ibp_mx_grouped_matmul(  # noqa: E731
+        ref(a), ref(b), off, n, y, t, err, None)
     assert call(t=7) == no and call(b=mx(ibp, rows=24)) == no and call(a=mx(ibp, reserved=1)) == no
     assert call(n=0) == ibp.IBP_ERR_SIZE and call(n=ibp.IBP_MAX_EXPERTS + 1) == ibp.IBP_ERR_SIZE
     assert call(n=7) == ibp.IBP_ERR_SIZE  # 24 rows of weights
     assert call(a=mx(ibp, cols=65)) == ibp.IBP_ERR_SIZE
     assert call(a=mx(ibp, rows=(1 << 30) + 1)) == ibp.IBP_ERR_SIZE
     assert call(off=None) == no and call(off=FAKE + 4) == no and call(y=None) == no and call(y=FAR + 2) == no
-    assert call(err=FAKE + 2) == no and call(w=FAKE + 8) == no
+    assert call(err=FAKE + 2) == no
     assert call(y=FAKE) == no and call(y=5 * FAKE) == no  # over the rows, over the offsets
     assert call(a=mx(ibp, rows=0)) == ibp.IBP_OK and call(b=mx(ibp, fmt=1, rows=0)) == ibp.IBP_OK
 
