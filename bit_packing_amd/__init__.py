@@ -155,25 +155,45 @@ class MxTensor:
 class I8Tensor:
     """A tensor of rows x cols elements in 8-bit integers: int8 codes [rows,
     ibp_i8_codes_pitch] and float32 scales [rows] on the device."""
-    __slots__ = ("rows", "cols", "codes", "scales")
+    __slots__ = ("rows", "cols", "_codes", "_scales", "_both")
 
-    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int):
-        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
+    def __init__(self, codes: torch.Tensor | None, scales: torch.Tensor | None, rows: int, cols: int,
+                 both: torch.Tensor | None = None):
+        # tensors made here share one allocation, scales behind the codes, as an MxTensor's
+        self.rows, self.cols, self._codes, self._scales, self._both = rows, cols, codes, scales, both
 
     def __repr__(self):
         return f"I8Tensor({self.rows} x {self.cols})"
 
     @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            pitch = _i8_pitch(self.cols)
+            self._codes = self._both[: self.rows * pitch].view(self.rows, pitch)
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            self._scales = self._both[self.rows * _i8_pitch(self.cols):].view(torch.float32)
+        return self._scales
+
+    @property
     def device(self) -> torch.device:
-        return _device(self.codes)
+        return _device(self._both if self._both is not None else self._codes)
 
     def struct(self) -> ibp_i8_t:
+        rows, cols = self.rows, self.cols
+        codes = rows * _i8_pitch(cols)
+        if self._both is not None:
+            at = self._both.data_ptr()
+            return ibp_i8_t(rows, cols, at, at + codes)
         # the C side sees pointers only: the tensors must hold what the shape says
-        if self.codes.dtype != torch.int8 or self.scales.dtype != torch.float32:
+        if self._codes.dtype != torch.int8 or self._scales.dtype != torch.float32:
             raise ValueError("codes are int8, scales float32")
-        if self.codes.numel() < self.rows * _i8_pitch(self.cols) or self.scales.numel() < self.rows:
+        if self._codes.numel() < codes or self._scales.numel() < rows:
             raise ValueError("codes or scales are smaller than their shape needs")
-        return ibp_i8_t(self.rows, self.cols, _ptr(self.codes), _ptr(self.scales))
+        return ibp_i8_t(rows, cols, _ptr(self._codes), _ptr(self._scales))
 
 
 def _i8_pitch(cols: int) -> int:
@@ -848,23 +868,17 @@ def ibp_mx_linear_wgrad(dy: torch.Tensor, x8: MxTensor, dw_dtype=None, dw: torch
 
 
 def _here(*tensors) -> torch.device:
-    """The device of the tensors that are on one, which has to be the current one: a call
-    runs on the current device's stream."""
-    dev = None
+    """The current device, on which a call runs, after a check that the tensors that are on a
+    device are on it."""
+    now = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and t.is_cuda:
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError("the tensors are on different devices")
-    if dev is None:
-        return _device()
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {dev}, not on the current device")
-    return dev
+        if t is not None and t.get_device() not in (now, -1):
+            raise ValueError(f"a tensor is on {t.device}, not on the current device {now}")
+    return torch.device("cuda", now)
 
 
-def _mx_tensors(m: MxTensor):
+def _parts(m) -> tuple:
+    """The tensors that hold an MxTensor or I8Tensor."""
     return (m._both,) if m._both is not None else (m._codes, m._scales)
 
 
@@ -886,8 +900,7 @@ def ibp_mx_grouped_wgrad_workspace_bytes(tokens: int, n_experts: int, outs: int,
 
 def make_i8(rows: int, cols: int, device) -> I8Tensor:
     """An I8Tensor of unwritten codes and scales."""
-    return I8Tensor(torch.empty(rows, _i8_pitch(cols), dtype=torch.int8, device=device),
-                    torch.empty(rows, dtype=torch.float32, device=device), rows, cols)
+    return I8Tensor(None, None, rows, cols, torch.empty(rows * (_i8_pitch(cols) + 4), dtype=torch.int8, device=device))
 
 
 def ibp_i8_pack(x: torch.Tensor, out: I8Tensor | None = None, stream=None) -> I8Tensor:
@@ -902,7 +915,7 @@ def ibp_i8_pack(x: torch.Tensor, out: I8Tensor | None = None, stream=None) -> I8
     elif (out.rows, out.cols) != (rows, cols):
         raise ValueError("the packed output has another shape")
     else:
-        _here(x, out.codes, out.scales)
+        _here(x, *_parts(out))
     _check(load_library().ibp_i8_pack(_ptr(x), dtype, ctypes.byref(out.struct()), _stream(None)), "ibp_i8_pack")
     return out
 
@@ -912,7 +925,7 @@ def ibp_i8_unpack(t: I8Tensor, dtype=torch.bfloat16, out: torch.Tensor | None = 
     if stream is not None:
         with _stream_context(stream):
             return ibp_i8_unpack(t, dtype, out)
-    out = _out(out, (t.rows, t.cols), dtype, _here(t.codes, t.scales, out))
+    out = _out(out, (t.rows, t.cols), dtype, _here(*_parts(t), out))
     _check(load_library().ibp_i8_unpack(ctypes.byref(t.struct()), _ptr(out), _dtype(out.dtype), _stream(None)),
            "ibp_i8_unpack")
     return out
@@ -925,7 +938,7 @@ def ibp_i8_matmul(a: I8Tensor, b: I8Tensor, dtype=torch.bfloat16, out: torch.Ten
     if stream is not None:
         with _stream_context(stream):
             return ibp_i8_matmul(a, b, dtype, out, workspace)
-    lib, dev = load_library(), _here(a.codes, a.scales, b.codes, b.scales, out, workspace)
+    lib, dev = load_library(), _here(*_parts(a), *_parts(b), out, workspace)
     out = _out(out, (a.rows, b.rows), dtype, dev)
     workspace = _workspace(workspace, int(lib.ibp_i8_matmul_workspace_bytes(a.rows, b.rows, a.cols)), dev)
     rc = lib.ibp_i8_matmul(ctypes.byref(a.struct()), ctypes.byref(b.struct()), _ptr(out), _dtype(out.dtype),
@@ -971,7 +984,7 @@ def ibp_mx_grouped_matmul(a: MxTensor, b: MxTensor, offsets: torch.Tensor, dtype
     n = _experts(offsets)
     if b.rows % n:
         raise ValueError("b's rows are not a multiple of the experts")
-    lib, dev = load_library(), _here(*_mx_tensors(a), *_mx_tensors(b), offsets, out, err)
+    lib, dev = load_library(), _here(*_parts(a), *_parts(b), offsets, out, err)
     out = _out(out, (a.rows, b.rows // n), dtype, dev)
     rc = lib.ibp_mx_grouped_matmul(ctypes.byref(a.struct()), ctypes.byref(b.struct()), _ptr(offsets), n, _ptr(out),
                                    _dtype(out.dtype), _ptr(err), _stream(None))
@@ -991,7 +1004,7 @@ def ibp_mx_grouped_wgrad(dy: torch.Tensor, x8: MxTensor, offsets: torch.Tensor, 
     if dy.dim() != 2 or dy.shape[0] != x8.rows:
         raise ValueError("dy is [x8.rows, outs]")
     n, outs = _experts(offsets), dy.shape[1]
-    lib, dev = load_library(), _here(dy, *_mx_tensors(x8), offsets, dw, workspace, err)
+    lib, dev = load_library(), _here(dy, *_parts(x8), offsets, dw, workspace, err)
     dw = _out(dw, (n, outs, x8.cols), dw_dtype or (dy.dtype if dw is None else dw.dtype), dev)
     need = int(lib.ibp_mx_grouped_wgrad_workspace_bytes(x8.rows, n, outs, x8.cols, _dtype(dy.dtype)))
     workspace = _workspace(workspace, need, dev)
