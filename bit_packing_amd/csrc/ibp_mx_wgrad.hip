@@ -100,11 +100,12 @@ template <typename TY> __device__ __forceinline__ v8b part_of(Vec8<TY> y, uint32
 //
 // GROUPED: the tokens are sorted by expert, and blockIdx.y counts units of tokens of one expert,
 // as many as there can be, of which an expert without tokens has one; dst is that expert's or,
-// where experts are cut into units, the unit's.  All parts of dY are summed by one workgroup.
-template <bool GROUPED, int F, int WI, int WO, int FI, int FO, bool DIRECT, int DY, int DO>
+// where experts are cut into units, the unit's.  All parts of dY are summed by one workgroup,
+// one after another (PARTED; the loop about them takes more registers than there are).
+template <bool GROUPED, bool PARTED, int F, int WI, int WO, int FI, int FO, bool DIRECT, int DY, int DO>
 __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *dst, uint64_t t_each, uint32_t tiles_o,
                                                            uint32_t tiles_i, uint32_t splits) {
-  static_assert(!GROUPED || DIRECT, "");
+  static_assert((!GROUPED || DIRECT) && (GROUPED || !PARTED), "");
   using TY = typename Num<DY>::T;
   static_assert(!DIRECT || DY == IBP_BF16, "");
   using TO = typename Num<DO>::T;
@@ -267,9 +268,9 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
     __builtin_amdgcn_s_setprio(0);
     phase_barrier();
   };
-  const uint32_t parts = GROUPED ? splits : part + 1;
-#pragma unroll 1
-  for (uint32_t p = part; p < parts; ++p) {
+  const uint32_t parts = PARTED ? splits : part + 1;
+  uint32_t p = part;
+  do {
     begin(p);
     if (steps) {
 #pragma unroll
@@ -291,8 +292,8 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
     }
     if (kPingPong && !behind) phase_barrier();
     __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);  // no load into LDS outlives the workgroup, or this part
-    if (GROUPED && p + 1 < parts) phase_barrier();  // every wavefront's
-  }
+    if (PARTED && p + 1 < parts) phase_barrier();  // every wavefront's
+  } while (PARTED && ++p < parts);
   TO *dw = static_cast<TO *>(dst) + (uint64_t)blockIdx.y * a.N * a.K;
   if constexpr (F == 16) {
     constexpr int kAt = sizeof(TO) == 2 ? 2 : 1;
@@ -413,13 +414,13 @@ template <int DO> hipError_t go(const MxWgradArgs &a, const Plan &p, void *dst, 
     kernel<<<grid, threads, 0, s>>>(a, dst, p.t_each, p.tiles_o, p.tiles_i, p.splits);
     return hipGetLastError();
   };
-  if (p.big) return launch(wgrad_kernel<false, 16, 2, 4, 8, 4, true, IBP_BF16, DO>, 512);
+  if (p.big) return launch(wgrad_kernel<false, false, 16, 2, 4, 8, 4, true, IBP_BF16, DO>, 512);
   if constexpr (DO == IBP_F32) {  // parts are always joined
-    if (a.dy_dtype == IBP_F16) return launch(wgrad_kernel<false, 32, 2, 2, 2, 2, false, IBP_F16, DO>, 256);
-    if (a.dy_dtype == IBP_F32) return launch(wgrad_kernel<false, 32, 2, 2, 2, 2, false, IBP_F32, DO>, 256);
+    if (a.dy_dtype == IBP_F16) return launch(wgrad_kernel<false, false, 32, 2, 2, 2, 2, false, IBP_F16, DO>, 256);
+    if (a.dy_dtype == IBP_F32) return launch(wgrad_kernel<false, false, 32, 2, 2, 2, 2, false, IBP_F32, DO>, 256);
   }
-  return a.N % 8 == 0 && (uintptr_t)a.dy % 16 == 0 ? launch(wgrad_kernel<false, 32, 2, 2, 2, 2, true, IBP_BF16, DO>, 256)
-                                                   : launch(wgrad_kernel<false, 32, 2, 2, 2, 2, false, IBP_BF16, DO>, 256);
+  return a.N % 8 == 0 && (uintptr_t)a.dy % 16 == 0 ? launch(wgrad_kernel<false, false, 32, 2, 2, 2, 2, true, IBP_BF16, DO>, 256)
+                                                   : launch(wgrad_kernel<false, false, 32, 2, 2, 2, 2, false, IBP_BF16, DO>, 256);
 }
 
 // ------------------------------------------------------------------ tokens of experts
@@ -451,6 +452,14 @@ struct GroupedPlan {
   uint64_t sums_bytes(uint32_t N, uint32_t K) const { return joined() ? (units * N * K * 4 + 15) & ~15ull : 0; }
 };
 
+// Tiles by their number, as without experts (256 x 256 against 128 x 128; 32 ragged experts, 2048
+// x 4096: 32768 tokens 606 us and 877; 24 of 500 x 1000 (192 large tiles), 1501 tokens 19.1 and
+// 22.9; 8 of 1024 x 1024 (128), 16384 tokens 134 and 71, 4000 tokens 25.7 and 22.2).
+// Where there are fewer small tiles than CUs, an expert's tokens are cut into units whose sums
+// another launch adds, as long as leave a tile for each CU, from 512 tokens to 8192 (8 experts
+// of 512 x 512, 16384 tokens: whole 61 us, units of 2048 tokens 43.5, 1024 36.7, 512 38.3; 4 of 256
+// x 512, 32768 tokens: 179, 1024 37.0, 512 44.9; 16 of 256 x 300, 30000 tokens: 75, 1024 29.1,
+// 512 28.4; 8 of 256 x 256, 2000 tokens: 13.4, 256 13.9).
 GroupedPlan grouped_plan(uint64_t T, uint32_t experts, uint32_t N, uint32_t K, int dy_dtype, bool aligned) {
   GroupedPlan p;
   p.parts = dy_dtype == IBP_BF16 ? 1 : dy_dtype == IBP_F16 ? 2 : 3;
@@ -460,16 +469,27 @@ GroupedPlan grouped_plan(uint64_t T, uint32_t experts, uint32_t N, uint32_t K, i
   const uint32_t wide = p.big ? 256 : 128;
   p.tiles_o = (uint32_t)(((uint64_t)N + wide - 1) / wide);
   p.tiles_i = (uint32_t)(((uint64_t)K + wide - 1) / wide);
+  const uint64_t tiles = (uint64_t)p.tiles_o * p.tiles_i;
   p.shift = 31;
+  if (tiles * experts < 256) {
+    uint32_t shift = T >> 13 < 1u << 15 ? 13 : 16;  // the grid holds 65535 units
+    while (shift > 9 && ((T >> shift) + experts / 2) * tiles < 256) --shift;
+    if (T / experts >= 1u << shift) p.shift = shift;
+  }
   p.units = most_units(T, experts, p.shift, true);
   return p;
 }
 
 template <int DO> hipError_t go_grouped(const MxWgradArgs &a, const GroupedPlan &p, void *dst, hipStream_t s) {
   const dim3 grid(p.tiles_o * p.tiles_i, (uint32_t)p.units);
-  if (p.big) wgrad_kernel<true, 16, 2, 4, 8, 4, true, IBP_BF16, DO><<<grid, 512, 0, s>>>(a, dst, 1ull << p.shift, p.tiles_o, p.tiles_i, p.parts);
-  else wgrad_kernel<true, 32, 2, 2, 2, 2, true, IBP_BF16, DO><<<grid, 256, 0, s>>>(a, dst, 1ull << p.shift, p.tiles_o, p.tiles_i, p.parts);
-  return hipGetLastError();
+  auto launch = [&](auto kernel, uint32_t threads) {
+    kernel<<<grid, threads, 0, s>>>(a, dst, 1ull << p.shift, p.tiles_o, p.tiles_i, p.parts);
+    return hipGetLastError();
+  };
+  if (p.big) return p.parts == 1 ? launch(wgrad_kernel<true, false, 16, 2, 4, 8, 4, true, IBP_BF16, DO>, 512)
+                                 : launch(wgrad_kernel<true, true, 16, 2, 4, 8, 4, true, IBP_BF16, DO>, 512);
+  return p.parts == 1 ? launch(wgrad_kernel<true, false, 32, 2, 2, 2, 2, true, IBP_BF16, DO>, 256)
+                      : launch(wgrad_kernel<true, true, 32, 2, 2, 2, 2, true, IBP_BF16, DO>, 256);
 }
 
 }  // namespace
