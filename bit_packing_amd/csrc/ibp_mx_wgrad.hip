@@ -101,7 +101,7 @@ template <typename TY> __device__ __forceinline__ v8b part_of(Vec8<TY> y, uint32
 // GROUPED: the tokens are sorted by expert, and blockIdx.y counts units of tokens of one expert,
 // as many as there can be, of which an expert without tokens has one; dst is that expert's or,
 // where experts are cut into units, the unit's.  All parts of dY are summed by one workgroup,
-// one after another (PARTED; the loop about them takes more registers than there are).
+// one after another (PARTED).
 template <bool GROUPED, bool PARTED, int F, int WI, int WO, int FI, int FO, bool DIRECT, int DY, int DO>
 __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *dst, uint64_t t_each, uint32_t tiles_o,
                                                            uint32_t tiles_i, uint32_t splits) {
@@ -147,13 +147,10 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
   // without DIRECT a piece past the row's end is the row's last eight elements (load8)
   const bool wide = a.N >= 8;
   const uint64_t at_y = DIRECT ? cy : (wide ? (cy + 8 <= a.N ? cy : a.N - 8) : 0);
-  const uint8_t *py, *px, *ps;  // ps: its scales' dword
-  auto begin = [&](uint32_t part) {
-    const uint64_t row_y = t0 + ty + (DIRECT ? part * a.T : 0);
-    py = in_y ? reinterpret_cast<const uint8_t *>(dy + row_y * a.dy_pitch + at_y) : kZeros;
-    px = in_x ? a.x_codes + (t0 + tx) * cp + cx : kZeros;
-    ps = in_x ? a.x_scales + (t0 + tx) * sp + cx / (4 * kMxBlock) * 4 : kZeros;
-  };
+  const uint64_t row_y = t0 + ty + (DIRECT ? part * a.T : 0);
+  const uint8_t *py = in_y ? reinterpret_cast<const uint8_t *>(dy + row_y * a.dy_pitch + at_y) : kZeros;
+  const uint8_t *px = in_x ? a.x_codes + (t0 + tx) * cp + cx : kZeros;
+  const uint8_t *ps = in_x ? a.x_scales + (t0 + tx) * sp + cx / (4 * kMxBlock) * 4 : kZeros;  // its dword
   const uint32_t scale_shift = cx / kMxBlock % 4 * 8;
   const uint64_t go_y = in_y ? (uint64_t)kStepY * a.dy_pitch * sizeof(TY) : 0, go_x = in_x ? (uint64_t)kStepX * cp : 0;
   const uint64_t go_s = in_x ? (uint64_t)kStepX * sp : 0;
@@ -271,7 +268,6 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
   const uint32_t parts = PARTED ? splits : part + 1;
   uint32_t p = part;
   do {
-    begin(p);
     if (steps) {
 #pragma unroll
       for (uint32_t k = 0; k < 3; ++k) fetch_direct(ring + k * kStage, k);
@@ -292,7 +288,14 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
     }
     if (kPingPong && !behind) phase_barrier();
     __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);  // no load into LDS outlives the workgroup, or this part
-    if (PARTED && p + 1 < parts) phase_barrier();  // every wavefront's
+    if constexpr (PARTED) {
+      phase_barrier();  // every wavefront's
+      // back over what was asked for: X's stages and four more, dY's and three more, to the next part
+      px -= (uint64_t)(steps + 4) * kPiecesX * go_x;
+      ps -= (uint64_t)(steps + 4) * kPiecesX * go_s;
+      py -= (uint64_t)(steps + 3) * kPiecesY * go_y;
+      if (in_y) py += a.T * a.dy_pitch * sizeof(TY);
+    }
   } while (PARTED && ++p < parts);
   TO *dw = static_cast<TO *>(dst) + (uint64_t)blockIdx.y * a.N * a.K;
   if constexpr (F == 16) {
