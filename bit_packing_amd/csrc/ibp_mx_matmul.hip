@@ -439,13 +439,14 @@ template <bool A8> hipError_t go(const MxMatmulArgs &a, hipStream_t s) {
 
 // A few rows an expert: bound by reading the weights.  A workgroup of four wavefronts
 // computes 16 FM rows of one expert by 64 FN columns, each wavefront all rows of 16 FN columns.
-// Operands come as in the larger tiles, in a ring of STAGES stages of 128 elements; one
-// barrier a stage, at which its loads are done and all have read the stage before, whose
-// place is filled anew.  Several workgroups a CU overlap their loads and products.
-template <bool A8, int FM, int FN, int STAGES, int DO>
+// Operands come as in the larger tiles, in a ring of three stages of 128 elements; one barrier a
+// stage, at which its loads are done and all have read the stage before, whose place is
+// filled anew.  Three workgroups a CU overlap their loads and products (with five stages two
+// fit: 64 rows of 64 experts, 2048 x 4096, e4m3 36.2 us against 33.4, 4.4 TB/s of weights).
+template <bool A8, int FM, int FN, int DO>
 __global__ __launch_bounds__(256) void mx_rows_kernel(MxMatmulArgs a, uint32_t tiles_n) {
   using TO = typename Num<DO>::T;
-  constexpr uint32_t kWaves = 4, kPitchA = A8 ? 128 : 64, kPitchB = 64, kRowsB = 64 * FN;
+  constexpr uint32_t kWaves = 4, kStages = 3, kPitchA = A8 ? 128 : 64, kPitchB = 64, kRowsB = 64 * FN;
   constexpr uint32_t kLeastA = 1024 * kWaves / kPitchA;  // rows that a load of every wavefront covers
   constexpr uint32_t kRowsA = 16 * FM < kLeastA ? kLeastA : 16 * FM;
   using TileA = Tile<kRowsA, kPitchA, kWaves>;
@@ -453,9 +454,9 @@ __global__ __launch_bounds__(256) void mx_rows_kernel(MxMatmulArgs a, uint32_t t
   constexpr uint32_t kStage = TileA::kBytes + TileB::kBytes, kLoads = TileA::kLoads + TileB::kLoads;
   // scales of four stages, 16 bytes of each row of A, then of B
   constexpr uint32_t kGroup = 4, kLoaders = (16 * FM + kRowsB + 63) / 64, kScales = kLoaders * 1024;
-  static_assert(STAGES - 1 <= (int)kGroup, "a stage is asked for after its scales");
-  static_assert(kLoaders <= kWaves && (STAGES - 2) * kLoads < 64, "");
-  __shared__ __align__(1024) uint8_t ring[STAGES * kStage + 2 * kScales];
+  static_assert(kStages - 1 <= kGroup, "a stage is asked for after its scales");
+  static_assert(kLoaders <= kWaves && (kStages - 2) * kLoads < 64, "");
+  __shared__ __align__(1024) uint8_t ring[kStages * kStage + 2 * kScales];
   const uint32_t lane = lane_id(), wave = uniform(threadIdx.x / kWave), r = lane & 15, g = lane >> 4;
   const Experts x{a.offsets, a.experts, (uint32_t)__builtin_ctz(16 * FM), a.M};
   if (a.err && blockIdx.x == 0 && wave == 0) check_offsets(x, a.err);
@@ -485,7 +486,7 @@ __global__ __launch_bounds__(256) void mx_rows_kernel(MxMatmulArgs a, uint32_t t
   for (int n = 0; n < FN; ++n)
 #pragma unroll
     for (int m = 0; m < FM; ++m) acc[n][m] = v4f{0, 0, 0, 0};
-  uint8_t *const scales = ring + STAGES * kStage;
+  uint8_t *const scales = ring + kStages * kStage;
   // Always kLoads loads, of zeros past the rows' end: the waits below count on it.
   auto fill = [&](uint8_t *st, uint32_t stage) {
     ta.load(st, stage * kPitchA, cpa, wave);
@@ -514,7 +515,7 @@ __global__ __launch_bounds__(256) void mx_rows_kernel(MxMatmulArgs a, uint32_t t
   auto read = [&](uint8_t *__restrict__ filled, uint8_t *__restrict__ filled_scales, const uint8_t *__restrict__ st,
                   const uint8_t *__restrict__ sc, uint32_t k) {
     if (k % kGroup == 0) fill_scales(filled_scales, k / kGroup + 1);
-    fill(filled, k + STAGES - 1);
+    fill(filled, k + kStages - 1);
     const uint4 none = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int n = 0; n < FN; ++n) {
@@ -530,16 +531,16 @@ __global__ __launch_bounds__(256) void mx_rows_kernel(MxMatmulArgs a, uint32_t t
   };
   fill_scales(scales, 0);
 #pragma unroll
-  for (uint32_t k = 0; k + 1 < STAGES; ++k) fill(ring + k * kStage, k);
-  uint32_t now = 0, next = STAGES - 1;
+  for (uint32_t k = 0; k + 1 < kStages; ++k) fill(ring + k * kStage, k);
+  uint32_t now = 0, next = kStages - 1;
 #pragma unroll 1
   for (uint32_t k = 0; k < steps; ++k) {
-    __builtin_amdgcn_s_waitcnt(wait_loads_and_lds((STAGES - 2) * kLoads));
+    __builtin_amdgcn_s_waitcnt(wait_loads_and_lds((kStages - 2) * kLoads));
     phase_barrier();
     const uint32_t odd = k / kGroup & 1;
     read(ring + next * kStage, scales + (odd ^ 1) * kScales, ring + now * kStage, scales + odd * kScales + k % kGroup * 4, k);
     next = now;
-    now = now + 1 == STAGES ? 0 : now + 1;
+    now = now + 1 == kStages ? 0 : now + 1;
 #pragma unroll
     for (int m = 0; m < FM; ++m)
 #pragma unroll
@@ -556,13 +557,13 @@ __global__ __launch_bounds__(256) void mx_rows_kernel(MxMatmulArgs a, uint32_t t
   }
 }
 
-template <bool A8, int FM, int STAGES> hipError_t go_rows(const MxMatmulArgs &a, hipStream_t s) {
+template <bool A8, int FM> hipError_t go_rows(const MxMatmulArgs &a, hipStream_t s) {
   constexpr uint32_t kCols = 128;
   const uint64_t tiles_n = (a.N + kCols - 1) / kCols;
   const uint64_t grid = most_units(a.M, a.experts, __builtin_ctz(16 * FM), false) * tiles_n;
   if (grid > 0xFFFFFF) return hipErrorInvalidValue;
   return with_dtype(a.dtype, [&](auto d) {
-    mx_rows_kernel<A8, FM, kCols / 64, STAGES, d.value><<<(uint32_t)grid, 256, 0, s>>>(a, (uint32_t)tiles_n);
+    mx_rows_kernel<A8, FM, kCols / 64, d.value><<<(uint32_t)grid, 256, 0, s>>>(a, (uint32_t)tiles_n);
     return hipGetLastError();
   });
 }
@@ -601,14 +602,14 @@ template <bool A8> hipError_t go_grouped(const MxMatmulArgs &a, hipStream_t s) {
     });
   }
   // Fewer rows a tile read and split fewer codes for nothing, more read the weights less often
-  // (32 ragged experts, 2048 x 4096; tiles of 16, 32 and 64 rows; e4m3: 512 rows 34, 41, 43 us,
-  // 1024 rows 55, 41, 60, 2048 rows 79, 70, 62; e2m1: 512 rows 32.5, 32.2, 31.1, 2048 rows 72, 51,
-  // 40; 64 rows of 64 experts 32.3, 32.3, 35.2).
+  // (32 ragged experts, 2048 x 4096; tiles of 16, 32 and 64 rows; e4m3: 512 rows 33, 38, 42 us,
+  // 1024 rows 50, 39, 59, 2048 rows 75, 63, 62; e2m1: 512 rows 31.6, 34.3, 29.0, 2048 rows 72, 52,
+  // 39; 256 rows of 128 experts, 768 x 2048 16.8, 16.9, 17.5).
   if constexpr (A8) {
-    if (T <= 16 * E) return go_rows<true, 1, 5>(a, s);
-    return T <= 48 * E ? go_rows<true, 2, 5>(a, s) : go_rows<true, 4, 4>(a, s);
+    if (T <= 16 * E) return go_rows<true, 1>(a, s);
+    return T <= 48 * E ? go_rows<true, 2>(a, s) : go_rows<true, 4>(a, s);
   } else {
-    return T < 8 * E ? go_rows<false, 2, 5>(a, s) : go_rows<false, 4, 4>(a, s);
+    return T < 8 * E ? go_rows<false, 2>(a, s) : go_rows<false, 4>(a, s);
   }
 }
 
