@@ -24,6 +24,7 @@ typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 constexpr uint32_t kT = 32;  // tokens per stage
+constexpr uint32_t kWholeShift = 31;  // log2 of the unit that no expert's tokens fill
 
 // The 32-byte pieces of row t of a tile are permuted by three bits of t, so that what half a
 // wavefront reads at a time falls into all 64 banks: for fragments of F = 16 columns a piece
@@ -121,11 +122,16 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
   if constexpr (GROUPED) {
     const Experts x{a.offsets, a.experts, (uint32_t)__builtin_ctzll(t_each), a.T};
     if (a.err && blockIdx.x == 0 && blockIdx.y == 0 && wave == 0) check_offsets(x, a.err);
-    const UnitSearch<true> search(x);
-    if (blockIdx.y >= search.total) return;
-    const Unit u = search.find(blockIdx.y);
-    t0 = u.row0;
-    t1 = u.row0 + t_each < u.end ? u.row0 + t_each : u.end;
+    if (t_each >> kWholeShift) {  // a unit an expert: nothing to search for
+      t0 = uniform64(x.start(blockIdx.y));
+      t1 = uniform64(x.start(blockIdx.y + 1));
+    } else {
+      const UnitSearch<true> search(x);
+      if (blockIdx.y >= search.total) return;
+      const Unit u = search.find(blockIdx.y);
+      t0 = u.row0;
+      t1 = u.row0 + t_each < u.end ? u.row0 + t_each : u.end;
+    }
   } else {
     part = blockIdx.y / splits;
     t0 = (blockIdx.y - part * splits) * t_each;
@@ -447,11 +453,11 @@ struct GroupedPlan {
   bool big;
   bool copied;      // dY laid out anew
   uint32_t parts;   // of dY
-  uint32_t shift;   // log2 of a unit's tokens; 31: experts are not cut
+  uint32_t shift;   // log2 of a unit's tokens; kWholeShift: experts are not cut
   uint32_t tiles_o, tiles_i;
   uint64_t units;   // at most
 
-  bool joined() const { return shift < 31; }
+  bool joined() const { return shift < kWholeShift; }
   uint64_t sums_bytes(uint32_t N, uint32_t K) const { return joined() ? (units * N * K * 4 + 15) & ~15ull : 0; }
 };
 
@@ -473,7 +479,7 @@ GroupedPlan grouped_plan(uint64_t T, uint32_t experts, uint32_t N, uint32_t K, i
   p.tiles_o = (uint32_t)(((uint64_t)N + wide - 1) / wide);
   p.tiles_i = (uint32_t)(((uint64_t)K + wide - 1) / wide);
   const uint64_t tiles = (uint64_t)p.tiles_o * p.tiles_i;
-  p.shift = 31;
+  p.shift = kWholeShift;
   if (tiles * experts < 256) {
     uint32_t shift = T >> 13 < 1u << 15 ? 13 : 16;  // the grid holds 65535 units
     while (shift > 9 && ((T >> shift) + experts / 2) * tiles < 256) --shift;
