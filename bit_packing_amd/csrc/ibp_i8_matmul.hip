@@ -90,11 +90,19 @@ hipError_t go_direct(const I8MatmulArgs &a, hipStream_t s) {
 // into a.ws + blockIdx.y * M * N.
 //
 // Operands go through LDS by the direct global-to-LDS loads, in stages of 128 codes of every
-// row, whole lines of memory; a stage is two units, A's rows and B's, in a ring of UNITS
-// units, and two matrix instructions deep.  Each of its halves is a reading phase and a
-// multiplying phase with a barrier after each; with two wavefronts a SIMD the second half of
-// the wavefronts runs one phase behind the first, so LDS serves one half while the other
-// multiplies.
+// row; a stage is two units, A's rows and B's, in a ring of UNITS units, and two matrix
+// instructions deep.  128 bytes of a row are a whole line of memory: loads of 64 fill LDS at 14
+// TB/s, of 128 at 22 (measured without the rest).
+//
+// Four wavefronts have one barrier a stage.  Eight, two a SIMD, take each half of a stage in a
+// reading phase and a multiplying phase with a barrier after each; the second half of the
+// wavefronts runs one phase behind the first, so LDS serves one half while the other
+// multiplies.  They go on from tile to tile, and a tile's results leave while the next one's
+// first stages arrive (8192 x 8192 outputs, 512 deep: 55.5 us, 59.0 without; 4096 deep 232 and
+// 235).  8192 x 8192 x 4096 takes 232 us, 2.4 POP/s, 8192 deep 429, 2.6 (registers alone reach
+// 3.5 with such operands, 4.5 with zeros): bound by power (194 us with zeros) and by the phases,
+// matrix units busy 54% of the time.  In turn with the library's product of 8-bit integers to
+// 32-bit sums: 230 us against 241, 4096 x 4096 x 4096 60 against 64, 1024 x 4096 x 4096 28 against 25.
 template <int WM, int WN, int FM, int FN, uint32_t UNITS, bool SUMS, int DO>
 __global__ __launch_bounds__(WM *WN *64, 2) void i8_tile_kernel(I8MatmulArgs a, uint32_t tiles_m, uint32_t tiles_n,
                                                              uint32_t stages_each) {
@@ -107,19 +115,26 @@ __global__ __launch_bounds__(WM *WN *64, 2) void i8_tile_kernel(I8MatmulArgs a, 
   static_assert(UNITS >= 5 && UNITS * kUnit <= 160 * 1024 && (UNITS - 2) * kLoads < 64, "");
   __shared__ __align__(1024) uint8_t ring[UNITS * kUnit];
   const uint32_t lane = lane_id(), wave = uniform(threadIdx.x / kWave), r = lane & 15, g = lane >> 4;
-  const TileId t = tile_of(blockIdx.x, tiles_m, tiles_n);
-  const uint64_t m0 = (uint64_t)t.row * kRowsA, n0 = (uint64_t)t.col * kRowsB;
   const uint32_t cp = (uint32_t)i8_pitch(a.K);
+  uint32_t m0, n0;  // rows are at most 2^30
   TileA ta;
   TileB tb;
-  ta.init(a.a_codes, m0, a.M, cp, wave, lane);
-  tb.init(a.b_codes, n0, a.N, cp, wave, lane);
+  auto aim = [&](uint32_t tile) {
+    const TileId t = tile_of(tile, tiles_m, tiles_n);
+    m0 = t.row * kRowsA;
+    n0 = t.col * kRowsB;
+    ta.init(a.a_codes, m0, a.M, cp, wave, lane);
+    tb.init(a.b_codes, n0, a.N, cp, wave, lane);
+  };
+  aim(blockIdx.x);
   const uint32_t wm = (wave % WM) * 16 * FM, wn = (wave / WM) * 16 * FN;
   v4i acc[FN][FM];
+  auto clear = [&] {
 #pragma unroll
-  for (int n = 0; n < FN; ++n)
+    for (int n = 0; n < FN; ++n)
 #pragma unroll
-    for (int m = 0; m < FM; ++m) acc[n][m] = v4i{0, 0, 0, 0};
+      for (int m = 0; m < FM; ++m) acc[n][m] = v4i{0, 0, 0, 0};
+  };
 
   const uint32_t all = (cp + kPitch - 1) / kPitch, begin = blockIdx.y * stages_each;
   const uint32_t steps = all - begin < stages_each ? all - begin : stages_each;
@@ -164,43 +179,82 @@ __global__ __launch_bounds__(WM *WN *64, 2) void i8_tile_kernel(I8MatmulArgs a, 
   constexpr int kNext = wait_loads_and_lds((UNITS - 4) * kLoads);
   uint32_t now = 0;  // place of stage s's first unit
   if constexpr (kPingPong) {
+    static_assert(!SUMS && UNITS == 5, "");
     const bool behind = wave >= kWaves / 2;
-    Half f;
+    // Results go through the last two places of the ring while the next tile's first three
+    // units are on their way into the others.
+    constexpr int kAt = sizeof(TO) == 2 ? 2 : 1;
+    static_assert(kWaves * out_bytes<TO, FN, kAt>() <= 2 * kUnit, "");
+    constexpr uint32_t kStores = FM * 16 * 16 * FN * sizeof(TO) / 1024;  // of a wavefront, of a whole tile
+    static_assert(3 * kLoads + kStores < 64, "");
     __builtin_amdgcn_s_waitcnt(wait_loads_and_lds((UNITS - 2) * kLoads));
-    phase_barrier();
-    if (behind) phase_barrier();
+    for (uint32_t tile = blockIdx.x;;) {
+      clear();
+      phase_barrier();
+      if (behind) phase_barrier();
 #pragma unroll 1
-    for (uint32_t s = 0; s < steps; ++s) {
-      const uint32_t now_b = place_after(now, 1);
+      for (uint32_t s = 0; s < steps; ++s) {
+        const uint32_t now_b = place_after(now, 1);
 #pragma unroll
-      for (uint32_t h = 0; h < 2; ++h) {
-        read(f, ring + fill_at, ring + now, ring + now_b, h);
-        // These reads are done; in the last phase before the first half reads stage s + 1, so
-        // are every wavefront's loads of it, but not those of the units after it.
-        __builtin_amdgcn_s_waitcnt(0xC07F);
-        if (h == 1 && behind) __builtin_amdgcn_s_waitcnt(kNext);
-        phase_barrier();
-        __builtin_amdgcn_s_setprio(1);
+        for (uint32_t h = 0; h < 2; ++h) {
+          Half f;
+          read(f, ring + fill_at, ring + now, ring + now_b, h);
+          // These reads are done; in the last phase before the first half reads stage s + 1, so
+          // are every wavefront's loads of it, but not those of the units after it.
+          __builtin_amdgcn_s_waitcnt(0xC07F);
+          if (h == 1 && behind) __builtin_amdgcn_s_waitcnt(kNext);
+          phase_barrier();
+          __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int m = 0; m < FM; ++m) {
+          for (int m = 0; m < FM; ++m) {
 #pragma unroll
-          for (int n = 0; n < FN; ++n) acc[n][m] = mfma(f.w[n], f.v[m], acc[n][m]);
-          if (m == 0) {
-            // The places of a stage that all have read: the half behind has when it multiplies the
-            // second half of it, the other when it multiplies the first of the next.
-            __builtin_amdgcn_sched_barrier(0);  // the compiler would issue the loads first
-            if (behind ? h == 1 : h == 0 && s > 0) refill(behind ? s : s - 1);
+            for (int n = 0; n < FN; ++n) acc[n][m] = mfma(f.w[n], f.v[m], acc[n][m]);
+            if (m == 0) {
+              // The places of a stage that all have read: the half behind has when it multiplies the
+              // second half of it, the other when it multiplies the first of the next.
+              __builtin_amdgcn_sched_barrier(0);  // the compiler would issue the loads first
+              if (behind ? h == 1 : h == 0 && s > 0) refill(behind ? s : s - 1);
+            }
           }
+          __builtin_amdgcn_sched_barrier(0);
+          __builtin_amdgcn_s_setprio(0);
+          if (h == 1 && !behind) __builtin_amdgcn_s_waitcnt(kNext);
+          phase_barrier();
         }
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_setprio(0);
-        if (h == 1 && !behind) __builtin_amdgcn_s_waitcnt(kNext);
-        phase_barrier();
+        now = place_after(now, 2);
       }
-      now = place_after(now, 2);
+      if (!behind) phase_barrier();
+      const uint32_t row0 = m0 + wm, col0 = n0 + wn;
+      const bool whole = m0 + kRowsA <= a.M && n0 + kRowsB <= a.N;
+      v4f sb[FN];
+      float sa[FM];
+#pragma unroll
+      for (int n = 0; n < FN; ++n) sb[n] = load4(a.b_scales, col0 + 16 * n + 4 * g, a.N);
+#pragma unroll
+      for (int m = 0; m < FM; ++m) sa[m] = row0 + 16 * m + r < a.M ? a.a_scales[row0 + 16 * m + r] : 0.0f;
+      __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);  // these, and the loads into LDS past the last stage
+      phase_barrier();
+      tile += gridDim.x;
+      const bool more = tile < tiles_m * tiles_n;
+      now = fill_at = 0;
+      if (more) {
+        aim(tile);
+#pragma unroll
+        for (uint32_t u = 0; u < 3; ++u) fill(u % 2, u / 2);
+      }
+      store_fragments<TO, FM, FN, kAt>(reinterpret_cast<TO *>(ring + 3 * kUnit + wave * out_bytes<TO, FN, kAt>()),
+                                       static_cast<TO *>(a.y), row0, (uint32_t)a.M, col0, (uint32_t)a.N, lane,
+                                       [&](int m, int n) { return scaled4(acc[n][m], sa[m], sb[n]); });
+      if (!more) return;
+      phase_barrier();  // all have stored
+#pragma unroll
+      for (uint32_t u = 3; u < UNITS; ++u) fill(u % 2, u / 2);
+      // Stage 0 is there; what was asked for later is one unit, the stores and two units.
+      if (whole) __builtin_amdgcn_s_waitcnt(wait_loads_and_lds(3 * kLoads + kStores));
+      else __builtin_amdgcn_s_waitcnt(wait_loads_and_lds(3 * kLoads));
     }
-    if (!behind) phase_barrier();
   } else {
+    clear();
     // One barrier a stage: every wavefront's loads of it are done, and all have read the stage
     // before, whose places are filled anew.
 #pragma unroll 1
@@ -255,7 +309,7 @@ __global__ __launch_bounds__(WM *WN *64, 2) void i8_tile_kernel(I8MatmulArgs a, 
 #pragma unroll
     for (int m = 0; m < FM; ++m) sa[m] = m0 + wm + 16 * m + r < a.M ? a.a_scales[m0 + wm + 16 * m + r] : 0.0f;
     store_fragments<TO, FM, FN>(reinterpret_cast<TO *>(ring + wave * out_bytes<TO, FN>()), static_cast<TO *>(a.y), m0 + wm,
-                                a.M, n0 + wn, a.N, lane, [&](int m, int n) { return scaled4(acc[n][m], sa[m], sb[n]); });
+                                (uint32_t)a.M, n0 + wn, (uint32_t)a.N, lane, [&](int m, int n) { return scaled4(acc[n][m], sa[m], sb[n]); });
   }
 }
 
@@ -319,13 +373,15 @@ Plan plan_of(uint64_t M, uint64_t N, uint32_t K) {
 }
 
 template <bool SUMS, int DO> hipError_t go_tile(const I8MatmulArgs &a, const Plan &p, hipStream_t s) {
-  const dim3 grid(p.tiles_m * p.tiles_n, p.splits);
-  auto launch = [&](auto kernel, uint32_t threads) { kernel<<<grid, threads, 0, s>>>(a, p.tiles_m, p.tiles_n, p.stages_each); };
+  auto launch = [&](auto kernel, uint32_t threads, uint32_t most) {
+    const uint32_t tiles = p.tiles_m * p.tiles_n;
+    kernel<<<dim3(tiles < most ? tiles : most, p.splits), threads, 0, s>>>(a, p.tiles_m, p.tiles_n, p.stages_each);
+  };
   // small tiles alone are cut; three workgroups of them, and two of the middle ones, fit a CU
-  if (SUMS || p.kind == Plan::kSmall) launch(i8_tile_kernel<2, 2, 2, 2, 6, SUMS, DO>, 256);
+  if (SUMS || p.kind == Plan::kSmall) launch(i8_tile_kernel<2, 2, 2, 2, 6, SUMS, DO>, 256, ~0u);
   else if constexpr (!SUMS) {
-    if (p.kind == Plan::kMiddle) launch(i8_tile_kernel<2, 4, 4, 2, 5, false, DO>, 512);
-    else launch(i8_tile_kernel<2, 4, 8, 4, 5, false, DO>, 512);
+    if (p.kind == Plan::kMiddle) launch(i8_tile_kernel<2, 4, 4, 2, 5, false, DO>, 512, 512);
+    else launch(i8_tile_kernel<2, 4, 8, 4, 5, false, DO>, 512, 256);
   }
   return hipGetLastError();
 }

@@ -354,7 +354,8 @@ __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, voi
   __syncthreads();
   static_assert(kWaves * out_bytes<TO, FN>() <= sizeof(ring), "");
   store_fragments<TO, FM, FN, 2, GROUPED>(reinterpret_cast<TO *>(ring + wave * out_bytes<TO, FN>()),
-                              static_cast<TO *>(dst) + (uint64_t)blockIdx.y * all_m * a.N, m0 + wm, a.M, n0 + wn, a.N, lane,
+                              static_cast<TO *>(dst) + (uint64_t)blockIdx.y * all_m * a.N, (uint32_t)(m0 + wm), (uint32_t)a.M,
+                              (uint32_t)(n0 + wn), (uint32_t)a.N, lane,
                               [&](int m, int n) { return acc[n][m]; });
 }
 

@@ -57,24 +57,26 @@ template <uint32_t PITCH> __device__ __forceinline__ uint32_t swizzle(uint32_t r
 // One operand's codes of a stage: ROWS rows of PITCH bytes, the loads shared by WAVES wavefronts.
 template <uint32_t ROWS, uint32_t PITCH, uint32_t WAVES> struct Tile {
   static constexpr uint32_t kBytes = ROWS * PITCH, kLoads = kBytes / (1024 * WAVES);
+  static_assert(WAVES * 1024 / PITCH % 8 == 0, "the permutation is the same for all of a lane's pieces");
   const uint8_t *code[kLoads];
-  uint32_t at[kLoads];
+  uint32_t at;
 
   __device__ __forceinline__ void init(const uint8_t *codes, uint64_t row0, uint64_t rows, uint32_t cp, uint32_t wave,
                                        uint32_t lane) {
+    const uint32_t first = (wave * 64 + lane) / (PITCH / 16);
+    at = swizzle<PITCH>(first, lane % (PITCH / 16)) * 16;
 #pragma unroll
     for (uint32_t i = 0; i < kLoads; ++i) {
-      const uint32_t slot = (i * WAVES + wave) * 64 + lane, row = slot / (PITCH / 16);
+      const uint32_t row = i * (WAVES * 1024 / PITCH) + first;
       const uint64_t r = row0 + row < rows ? row0 + row : rows - 1;  // results of rows past the end are not stored
-      at[i] = swizzle<PITCH>(row, slot % (PITCH / 16)) * 16;
-      code[i] = codes + r * cp + at[i];
+      code[i] = codes + r * cp + at;
     }
   }
   // The rows' bytes from k on, zeros past the rows' ends.
   __device__ __forceinline__ void load(uint8_t *lds, uint32_t k, uint32_t cp, uint32_t wave) {
 #pragma unroll
     for (uint32_t i = 0; i < kLoads; ++i)
-      to_lds16(k + at[i] < cp ? code[i] + k : kZeros, lds + (i * WAVES + wave) * 1024);
+      to_lds16(k + at < cp ? code[i] + k : kZeros, lds + (i * WAVES + wave) * 1024);
   }
 };
 
@@ -88,7 +90,8 @@ __device__ __forceinline__ void phase_barrier() {
 }
 
 // A wavefront's FM x FN fragments, value(m, n) being four consecutive columns of a lane's row
-// of fragment (m, n), into y from row0 and col0 on, rows and columns below their ends.  They
+// of fragment (m, n), into y from row0 and col0 on, rows and columns below their ends (at most
+// 2^30).  They
 // go through LDS (`out`, the wavefront's own), AT fragments' rows at a time, so that a store
 // covers whole lines of y (from the fragments themselves a row gets 32 bytes at a time).  STREAM:
 // past the caches, which large results would empty of operands (the weight gradients of 32
@@ -96,8 +99,8 @@ __device__ __forceinline__ void phase_barrier() {
 // the product of 32768 rows, 134 MB, 403 and 394; that of 8-bit integers, 134 MB, 235 and 239).
 template <typename TO, int FN, int AT = 2> constexpr uint32_t out_bytes() { return AT * 16 * (16 * FN * sizeof(TO) + 16); }
 template <typename TO, int FM, int FN, int AT = 2, bool STREAM = false, typename F>
-__device__ __forceinline__ void store_fragments(TO *out, TO *y, uint64_t row0, uint64_t rows, uint64_t col0,
-                                                uint64_t cols, uint32_t lane, F &&value) {
+__device__ __forceinline__ void store_fragments(TO *out, TO *y, uint32_t row0, uint32_t rows, uint32_t col0,
+                                                uint32_t cols, uint32_t lane, F &&value) {
   constexpr uint32_t kCols = 16 * FN, kPad = 16 / sizeof(TO), kEach = 16 / sizeof(TO), kPieces = AT * 16 * kCols / kEach / 64;
   typedef TO Aligned __attribute__((ext_vector_type(kEach)));
   typedef TO Loose __attribute__((ext_vector_type(kEach), aligned(sizeof(TO))));
@@ -117,16 +120,16 @@ __device__ __forceinline__ void store_fragments(TO *out, TO *y, uint64_t row0, u
 #pragma unroll
     for (uint32_t p = 0; p < kPieces; ++p) {
       const uint32_t slot = p * 64 + lane, row = slot / (kCols / kEach), c = slot % (kCols / kEach) * kEach;
-      const uint64_t gm = row0 + 16 * m + row, gn = col0 + c;
+      const uint32_t gm = row0 + 16 * m + row, gn = col0 + c;
       if (gm >= rows || gn >= cols) continue;
       const Aligned x = *reinterpret_cast<const Aligned *>(out + row * (kCols + kPad) + c);
       if (gn + kEach <= cols) {
-        if constexpr (STREAM) __builtin_nontemporal_store((Loose)x, reinterpret_cast<Loose *>(y + gm * cols + gn));
-        else *reinterpret_cast<Loose *>(y + gm * cols + gn) = x;
+        if constexpr (STREAM) __builtin_nontemporal_store((Loose)x, reinterpret_cast<Loose *>(y + (uint64_t)gm * cols + gn));
+        else *reinterpret_cast<Loose *>(y + (uint64_t)gm * cols + gn) = x;
       } else {
 #pragma unroll
         for (uint32_t e = 0; e < kEach; ++e)
-          if (gn + e < cols) y[gm * cols + gn + e] = x[e];
+          if (gn + e < cols) y[(uint64_t)gm * cols + gn + e] = x[e];
       }
     }
   }

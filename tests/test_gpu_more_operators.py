@@ -414,6 +414,26 @@ def test_grouped_weights_past_32_bit_offsets(ibp):
     assert np.array_equal(host(dw[4, -64:]), rounded(want.astype(np.float32), "bf16")) and not dw[2].any()
 
 
+def test_grouped_tokens_past_32_bit_offsets(ibp):
+    """The second expert's rows lie 8 GB into the checkpoint and 4 GB into dy; the first one's
+    are not written and not looked at."""
+    t, n, k = (1 << 28) + 40, 8, 32
+    rng = np.random.default_rng(13)
+    x = codes_of(rng, 40, k, mx_ref.E4M3, 0, 0)
+    x8 = ibp.make_mx(t, k, ibp.IBP_MX_E4M3, "cuda")
+    x8.codes[-40:], x8.scales[-40:] = torch.from_numpy(x[0]).cuda(), torch.from_numpy(x[1]).cuda()
+    dy = torch.empty(t, n, dtype=torch.bfloat16, device="cuda")
+    tail = rng.integers(-4, 5, (40, n)).astype(float)
+    dy[-40:] = gpu(tail, "bf16")
+    off = torch.tensor([0, t - 40, t], device="cuda")
+    v = mx_ref.unpack(*x, k, mx_ref.E4M3)
+    dw = ibp.ibp_mx_grouped_wgrad(dy, x8, off, dw_dtype=torch.float32)
+    assert np.array_equal(host(dw[1]), tail.T @ v)
+    b = codes_of(rng, 2 * n, k, mx_ref.E2M1, 0, 0)
+    y = ibp.ibp_mx_grouped_matmul(x8, mx(ibp, *b, k, mx_ref.E2M1), off, dtype=torch.float32)
+    assert np.array_equal(host(y[-40:]), v @ mx_ref.unpack(*b, k, mx_ref.E2M1)[n:].T)
+
+
 WGRADS = [(1, 1, 1, 1, "even"), (31, 3, 16, 32, "ragged"), (32, 4, 33, 31, "one"), (33, 40, 128, 129, "ragged"), (100, 6, 130, 257, "ragged"),
           (999, 2, 50, 100, "even"), (3000, 9, 40, 64, "ragged"), (700, 3, 300, 520, "ragged"), (5000, 1, 129, 64, "even"),
           (64, 1024, 8, 40, "ragged"), (64, 5, 512, 512, "ragged"), (130, 33, 504, 600, "ragged"), (2100, 30, 520, 500, "one"),
@@ -611,6 +631,25 @@ def test_side_stream_and_graph_replays(ibp, tokens):
         torch.cuda.synchronize()
         for _, got in graphs:
             same(got, want)
+
+
+def test_two_streams_at_once(ibp):
+    """Calls that run beside each other share nothing."""
+    layers = [Layer(ibp, n, 160, 264, 10, 2, n) for n in (900, 3000)]
+    w8 = ibp.ibp_i8_pack(torch.randn(200, 160, device="cuda"))
+    want = [(layer.step(), ibp.ibp_i8_matmul(ibp.ibp_i8_pack(layer.x), w8)) for layer in layers]
+    streams = [torch.cuda.Stream() for _ in layers]
+    torch.cuda.synchronize()
+    got = [[] for _ in layers]
+    for _ in range(3):
+        for layer, stream, g in zip(layers, streams, got):
+            with torch.cuda.stream(stream):
+                g.append((layer.step(), ibp.ibp_i8_matmul(ibp.ibp_i8_pack(layer.x), w8)))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        for s, y in g:
+            same(s, w[0])
+            assert torch.equal(y, w[1])
 
 
 def test_the_stream_argument(ibp):
