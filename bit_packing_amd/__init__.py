@@ -304,7 +304,7 @@ def load_library() -> ctypes.CDLL:
         lib.ibp_expert_order_workspace_bytes.argtypes = [_u64, _u64]
         lib.ibp_mx_grouped_matmul.argtypes = [_mxp, _mxp, _vp, _u64, _vp, _int, _vp, _vp]
         lib.ibp_mx_grouped_wgrad.argtypes = [_vp, _int, _u64, _mxp, _vp, _u64, _vp, _int, _vp, _u64, _vp, _vp]
-        lib.ibp_mx_grouped_wgrad_workspace_bytes.argtypes = [_u64, _u64, _u64, _u64, _int]
+        lib.ibp_mx_grouped_wgrad_workspace_bytes.argtypes = [_u64, _u64, _u64, _u64, _int, _vp]
         for f in ("ibp_i8_codes_pitch", "ibp_i8_matmul_workspace_bytes", "ibp_expert_order_workspace_bytes",
                   "ibp_mx_grouped_wgrad_workspace_bytes", "ibp_embedding_grad_workspace_bytes", "ibp_mx_codes_pitch", "ibp_mx_scales_pitch",
                   "ibp_mx_matmul_workspace_bytes", "ibp_mx_linear_wgrad_workspace_bytes"):
@@ -667,9 +667,12 @@ def _ids(ids: torch.Tensor) -> torch.Tensor:
 
 def _matrix(x: torch.Tensor) -> tuple[int, int]:
     """(rows, cols) of a tensor read as rows of its last dimension."""
-    if x.dim() == 0:
+    shape = x.shape
+    if len(shape) == 2:
+        return shape[0], shape[1]
+    if not shape:
         raise ValueError("a tensor of rows is needed")
-    return math.prod(x.shape[:-1]), x.shape[-1]
+    return math.prod(shape[:-1]), shape[-1]
 
 
 def _out(out: torch.Tensor | None, shape, dtype, device) -> torch.Tensor:
@@ -867,14 +870,19 @@ def ibp_mx_linear_wgrad(dy: torch.Tensor, x8: MxTensor, dw_dtype=None, dw: torch
 # ------------------------------------------------------------------ 8-bit integer rows and experts
 
 
-def _here(*tensors) -> torch.device:
+def _here(*tensors) -> int:
     """The current device, on which a call runs, after a check that the tensors that are on a
     device are on it."""
     now = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() not in (now, -1):
             raise ValueError(f"a tensor is on {t.device}, not on the current device {now}")
-    return torch.device("cuda", now)
+    return now
+
+
+def _stream_of(device: int) -> int:
+    """The current stream's handle of a device."""
+    return _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
 
 
 def _parts(m) -> tuple:
@@ -894,8 +902,11 @@ def ibp_expert_order_workspace_bytes(n_ids: int, n_experts: int) -> int:
     return int(load_library().ibp_expert_order_workspace_bytes(n_ids, n_experts))
 
 
-def ibp_mx_grouped_wgrad_workspace_bytes(tokens: int, n_experts: int, outs: int, ins: int, dy_dtype=torch.bfloat16) -> int:
-    return int(load_library().ibp_mx_grouped_wgrad_workspace_bytes(tokens, n_experts, outs, ins, _dtype(dy_dtype)))
+def ibp_mx_grouped_wgrad_workspace_bytes(tokens: int, n_experts: int, outs: int, ins: int, dy_dtype=torch.bfloat16,
+                                         dy: torch.Tensor | None = None) -> int:
+    """For a given dy, whose address counts, or for any."""
+    return int(load_library().ibp_mx_grouped_wgrad_workspace_bytes(tokens, n_experts, outs, ins, _dtype(dy_dtype),
+                                                                   _ptr(dy)))
 
 
 def make_i8(rows: int, cols: int, device) -> I8Tensor:
@@ -911,12 +922,13 @@ def ibp_i8_pack(x: torch.Tensor, out: I8Tensor | None = None, stream=None) -> I8
     rows, cols = _matrix(x)
     dtype = _dtype(x.dtype)
     if out is None:
-        out = make_i8(rows, cols, _here(x))
+        dev = _here(x)
+        out = make_i8(rows, cols, dev)
     elif (out.rows, out.cols) != (rows, cols):
         raise ValueError("the packed output has another shape")
     else:
-        _here(x, *_parts(out))
-    _check(load_library().ibp_i8_pack(_ptr(x), dtype, ctypes.byref(out.struct()), _stream(None)), "ibp_i8_pack")
+        dev = _here(x, *_parts(out))
+    _check(load_library().ibp_i8_pack(_ptr(x), dtype, ctypes.byref(out.struct()), _stream_of(dev)), "ibp_i8_pack")
     return out
 
 
@@ -925,8 +937,9 @@ def ibp_i8_unpack(t: I8Tensor, dtype=torch.bfloat16, out: torch.Tensor | None = 
     if stream is not None:
         with _stream_context(stream):
             return ibp_i8_unpack(t, dtype, out)
-    out = _out(out, (t.rows, t.cols), dtype, _here(*_parts(t), out))
-    _check(load_library().ibp_i8_unpack(ctypes.byref(t.struct()), _ptr(out), _dtype(out.dtype), _stream(None)),
+    dev = _here(*_parts(t), out)
+    out = _out(out, (t.rows, t.cols), dtype, dev)
+    _check(load_library().ibp_i8_unpack(ctypes.byref(t.struct()), _ptr(out), _dtype(out.dtype), _stream_of(dev)),
            "ibp_i8_unpack")
     return out
 
@@ -942,7 +955,7 @@ def ibp_i8_matmul(a: I8Tensor, b: I8Tensor, dtype=torch.bfloat16, out: torch.Ten
     out = _out(out, (a.rows, b.rows), dtype, dev)
     workspace = _workspace(workspace, int(lib.ibp_i8_matmul_workspace_bytes(a.rows, b.rows, a.cols)), dev)
     rc = lib.ibp_i8_matmul(ctypes.byref(a.struct()), ctypes.byref(b.struct()), _ptr(out), _dtype(out.dtype),
-                           _ptr(workspace), 0 if workspace is None else _nbytes(workspace), _stream(None))
+                           _ptr(workspace), 0 if workspace is None else _nbytes(workspace), _stream_of(dev))
     _check(rc, "ibp_i8_matmul")
     return out
 
@@ -961,7 +974,7 @@ def ibp_expert_order(ids: torch.Tensor, n_experts: int, order: torch.Tensor | No
     offsets = _out(offsets, (n_experts + 1,), torch.int64, dev)
     workspace = _workspace(workspace, int(lib.ibp_expert_order_workspace_bytes(n, n_experts)), dev)
     rc = lib.ibp_expert_order(_ptr(ids), n, n_experts, _ptr(order), _ptr(offsets), _ptr(workspace),
-                              0 if workspace is None else _nbytes(workspace), _ptr(err), _stream(None))
+                              0 if workspace is None else _nbytes(workspace), _ptr(err), _stream_of(dev))
     _check(rc, "ibp_expert_order")
     return order, offsets
 
@@ -987,7 +1000,7 @@ def ibp_mx_grouped_matmul(a: MxTensor, b: MxTensor, offsets: torch.Tensor, dtype
     lib, dev = load_library(), _here(*_parts(a), *_parts(b), offsets, out, err)
     out = _out(out, (a.rows, b.rows // n), dtype, dev)
     rc = lib.ibp_mx_grouped_matmul(ctypes.byref(a.struct()), ctypes.byref(b.struct()), _ptr(offsets), n, _ptr(out),
-                                   _dtype(out.dtype), _ptr(err), _stream(None))
+                                   _dtype(out.dtype), _ptr(err), _stream_of(dev))
     _check(rc, "ibp_mx_grouped_matmul")
     return out
 
@@ -1006,10 +1019,10 @@ def ibp_mx_grouped_wgrad(dy: torch.Tensor, x8: MxTensor, offsets: torch.Tensor, 
     n, outs = _experts(offsets), dy.shape[1]
     lib, dev = load_library(), _here(dy, *_parts(x8), offsets, dw, workspace, err)
     dw = _out(dw, (n, outs, x8.cols), dw_dtype or (dy.dtype if dw is None else dw.dtype), dev)
-    need = int(lib.ibp_mx_grouped_wgrad_workspace_bytes(x8.rows, n, outs, x8.cols, _dtype(dy.dtype)))
+    need = int(lib.ibp_mx_grouped_wgrad_workspace_bytes(x8.rows, n, outs, x8.cols, _dtype(dy.dtype), _ptr(dy)))
     workspace = _workspace(workspace, need, dev)
     rc = lib.ibp_mx_grouped_wgrad(_ptr(dy), _dtype(dy.dtype), outs, ctypes.byref(x8.struct()), _ptr(offsets), n,
                                   _ptr(dw), _dtype(dw.dtype), _ptr(workspace),
-                                  0 if workspace is None else _nbytes(workspace), _ptr(err), _stream(None))
+                                  0 if workspace is None else _nbytes(workspace), _ptr(err), _stream_of(dev))
     _check(rc, "ibp_mx_grouped_wgrad")
     return dw

@@ -32,7 +32,7 @@ constexpr uint32_t kStep = 16;  // blocks per step of the direct kernel: 512 ele
 // more, whose codes have bit 6, go through one instruction (2^10 down to 2^-3) and the rest
 // through another (4 down to 2^-10): nothing is dropped.  In one instruction a block whose
 // large products cancel, as those of an outlier column may, would lose its result: 8192 x
-// 8192 x 8192 would take 370 us so, against 742 (614 without the work of splitting).
+// 8192 x 8192 would take 370 us so, against 590.
 //
 // split takes the large elements' bytes out of four.
 __device__ __forceinline__ int split(int &x) {
@@ -310,7 +310,8 @@ __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, voi
     __builtin_amdgcn_s_setprio(1);
     if constexpr (A8) {
       // A fragment's successor is split between its matrix instructions, four bytes at a time,
-      // which they hide: split all at once, before them, the matrix units would wait meanwhile.
+      // which they hide: split all at once, before them, the matrix units would wait meanwhile
+      // (8192 x 8192 x 8192: 740 us, and 727 with few fragments a wavefront, against 590).
       v8i high, next;
       constexpr int kEach = 2 * FN / 8;  // matrix instructions for four bytes
 #pragma unroll
@@ -385,7 +386,7 @@ Plan plan_of(uint64_t M, uint64_t N, uint32_t K) {
   if (blocks <= 512 || (M <= 16 && blocks <= 1u << 22)) return p;
   // Many rows: the larger tiles from 192 of them on (e2m1: 1536 x 8192 outputs, 4096 deep 34
   // us against 45, 8192 deep 60 against 83; 1024 x 8192, 8192 deep, 128 large tiles: 54 each;
-  // e4m3: 98 against 95, 185 against 178; 185 against 106).
+  // e4m3: 82 against 97, 137 against 183; 136 against 108).
   const bool big = ((M + 255) / 256) * ((N + 255) / 256) >= 192;
   const uint32_t wide = big ? 256 : 128;
   p.kind = big ? Plan::kBig : Plan::kMiddle;

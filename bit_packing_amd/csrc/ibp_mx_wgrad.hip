@@ -503,9 +503,8 @@ template <int DO> hipError_t go_grouped(const MxWgradArgs &a, const GroupedPlan 
 
 }  // namespace
 
-uint64_t mx_grouped_wgrad_workspace(uint64_t T, uint32_t experts, uint32_t N, uint32_t K, int dy_dtype) {
-  // as for a dY that begins off 16 bytes, which is laid out anew whatever its rows
-  const GroupedPlan p = grouped_plan(T, experts, N, K, dy_dtype, false);
+uint64_t mx_grouped_wgrad_workspace(uint64_t T, uint32_t experts, uint32_t N, uint32_t K, int dy_dtype, bool dy_aligned) {
+  const GroupedPlan p = grouped_plan(T, experts, N, K, dy_dtype, dy_aligned);
   return p.sums_bytes(N, K) + (p.copied ? p.parts * T * padded(N) * 2 : 0);
 }
 

@@ -89,7 +89,7 @@ struct MxWgradArgs {
   uint32_t *err;           // optional
 };
 uint64_t mx_wgrad_workspace(uint64_t T, uint32_t N, uint32_t K, int dy_dtype);
-uint64_t mx_grouped_wgrad_workspace(uint64_t T, uint32_t experts, uint32_t N, uint32_t K, int dy_dtype);
+uint64_t mx_grouped_wgrad_workspace(uint64_t T, uint32_t experts, uint32_t N, uint32_t K, int dy_dtype, bool dy_aligned);
 
 // 8-bit integer rows with a scale each.
 __host__ __device__ constexpr uint64_t i8_pitch(uint64_t cols) { return (cols + 15) / 16 * 16; }

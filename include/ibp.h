@@ -531,10 +531,12 @@ IBP_API int ibp_mx_grouped_matmul(const ibp_mx_t *a, const ibp_mx_t *b, const in
 /*
  * Weight gradients of experts from the 8-bit checkpoint of their input: d_dw[e][o][i] = sum
  * over the rows t of expert e of d_dy[t][o] * x8[t][i], as ibp_mx_linear_wgrad; zeros for an
- * expert without rows.  d_dw n_experts x outs x x8->cols of dw_dtype.  Asynchronous.
+ * expert without rows.  d_dw n_experts x outs x x8->cols of dw_dtype.  The workspace holds a
+ * copy of d_dy unless that is BF16, begins at 16 bytes and has a multiple of 8 columns; the
+ * query takes d_dy for its address alone, NULL for any.  Asynchronous.
  */
 IBP_API uint64_t ibp_mx_grouped_wgrad_workspace_bytes(uint64_t tokens, uint64_t n_experts, uint64_t outs, uint64_t ins,
-                                                      int dy_dtype);
+                                                      int dy_dtype, const void *d_dy);
 IBP_API int ibp_mx_grouped_wgrad(const void *d_dy, int dy_dtype, uint64_t outs, const ibp_mx_t *x8,
                                  const int64_t *d_offsets, uint64_t n_experts, void *d_dw, int dw_dtype,
                                  void *d_workspace, uint64_t workspace_bytes, uint32_t *d_err_word, void *hip_stream);

@@ -50,6 +50,11 @@ def test_queries(ibp):
     assert ibp.ibp_expert_order_workspace_bytes(1 << 20, ibp.IBP_MAX_EXPERTS + 1) == 0
     assert ibp.ibp_mx_grouped_wgrad_workspace_bytes(10, 0, 8, 32) == 0
     assert ibp.ibp_mx_grouped_wgrad_workspace_bytes(10, 2, 8, 32, torch.float32) >= 3 * 10 * 8 * 2
+    lib = ibp.load_library()
+    assert lib.ibp_mx_grouped_wgrad_workspace_bytes(10, 2, 8, 32, BF16, FAKE) == 0  # taken as it lies
+    assert lib.ibp_mx_grouped_wgrad_workspace_bytes(10, 2, 8, 32, BF16, FAKE + 2) == 10 * 8 * 2
+    assert lib.ibp_mx_grouped_wgrad_workspace_bytes(10, 2, 9, 32, BF16, FAKE) == 10 * 16 * 2
+    assert lib.ibp_mx_grouped_wgrad_workspace_bytes(10, 2, 8, 32, BF16, None) == 10 * 8 * 2
 
 
 def test_i8_refusals(ibp):
@@ -143,7 +148,7 @@ def test_grouped_refusals(ibp):
     assert call(dy=None) == no and call(dw=None) == no and call(off=None) == no and call(off=FAKE + 4) == no
     assert call(dy=FAR + 1) == no and call(dw=FAR + 2) == no and call(w=FAR + 8) == no and call(err=FAKE + 2) == no
     assert call(dw=FAR) == no and call(dw=4 * FAR) == no  # over dy, over the workspace
-    assert need == 0 or call(wb=need - 1) == ibp.IBP_ERR_CAPACITY
+    assert need > 0 and call(dy=FAR + 2, wb=need - 1) == ibp.IBP_ERR_CAPACITY and call(dy=FAR + 2, w=None) == no
     assert call(t=F32, wb=0) == ibp.IBP_ERR_CAPACITY
     assert call(outs=0, dw=None) == ibp.IBP_OK
 
