@@ -28,9 +28,6 @@ __device__ __forceinline__ float scaled(int sum, float sa, float sb) {
   return (float)sum * (a_less ? sa : sb) * (a_less ? sb : sa);
 }
 
-// The scales of four columns from n on, zeros past the end.
-__device__ __forceinline__ v4f scales4(const float *scales, uint64_t n, uint64_t N) { return load4(scales, n, N); }
-
 __device__ __forceinline__ v4f scaled4(v4i sum, float sa, v4f sb) {
   return v4f{scaled(sum[0], sa, sb[0]), scaled(sum[1], sa, sb[1]), scaled(sum[2], sa, sb[2]), scaled(sum[3], sa, sb[3])};
 }
@@ -67,7 +64,7 @@ template <int DO> __global__ void i8_direct_kernel(I8MatmulArgs a) {
   }
   if (m0 + r < a.M)
     store4<TO>(static_cast<TO *>(a.y) + (m0 + r) * a.N, n0 + 4 * g, a.N,
-               scaled4(acc, a.a_scales[m0 + r], scales4(a.b_scales, n0 + 4 * g, a.N)));
+               scaled4(acc, a.a_scales[m0 + r], load4(a.b_scales, n0 + 4 * g, a.N)));
 }
 
 hipError_t go_direct(const I8MatmulArgs &a, hipStream_t s) {
@@ -354,8 +351,9 @@ Plan plan_of(uint64_t M, uint64_t N, uint32_t K) {
   // 128 x 128; 1500 x 2000 (192), 1000 deep 10.2 and 10.7; 1024 x 4096 (256), 4096 deep 28.9 and
   // 27.1; 64 x 65536 46.6 and 46.5, 100 x 65536 67.1 and 48.9.  256 x 256: 2048 x 4096 outputs
   // (128 tiles of 256), 2048 deep 33.0 against 28.7 with 128 x 128; 1536 x 8192 (192), 4096 deep
-  // 56.6 and 63.8; 4096 x 4096 (256), 1024 deep 23.5 and 28.6; 256 x 32768 53.2 and 42.4.
-  p.kind = tiles(128) <= 192 || least <= 64 ? Plan::kSmall : (tiles(256) < 192 || least <= 256 ? Plan::kMiddle : Plan::kBig);
+  // 56.6 and 63.8; 4096 x 4096 (256), 1024 deep 23.5 and 28.6; 256 x 32768 53.2 and 42.4.  A
+  // launch holds less than 2^24 small tiles, each a workgroup; the others go on from tile to tile.
+  p.kind = tiles(128) <= 192 || (least <= 64 && tiles(64) < 1u << 24) ? Plan::kSmall : (tiles(256) < 192 || least <= 256 ? Plan::kMiddle : Plan::kBig);
   const uint32_t wide = p.kind == Plan::kSmall ? 64 : (p.kind == Plan::kMiddle ? 128 : 256);
   p.tiles_m = (uint32_t)((M + wide - 1) / wide);
   p.tiles_n = (uint32_t)((N + wide - 1) / wide);
@@ -396,7 +394,6 @@ uint64_t i8_matmul_workspace(uint64_t M, uint64_t N, uint32_t K) {
 hipError_t launch_i8_matmul(const I8MatmulArgs &a, hipStream_t s) {
   const Plan p = plan_of(a.M, a.N, a.K);
   if (p.kind == Plan::kDirect) return go_direct(a, s);
-  if ((uint64_t)p.tiles_m * p.tiles_n > 0x7FFFFF) return hipErrorInvalidValue;
   if (p.splits > 1) {
     const hipError_t e = go_tile<true, IBP_F32>(a, p, s);
     if (e != hipSuccess) return e;

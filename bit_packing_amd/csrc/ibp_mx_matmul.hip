@@ -81,9 +81,9 @@ __device__ __forceinline__ uint4 scales16(const uint8_t *row, uint32_t b, uint32
 
 // Few rows of A: bound by the latency of a step's loads, of which the next step's are not in
 // flight (1 x 8192 outputs, 8192 deep: 8.3 us from e2m1, 4.3 TB/s of weights, 10.2 from e4m3, 3.5
-// TB/s; half of the wavefronts' time is waiting).  A workgroup computes 16 x 16 outputs, its wavefronts take the steps of k in
-// turn and their sums are added in order through LDS.  A step is 16 blocks, four matrix
-// instructions; each load takes 64 consecutive bytes of 16 rows.
+// TB/s; half of the wavefronts' time is waiting).  A workgroup computes 16 x 16 outputs, its
+// wavefronts take the steps of k in turn and their sums are added in order through LDS.  A step
+// is 16 blocks, four matrix instructions; each load takes 64 consecutive bytes of 16 rows.
 //
 // GROUPED: the rows are sorted by expert, and blockIdx.y counts units of 16 rows of one
 // expert, as many as there can be; those that there are not have nothing to do.
@@ -461,10 +461,11 @@ __global__ __launch_bounds__(256) void mx_rows_kernel(MxMatmulArgs a, uint32_t t
   __shared__ __align__(1024) uint8_t ring[kStages * kStage + 2 * kScales];
   const uint32_t lane = lane_id(), wave = uniform(threadIdx.x / kWave), r = lane & 15, g = lane >> 4;
   const Experts x{a.offsets, a.experts, (uint32_t)__builtin_ctz(16 * FM), a.M};
-  if (a.err && blockIdx.x == 0 && wave == 0) check_offsets(x, a.err);
+  const uint32_t block = blockIdx.y * gridDim.x + blockIdx.x;
+  if (a.err && block == 0 && wave == 0) check_offsets(x, a.err);
   const UnitSearch<false> search(x);
-  if (blockIdx.x >= (uint64_t)search.total * tiles_n) return;
-  const TileId t = tile_of(blockIdx.x, search.total, tiles_n);
+  if (block >= (uint64_t)search.total * tiles_n) return;
+  const TileId t = tile_of(block, search.total, tiles_n);
   const Unit u = search.find(t.row);
   if (u.row0 >= u.end) return;
   const uint64_t m0 = u.row0, n0 = (uint64_t)t.col * kRowsB;
@@ -563,9 +564,9 @@ template <bool A8, int FM> hipError_t go_rows(const MxMatmulArgs &a, hipStream_t
   constexpr uint32_t kCols = 128;
   const uint64_t tiles_n = (a.N + kCols - 1) / kCols;
   const uint64_t grid = most_units(a.M, a.experts, __builtin_ctz(16 * FM), false) * tiles_n;
-  if (grid > 0xFFFFFF) return hipErrorInvalidValue;
+  const uint64_t many = (grid + (1u << 20) - 1) >> 20;  // a dimension of a launch holds less than 2^24 workgroups of 256
   return with_dtype(a.dtype, [&](auto d) {
-    mx_rows_kernel<A8, FM, kCols / 64, d.value><<<(uint32_t)grid, 256, 0, s>>>(a, (uint32_t)tiles_n);
+    mx_rows_kernel<A8, FM, kCols / 64, d.value><<<dim3((uint32_t)(many > 1 ? 1u << 20 : grid), (uint32_t)many), 256, 0, s>>>(a, (uint32_t)tiles_n);
     return hipGetLastError();
   });
 }

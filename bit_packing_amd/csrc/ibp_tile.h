@@ -91,10 +91,9 @@ __device__ __forceinline__ void phase_barrier() {
 
 // A wavefront's FM x FN fragments, value(m, n) being four consecutive columns of a lane's row
 // of fragment (m, n), into y from row0 and col0 on, rows and columns below their ends (at most
-// 2^30).  They
-// go through LDS (`out`, the wavefront's own), AT fragments' rows at a time, so that a store
-// covers whole lines of y (from the fragments themselves a row gets 32 bytes at a time).  STREAM:
-// past the caches, which large results would empty of operands (the weight gradients of 32
+// 2^30).  They go through LDS (`out`, the wavefront's own), AT fragments' rows at a time, so that
+// a store covers whole lines of y (from the fragments themselves a row gets 32 bytes at a time).
+// STREAM: past the caches, which large results would empty of operands (the weight gradients of 32
 // experts, 2048 x 4096, 537 MB: of 32768 tokens 642 us without, 606 with; of 8192 304 and 245;
 // the product of 32768 rows, 134 MB, 403 and 394; that of 8-bit integers, 134 MB, 235 and 239).
 template <typename TO, int FN, int AT = 2> constexpr uint32_t out_bytes() { return AT * 16 * (16 * FN * sizeof(TO) + 16); }

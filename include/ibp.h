@@ -458,8 +458,9 @@ IBP_API int ibp_mx_linear_wgrad(const void *d_dy, int dy_dtype, uint64_t outs, c
  * 8-bit integer rows.  A row of cols elements with the largest magnitude m has the scale
  * m / 127, rounded to 32 bits (down where 127 times it would be infinite), and the codes
  * 127 x / m rounded to the nearest whole number, ties to even (the quotient itself is
- * rounded, whatever the element type); an element reads back as its code times the scale.  A row of zeros has the scale 0; a row that holds
- * an infinity or a NaN has codes 0 and a NaN scale, and reads back as NaN throughout.
+ * rounded, whatever the element type); an element reads back as its code times the scale.  A
+ * row of zeros has the scale 0; a row that holds an infinity or a NaN has codes 0 and a NaN
+ * scale, and reads back as NaN throughout.
  *   codes:  rows x ibp_i8_codes_pitch(cols) bytes, cols filled up with zeros to a multiple
  *           of 16; aligned to 16.
  *   scales: rows floats.

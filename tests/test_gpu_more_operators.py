@@ -174,6 +174,23 @@ def test_i8_pack_past_32_bit_offsets(ibp):
     assert np.array_equal(host(got), i8_ref.product(codes, scales, b.codes.cpu().numpy(), b.scales.cpu().numpy()))
 
 
+def test_i8_matmul_of_more_tiles_than_a_launch_has(ibp):
+    """2^24 small tiles and some, of few rows and very many columns."""
+    m, n, k = 10, (1 << 30) - 3, 16
+    rng = np.random.default_rng(14)
+    ac = rng.integers(-127, 128, (m, k)).astype(np.int8)
+    a, b = ibp.make_i8(m, k, "cuda"), ibp.make_i8(n, k, "cuda")
+    a.codes[:], a.scales[:] = torch.from_numpy(ac).cuda(), 0.5
+    b.codes.random_(-128, 128)
+    b.scales.fill_(2.0)
+    y = ibp.ibp_i8_matmul(a, b, dtype=torch.float16)
+    for c in (0, (1 << 28) - 500, (1 << 29) + 17, n - 1000):
+        bc = b.codes[c : c + 1000].cpu().numpy()
+        want = (ac.astype(np.int64) @ bc.T.astype(np.int64)).astype(np.float32)
+        with np.errstate(over="ignore"):
+            assert np.array_equal(host(y[:, c : c + 1000]), rounded(want, "f16"))
+
+
 PRODUCTS = [(1, 1, 1), (1, 16, 64), (2, 33, 31), (16, 17, 129), (17, 100, 512), (31, 64, 513), (64, 65, 1000), (65, 200, 96),
             (130, 129, 640), (257, 300, 1056), (1, 1000, 2080), (300, 20, 160), (512, 512, 256), (1000, 1100, 288),
             (1030, 1000, 33), (3500, 3600, 160), (3600, 3500, 545), (128, 512, 4100), (1, 5000, 9000), (2050, 2049, 129),
@@ -412,6 +429,21 @@ def test_grouped_weights_past_32_bit_offsets(ibp):
     dw = ibp.ibp_mx_grouped_wgrad(gpu(dy, "bf16"), a8, off, dw_dtype=torch.bfloat16)
     want = dy[3:, -64:].T @ va[3:]
     assert np.array_equal(host(dw[4, -64:]), rounded(want.astype(np.float32), "bf16")) and not dw[2].any()
+
+
+def test_grouped_matmul_of_more_tiles_than_a_launch_has(ibp):
+    """2^24 tiles of one expert's rows."""
+    t, n, k = 36, 1 << 30, 32
+    rng = np.random.default_rng(15)
+    a = codes_of(rng, t, k, mx_ref.E4M3, 0, 0)
+    w = ibp.make_mx(n, k, ibp.IBP_MX_E2M1, "cuda")
+    w.codes.random_(0, 256)
+    w.scales.fill_(127)
+    y = ibp.ibp_mx_grouped_matmul(mx(ibp, *a, k, mx_ref.E4M3), w, torch.tensor([0, t], device="cuda"), dtype=torch.bfloat16)
+    for c in (0, (1 << 29) - 500, n - 1000):
+        b = w.codes[c : c + 1000].cpu().numpy(), w.scales[c : c + 1000].cpu().numpy()
+        want = mx_ref.unpack(*a, k, mx_ref.E4M3) @ mx_ref.unpack(*b, k, mx_ref.E2M1).T
+        assert np.array_equal(host(y[:, c : c + 1000]), rounded(want.astype(np.float32), "bf16"))
 
 
 def test_grouped_tokens_past_32_bit_offsets(ibp):
