@@ -117,14 +117,25 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
   static_assert(kStepY % 8 == 0 && kStepX % 8 == 0, "the permutation goes by t & 7, the same for all pieces of a thread");
   __shared__ __align__(1024) uint8_t ring[kRing * kStage];
   const uint32_t lane = lane_id(), wave = uniform(threadIdx.x / kWave);
-  uint32_t part = 0;
+  uint32_t part = 0, of = blockIdx.y;  // of dY; the place in dst
   uint64_t t0, t1;
   if constexpr (GROUPED) {
     const Experts x{a.offsets, a.experts, (uint32_t)__builtin_ctzll(t_each), a.T};
     if (a.err && blockIdx.x == 0 && blockIdx.y == 0 && wave == 0) check_offsets(x, a.err);
     if (t_each >> kWholeShift) {  // a unit an expert: nothing to search for
-      t0 = uniform64(x.start(blockIdx.y));
-      t1 = uniform64(x.start(blockIdx.y + 1));
+      // In a few rounds of workgroups the experts of many tokens go first, so that the last round
+      // is short (60 experts of 400 x 600, 20000 tokens, 360 workgroups: 41.6 us, 55.6 in their
+      // order; 1500 x 1000, 1440: 120, 135; 32 of 1024 x 2048, 1024: 164, 181; 60 of 128 x 1600,
+      // 3000 tokens, 420: 17.6, 19.6).  In many rounds the search costs more than that (32 of 2048 x
+      // 4096, 8192 tokens, 4096 workgroups 221 and 214; 16, 8000 tokens, 2048: 161 and 158), and
+      // where experts have a stage or less (40 of 1000 x 1000, 500 tokens, 640: 37.2 and 35.9).
+      // Smaller tiles are never more than a round.
+      if constexpr (F == 16) {
+        const uint32_t groups = gridDim.x * gridDim.y;
+        if (a.experts <= kWave && a.T >= (uint64_t)kT * a.experts && groups > 256 && groups < 2048) of = by_size(x, of);
+      }
+      t0 = uniform64(x.start(of));
+      t1 = uniform64(x.start(of + 1));
     } else {
       const UnitSearch<true> search(x);
       if (blockIdx.y >= search.total) return;
@@ -303,7 +314,7 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
       if (in_y) py += a.T * a.dy_pitch * sizeof(TY);
     }
   } while (PARTED && ++p < parts);
-  TO *dw = static_cast<TO *>(dst) + (uint64_t)blockIdx.y * a.N * a.K;
+  TO *dw = static_cast<TO *>(dst) + (uint64_t)of * a.N * a.K;
   if constexpr (F == 16) {
     constexpr int kAt = sizeof(TO) == 2 ? 2 : 1;
     static_assert(kWaves * out_bytes<TO, FI, kAt>() <= sizeof(ring), "");

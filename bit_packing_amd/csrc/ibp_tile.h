@@ -210,6 +210,27 @@ template <bool EMPTY> struct UnitSearch {
   }
 };
 
+// The expert that comes `place`th by its rows, the most first, of up to a wavefront's lanes of
+// experts with less than 2^32 rows: of the sizes' bits from the highest on, those with the bit
+// come before those without.
+__device__ __forceinline__ uint32_t by_size(const Experts &x, uint32_t place) {
+  const uint32_t e = lane_id();
+  uint32_t size = 0;
+  if (e < x.n) {
+    const uint64_t b = x.start(e), end = x.start(e + 1);
+    size = end > b ? (uint32_t)(end - b) : 0u;
+  }
+  uint64_t left = ~0ull >> (kWave - x.n);
+  for (uint32_t bits = 64 - (uint32_t)__builtin_clzll(x.rows | 1); bits > 0; --bits) {
+    const uint64_t more = ballot(size >> (bits - 1) & 1) & left;
+    const uint32_t n = popc(more);
+    const bool among = place < n;
+    left = among ? more : left & ~more;
+    place -= among ? 0u : n;
+  }
+  return (uint32_t)__builtin_ctzll(ballot((left >> e & 1) && count_below(left) == place));
+}
+
 // Offsets that fall or leave the rows, seen by the calling wavefront's lanes together.
 __device__ __forceinline__ void check_offsets(const Experts &x, uint32_t *err) {
   bool bad = false;

@@ -469,7 +469,8 @@ def test_grouped_tokens_past_32_bit_offsets(ibp):
 WGRADS = [(1, 1, 1, 1, "even"), (31, 3, 16, 32, "ragged"), (32, 4, 33, 31, "one"), (33, 40, 128, 129, "ragged"), (100, 6, 130, 257, "ragged"),
           (999, 2, 50, 100, "even"), (3000, 9, 40, 64, "ragged"), (700, 3, 300, 520, "ragged"), (5000, 1, 129, 64, "even"),
           (64, 1024, 8, 40, "ragged"), (64, 5, 512, 512, "ragged"), (130, 33, 504, 600, "ragged"), (2100, 30, 520, 500, "one"),
-          (6000, 4, 256, 264, "ragged")]
+          (6000, 4, 256, 264, "ragged"), (2500, 45, 500, 600, "ragged"), (3000, 64, 264, 520, "ragged"), (2000, 50, 264, 513, "one"),
+          (2100, 64, 300, 300, "even")]
 
 
 @pytest.mark.parametrize("ty", ["bf16", "f32"])
