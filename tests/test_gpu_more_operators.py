@@ -733,3 +733,21 @@ def test_device_refusals(ibp):
         ibp.ibp_mx_grouped_matmul(a, a, torch.tensor([0, 1, 4], device="cuda"))  # weights in 8 bits
     with pytest.raises(ibp.IBPError):
         ibp.ibp_mx_grouped_wgrad(cuda, w, torch.tensor([0, 1, 4], device="cuda"))  # a checkpoint in 4 bits
+
+
+def test_ranges_that_leave_an_allocation_are_refused(ibp):
+    """Also where another tensor of the call, seen before, lies inside the same one."""
+    import ctypes
+
+    x = torch.ones(4, 64, device="cuda")
+    (begin, end), = [(s["address"], s["address"] + s["total_size"]) for s in torch.cuda.memory_snapshot()
+                     if s["address"] <= x.data_ptr() < s["address"] + s["total_size"]]
+    p = ibp.ibp_i8_pack(x)
+    lib, stream = ibp.load_library(), torch.cuda.current_stream().cuda_stream
+    for codes, scales in ((end - 128, p.scales.data_ptr()), (p.codes.data_ptr(), end - 8), (begin - 128, p.scales.data_ptr())):
+        t = ibp.ibp_i8_t(4, 64, codes, scales)
+        assert lib.ibp_i8_pack(x.data_ptr(), 0, ctypes.byref(t), stream) == ibp.IBP_ERR_INVALID_ARG
+    t = ibp.ibp_i8_t(4, 64, p.codes.data_ptr(), p.scales.data_ptr())
+    assert lib.ibp_i8_unpack(ctypes.byref(t), end - 64, 0, stream) == ibp.IBP_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert torch.equal(ibp.ibp_i8_unpack(p, torch.float32), x)
