@@ -127,8 +127,8 @@ __global__ __launch_bounds__(THREADS) void i8_pack_kernel(I8Args a, uint32_t lan
   });
 }
 
-// A code times its row's scale, rounded to 32 bits and then to T: two roundings, as the float
-// products of most users would have.
+// A code times its row's scale, rounded to 32 bits and then to T, as a float product and a
+// conversion are.
 template <int D> __global__ __launch_bounds__(kBlock) void i8_unpack_kernel(I8Args a, uint32_t lanes, uint32_t strips) {
   using T = typename Num<D>::T;
   const uint32_t tx = threadIdx.x & (lanes - 1), ty = threadIdx.x / lanes, rows_blk = kBlock / lanes;
@@ -141,12 +141,14 @@ template <int D> __global__ __launch_bounds__(kBlock) void i8_unpack_kernel(I8Ar
     if (row >= a.rows || c >= a.cols) continue;
     const uint2 q = *reinterpret_cast<const uint2 *>(a.codes + row * cp + c);
     const float s = a.scales[row];
-    F8 v;
+    auto four = [s](uint32_t q) {
+      v4f v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v.v[i] = (float)(int8_t)(q.x >> (8 * i)) * s;
-      v.v[4 + i] = (float)(int8_t)(q.y >> (8 * i)) * s;
-    }
+      for (int i = 0; i < 4; ++i) v[i] = (float)(int8_t)(q >> (8 * i)) * s;
+      return as_floats(v);
+    };
+    const v4f lo = four(q.x), hi = four(q.y);
+    const F8 v{{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}};
     store8<T>(out + row * a.cols, c, a.cols, v);
   }
 }

@@ -22,14 +22,15 @@ __device__ __forceinline__ v4i mfma(v4i w, v4i x, v4i acc) { return __builtin_am
 __device__ __forceinline__ v4i as_int(uint4 v) { return v4i{(int)v.x, (int)v.y, (int)v.z, (int)v.w}; }
 
 // A sum times its scales, the smaller first: no product on the way is beyond the floats
-// where the result is not.
+// where the result is not.  Each step is rounded to 32 bits, and then the result to y's type, in
+// every kernel here alike.
 __device__ __forceinline__ float scaled(int sum, float sa, float sb) {
   const bool a_less = fabsf(sa) < fabsf(sb);
   return (float)sum * (a_less ? sa : sb) * (a_less ? sb : sa);
 }
 
 __device__ __forceinline__ v4f scaled4(v4i sum, float sa, v4f sb) {
-  return v4f{scaled(sum[0], sa, sb[0]), scaled(sum[1], sa, sb[1]), scaled(sum[2], sa, sb[2]), scaled(sum[3], sa, sb[3])};
+  return as_floats(v4f{scaled(sum[0], sa, sb[0]), scaled(sum[1], sa, sb[1]), scaled(sum[2], sa, sb[2]), scaled(sum[3], sa, sb[3])});
 }
 
 // Few rows of A.  A workgroup computes 16 x 16 outputs, its wavefronts take steps of 256 codes

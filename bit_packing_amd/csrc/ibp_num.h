@@ -128,6 +128,14 @@ __device__ __forceinline__ v4f load4(const float *row, uint64_t n, uint64_t N) {
   return v;
 }
 
+// Four products as floats.  The empty statement keeps the compiler from making one instruction
+// with one rounding of a product and its conversion to half precision, which it does for some
+// of a kernel's stores and not for others (a pragma against contraction does not).
+__device__ __forceinline__ v4f as_floats(v4f products) {
+  asm("" : "+v"(products));
+  return products;
+}
+
 // ------------------------------------------------------------------ microscaled blocks
 
 constexpr int kMxMinExp = -117;  // smallest scale exponent: the smallest non-zero e4m3 value is then 2^-126, normal

@@ -342,8 +342,9 @@ IBP_API int ibp_zip_decompress(const uint8_t *table, const uint8_t *d_sm, const 
  * checkpoints in 8 bits with their use in the backward pass, and 4-bit weights with
  * their product.  Matrices are row-major and contiguous; element alignment is enough
  * for plain tensors, packed ones are aligned to 16.  Sums are held in 32 bits and
- * each result is rounded once (to nearest, ties to even).  Results do not depend on
- * timing.  Sizes of zero are allowed and write what there is to write.
+ * each result is rounded once (to nearest, ties to even) where nothing else is said.
+ * Results do not depend on timing.  Sizes of zero are allowed and write what there is to
+ * write.
  */
 
 /* Element types of plain tensors. */
@@ -458,9 +459,10 @@ IBP_API int ibp_mx_linear_wgrad(const void *d_dy, int dy_dtype, uint64_t outs, c
  * 8-bit integer rows.  A row of cols elements with the largest magnitude m has the scale
  * m / 127, rounded to 32 bits (down where 127 times it would be infinite), and the codes
  * 127 x / m rounded to the nearest whole number, ties to even (the quotient itself is
- * rounded, whatever the element type); an element reads back as its code times the scale.  A
- * row of zeros has the scale 0; a row that holds an infinity or a NaN has codes 0 and a NaN
- * scale, and reads back as NaN throughout.
+ * rounded, whatever the element type); an element reads back as its code times the scale,
+ * rounded to 32 bits and then to the output's type.  A row of zeros has the scale 0; a row
+ * that holds an infinity or a NaN has codes 0 and a NaN scale, and reads back as NaN
+ * throughout.
  *   codes:  rows x ibp_i8_codes_pitch(cols) bytes, cols filled up with zeros to a multiple
  *           of 16; aligned to 16.
  *   scales: rows floats.
@@ -488,8 +490,9 @@ IBP_API int ibp_i8_unpack(const ibp_i8_t *in, void *d_out, int dtype, void *hip_
  * d_y[i][j] = a.scale[i] * b.scale[j] * sum over k of a.code[i][k] * b.code[j][k], a of M
  * rows, b of N rows, a->cols == b->cols <= IBP_I8_MAX_DEPTH, d_y M x N of dtype.  The sum is
  * exact (of whole numbers in 32 bits, which hold that many products of any codes), then
- * rounded to a float and multiplied by the smaller scale and the larger one, so that it
- * overflows only where the result does.  d_y may not overlap an input.  d_workspace may be
+ * rounded to a float and multiplied by the smaller scale and the larger one, each product
+ * rounded to a float and the last one then to dtype, so that it overflows only where the
+ * result does.  d_y may not overlap an input.  d_workspace may be
  * NULL when the query says 0; aligned to 16.  Asynchronous.
  */
 #define IBP_I8_MAX_DEPTH 131071u
