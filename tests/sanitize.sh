@@ -16,4 +16,4 @@ IBP_SANITIZE_ORACLE=1 ASAN_OPTIONS=detect_leaks=0 \
 python -c "from bit_packing_amd.build import build_library; build_library(sanitize=True)"
 RT=$(ls /opt/rocm/llvm/lib/clang/*/lib/linux/libclang_rt.asan-x86_64.so | head -1)
 IBP_SANITIZE_LIB=1 ASAN_OPTIONS=detect_leaks=0 LD_PRELOAD="$RT" \
-  python -m pytest -q -p no:cacheprovider -m "not gpu" tests/test_abi.py tests/test_more_operators_host.py
+  python -m pytest -q -p no:cacheprovider -m "not gpu" tests/test_abi.py tests/test_more_operators_host.py tests/test_more_operators_limits.py

@@ -267,3 +267,16 @@ def test_large_gradients_of_any_values(ibp, ty, t, e, n, k):
         got = host(ibp.ibp_mx_grouped_wgrad(dy, mx(ibp, *x, k, mx_ref.E4M3), torch.from_numpy(off).cuda(), dw_dtype=DT[to]))
         over = np.abs(got - want) - (np.abs(want) * half(to) + mag * terms * U + TINY[to])
         assert over.max() <= 0
+
+
+@pytest.mark.parametrize("m,n", [(2050, 2050), (4400, 4300)])
+def test_i8_matmul_of_the_largest_sums_in_larger_tiles(ibp, m, n):
+    """The deepest product of the largest codes, in 128 x 128 and in 256 x 256 tiles."""
+    k = ibp.IBP_I8_MAX_DEPTH
+    a, b = (torch.zeros(r, i8_ref.pitch(k), dtype=torch.int8, device="cuda") for r in (m, n))
+    a[:, :k], b[:, :k] = -128, -128
+    b[n // 2:, :k] = 127
+    one = lambda r: torch.ones(r, device="cuda")  # noqa: E731
+    print(f"product of 8-bit integers: m={m} n={n} k={k}", flush=True)
+    y = ibp.ibp_i8_matmul(ibp.I8Tensor(a, one(m), m, k), ibp.I8Tensor(b, one(n), n, k), dtype=torch.float32)
+    assert (y[:, : n // 2] == float(np.float32(k * 16384))).all() and (y[:, n // 2:] == float(np.float32(-k * 128 * 127))).all()
