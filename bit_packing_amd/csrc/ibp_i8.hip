@@ -1,8 +1,8 @@
 // ibp_i8.hip -- 8-bit integer rows with a scale each: codes 127 x / m, m the row's largest
 // magnitude, rounded to the nearest whole number, and reading them back.
 //
-// Both are one pass over the data, bound by HBM: 16384 x 8192 in bf16 is packed in 74 us (5.5
-// TB/s; a copy of 1 GiB reaches 5.2) and read back in 75.  A row belongs to a power of two of
+// Both are one pass over the data, bound by HBM: 16384 x 8192 in bf16 is packed in 81 us (5.0
+// TB/s; a copy of 1 GiB reaches 5.0) and read back in 75.  A row belongs to a power of two of
 // lanes, 16 to 256 or 1024, each with eight elements of every strip of 8 * lanes columns; a lane
 // keeps what it has of a few strips in registers between the search for m and the rounding,
 // longer rows are read twice.
@@ -168,8 +168,10 @@ uint32_t grid_of(uint64_t units) { return (uint32_t)(units < (1u << 20) ? units 
 hipError_t launch_i8_pack(const I8Args &a, hipStream_t s) {
   return with_dtype(a.dtype, [&](auto d) {
     // Rows of more strips than registers hold well take a workgroup of sixteen wavefronts (4096 x
-    // 16384: single precision 98 us with 256 lanes and eight strips, 75 with 1024 and two; bf16 40
-    // and 48; 2048 x 32768 in bf16 43 with 1024 and four).
+    // 16384: single precision 98 us with 256 lanes and eight strips, 75 with 1024 and two; bf16 42
+    // and 60; 8192 x 8192 in single precision 67 with 256 and four, 99 with 1024 and one; 2048 x
+    // 32768 in bf16 43 with 1024 and four).  A few rows would be quicker with them sooner (64 x
+    // 16384 in bf16 5.3 and 4.7).
     constexpr bool kSingle = d.value == IBP_F32;
     constexpr uint32_t kLong = 1024, kStrips = kSingle ? 4 : 8, kLongStrips = kSingle ? 2 : 4;
     uint32_t lanes, strips, threads = kBlock;

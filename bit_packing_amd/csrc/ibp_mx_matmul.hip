@@ -32,7 +32,7 @@ constexpr uint32_t kStep = 16;  // blocks per step of the direct kernel: 512 ele
 // more, whose codes have bit 6, go through one instruction (2^10 down to 2^-3) and the rest
 // through another (4 down to 2^-10): nothing is dropped.  In one instruction a block whose
 // large products cancel, as those of an outlier column may, would lose its result: 8192 x
-// 8192 x 8192 would take 370 us so, against 590.
+// 8192 x 8192 would take 370 us so, against 600.
 //
 // split takes the large elements' bytes out of four.
 __device__ __forceinline__ int split(int &x) {
@@ -311,7 +311,7 @@ __global__ __launch_bounds__(WM *WN *64) void mx_tile_kernel(MxMatmulArgs a, voi
     if constexpr (A8) {
       // A fragment's successor is split between its matrix instructions, four bytes at a time,
       // which they hide: split all at once, before them, the matrix units would wait meanwhile
-      // (8192 x 8192 x 8192: 740 us, and 727 with few fragments a wavefront, against 590).
+      // (8192 x 8192 x 8192: 740 us, and 727 with few fragments a wavefront, against 600).
       v8i high, next;
       constexpr int kEach = 2 * FN / 8;  // matrix instructions for four bytes
 #pragma unroll
@@ -444,7 +444,10 @@ template <bool A8> hipError_t go(const MxMatmulArgs &a, hipStream_t s) {
 // Operands come as in the larger tiles, in a ring of three stages of 128 elements; one barrier a
 // stage, at which its loads are done and all have read the stage before, whose place is
 // filled anew.  Three workgroups a CU overlap their loads and products (with five stages two
-// fit: 64 rows of 64 experts, 2048 x 4096, e4m3 36.2 us against 33.4, 4.4 TB/s of weights).
+// fit: 64 rows of 64 experts, 2048 x 4096, e4m3 36.2 us against 33.4, 4.4 TB/s of weights; 1501 of
+// 24, 1000 x 1503, one or two workgroups a CU, e2m1 9.3 and 9.1, e4m3 15.4 and 14.6).  Of 64 rows
+// of e4m3 all four wavefronts split the same codes, ten vector instructions to a matrix one (2048
+// rows of 32 ragged experts, 2048 x 4096: 62 us, e2m1, which has nothing to split, 39).
 template <bool A8, int FM, int FN, int DO>
 __global__ __launch_bounds__(256) void mx_rows_kernel(MxMatmulArgs a, uint32_t tiles_n) {
   using TO = typename Num<DO>::T;

@@ -90,7 +90,7 @@ template <typename TY> __device__ __forceinline__ v8b part_of(Vec8<TY> y, uint32
 // has laid them out so; part p is then T rows further on), else through registers like
 // X, which is loaded four stages ahead and decoded into LDS two stages ahead.  As in the
 // 4-bit product, half of the eight wavefronts of a large tile read a stage while the other
-// half multiplies (16384 x 4096 x 8192: 859 us, 1.28 PFLOP/s, against 1090 with all in
+// half multiplies (16384 x 4096 x 8192: 874 us, 1.26 PFLOP/s, against 1090 with all in
 // step and two stages of 64 tokens).  Bound by the phases (the matrix units are busy 57% of the
 // time, LDS 28%) and by power: the clock falls to 1.9 to 2.1 GHz.
 //
@@ -126,9 +126,11 @@ __global__ __launch_bounds__(WI *WO *64) void wgrad_kernel(MxWgradArgs a, void *
       // In a few rounds of workgroups the experts of many tokens go first, so that the last round
       // is short (60 experts of 400 x 600, 20000 tokens, 360 workgroups: 41.6 us, 55.6 in their
       // order; 1500 x 1000, 1440: 120, 135; 32 of 1024 x 2048, 1024: 164, 181; 60 of 128 x 1600,
-      // 3000 tokens, 420: 17.6, 19.6).  In many rounds the search costs more than that (32 of 2048 x
-      // 4096, 8192 tokens, 4096 workgroups 221 and 214; 16, 8000 tokens, 2048: 161 and 158), and
-      // where experts have a stage or less (40 of 1000 x 1000, 500 tokens, 640: 37.2 and 35.9).
+      // 3000 tokens, 420: 17.6, 19.6; with other routes, whose long experts do not come late by
+      // themselves, the first of these takes 42.7 and 42.1).  In many rounds the search costs more than
+      // that (32 of 2048 x 4096, 4096 workgroups: 8192 tokens 221 and 214, 32768 tokens 542 and 534;
+      // 16, 8000 tokens, 2048: 161 and 158), and where experts have a stage or less (40 of 1000 x
+      // 1000, 500 tokens, 640: 37.2 and 35.9).
       // Smaller tiles are never more than a round.
       if constexpr (F == 16) {
         const uint32_t groups = gridDim.x * gridDim.y;
@@ -473,13 +475,16 @@ struct GroupedPlan {
 };
 
 // Tiles by their number, as without experts (256 x 256 against 128 x 128; 32 ragged experts, 2048
-// x 4096: 32768 tokens 606 us and 877; 24 of 500 x 1000 (192 large tiles), 1501 tokens 19.1 and
-// 22.9; 8 of 1024 x 1024 (128), 16384 tokens 134 and 71, 4000 tokens 25.7 and 22.2).
+// x 4096: 32768 tokens 534 us and 815; 24 of 500 x 1000 (192 large tiles), 1501 tokens 17.6 and
+// 21.4; 8 of 1024 x 1024 (128), 16384 tokens 134 and 71, 4000 tokens 25.7 and 22.2).
 // Where there are fewer small tiles than CUs, an expert's tokens are cut into units whose sums
 // another launch adds, as long as leave a tile for each CU, from 512 tokens to 8192 (8 experts
 // of 512 x 512, 16384 tokens: whole 61 us, units of 2048 tokens 43.5, 1024 36.7, 512 38.3; 4 of 256
 // x 512, 32768 tokens: 179, 1024 37.0, 512 44.9; 16 of 256 x 300, 30000 tokens: 75, 1024 29.1,
-// 512 28.4; 8 of 256 x 256, 2000 tokens: 13.4, 256 13.9).
+// 512 28.4; 8 of 256 x 256, 2000 tokens: 13.4, 256 13.9).  The host knows the experts' average
+// alone: where that does not fill a unit, or tiles are many, an expert's tokens are one loop of a
+// workgroup a tile, as long as they are many (32768 tokens of 64 experts, 300 x 300: evenly spread
+// 34 us, by p ~ rank^-1/2 69, by p ~ 1 / rank 167, all of one expert 722).
 GroupedPlan grouped_plan(uint64_t T, uint32_t experts, uint32_t N, uint32_t K, int dy_dtype, bool aligned) {
   GroupedPlan p;
   p.parts = dy_dtype == IBP_BF16 ? 1 : dy_dtype == IBP_F16 ? 2 : 3;

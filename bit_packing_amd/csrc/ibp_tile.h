@@ -94,8 +94,12 @@ __device__ __forceinline__ void phase_barrier() {
 // 2^30).  They go through LDS (`out`, the wavefront's own), AT fragments' rows at a time, so that
 // a store covers whole lines of y (from the fragments themselves a row gets 32 bytes at a time).
 // STREAM: past the caches, which large results would empty of operands (the weight gradients of 32
-// experts, 2048 x 4096, 537 MB: of 32768 tokens 642 us without, 606 with; of 8192 304 and 245;
-// the product of 32768 rows, 134 MB, 403 and 394; that of 8-bit integers, 134 MB, 235 and 239).
+// experts, 2048 x 4096, 537 MB: of 32768 tokens 563 us without, 533 with; of 8192 254 and 214;
+// the product of 32768 rows, 134 MB, and the packing that reads it 430 and 422; that of 8-bit
+// integers, 134 MB, 235 and 239).  Small results gain too, also where the next operator reads them
+// at once (product and packing of 4096 rows of 8 experts, 1024 x 1024, 8 MB: e4m3 24.4 and 22.7,
+// e2m1 17.0 and 15.5), but not the gradients of few tokens (2500 of 45 experts, 500 x 600, 27 MB:
+// 24.4 and 25.2; 54 MB: 27.4 and 30.7).
 template <typename TO, int FN, int AT = 2> constexpr uint32_t out_bytes() { return AT * 16 * (16 * FN * sizeof(TO) + 16); }
 template <typename TO, int FM, int FN, int AT = 2, bool STREAM = false, typename F>
 __device__ __forceinline__ void store_fragments(TO *out, TO *y, uint32_t row0, uint32_t rows, uint32_t col0,
